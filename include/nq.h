@@ -71,6 +71,8 @@ typedef enum {
 #define NQ_DEV_TIMEOUT   0x4u
 #define NQ_DEV_ACT_RANGE 0x8u   /* an activation exceeded the fp16 range (|x| > 65504) */
 #define NQ_DEV_SEQ_FULL  0x10u  /* spec_round_commit: a sequence buffer was full, tokens dropped */
+#define NQ_DEV_BAD_PAGE  0x20u  /* a page id, sequence slot or row outside the map or the pool */
+#define NQ_DEV_POOL_FULL 0x40u  /* nq_page_reserve: too few free pages for a request */
 
 /*
  * Weight formats (SpecQuant Sec. III.A tiers; BitNest Fig. 3 planes).
@@ -374,6 +376,209 @@ NQ_API nq_status nq_kv_append(const nq_kv_cache *cache, const float *k_new, cons
 NQ_API size_t nq_attn_workspace_bytes(int batch, int M, int heads_q, int head_dim, int max_len);
 NQ_API nq_status nq_attn_decode(const nq_kv_cache *cache, const float *q, int M, int heads_q, const int32_t *len,
                                 int planes, float scale, float *out, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------- rotary positions
+ * A rotation turns the pairs of a head's first rot_dim values by angles that
+ * grow with the token's position:
+ *   y1 = mscale (x1 cos a - x2 sin a),  y2 = mscale (x1 sin a + x2 cos a),  a = pos * w_i,
+ * pair i = (x[i], x[i + rot_dim/2]) (NQ_ROPE_HALF) or (x[2i], x[2i+1])
+ * (NQ_ROPE_INTERLEAVED); values at and past rot_dim are kept.  w_i is given as
+ * a rate in turns per position in 64-bit fixed point, rates[i] =
+ * round(w_i / (2 pi) * 2^64): the kernels take frac(pos * rate) in integers, so
+ * that the angle of a far position is as exact as that of a near one.
+ *
+ * nq_rope_rates: the rot_dim/2 rates into HOST memory (no CUDA), and *mscale.
+ *   NONE    w_i = theta^(-2i/rot_dim)
+ *   LINEAR  w_i / factor (positions interpolated)
+ *   NTK     theta replaced by theta factor^(rot_dim/(rot_dim-2))
+ *   PARTS   by the turns t = old_len w_i / (2 pi) that a pair makes over the
+ *           trained length: w_i for t >= 32, w_i / factor for t <= 1, linear in
+ *           t between; mscale = 0.1 ln(factor) + 1
+ *   (mscale = 1 otherwise.)  rot_dim a multiple of 8 up to 128 (NTK: at least 8);
+ *   theta > 1, factor >= 1 for any scaling, old_len >= 1 for PARTS.
+ */
+typedef enum { NQ_ROPE_HALF = 0, NQ_ROPE_INTERLEAVED = 1 } nq_rope_layout;
+typedef enum { NQ_ROPE_NONE = 0, NQ_ROPE_LINEAR = 1, NQ_ROPE_NTK = 2, NQ_ROPE_PARTS = 3 } nq_rope_scaling;
+
+/* Host struct; rates: uint64 [rot_dim/2] on the device, caller-owned. */
+typedef struct {
+    int32_t rot_dim;
+    int32_t layout;   /* nq_rope_layout */
+    float mscale;
+    int32_t pad;
+    const uint64_t *rates;
+} nq_rope_plan;
+
+/* Element types of the calls that take either. */
+typedef enum { NQ_F32 = 0, NQ_BF16 = 1 } nq_dtype;
+
+NQ_API nq_status nq_rope_rates(int rot_dim, double theta, int scaling, double factor, int old_len, uint64_t *rates,
+                               float *mscale);
+
+/*
+ * Rotate x [T][heads][head_dim] by pos int32 [T] (device, >= 0) into out of the
+ * same shape; x and out each fp32 or bf16 (nq_dtype), rounded once.  Rows of a
+ * token are contiguous, x_stride / out_stride elements lie between tokens
+ * (multiples of 8, at least heads * head_dim): the heads of a fused linear's
+ * output are rotated where they lie.  head_dim 64 or 128, rot_dim <= head_dim.
+ * out may be x itself (same type and stride).  inverse != 0 turns by -a: the
+ * gradient of the rotation (mscale kept).
+ */
+NQ_API nq_status nq_rope(const nq_rope_plan *rope, const void *x, int x_dtype, int64_t x_stride, const int32_t *pos,
+                         int T, int heads, int head_dim, int inverse, void *out, int out_dtype, int64_t out_stride,
+                         cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------- the paged KV cache
+ * A pool holds the K and V rows of many sequences in pages of page_size rows;
+ * the pages of a sequence may lie anywhere and may be shared.  One page id
+ * stands for the same page in every layer.  data: uint8
+ * [layers][n_pages][heads_kv][record], device, 16-byte aligned,
+ * nq_page_pool_bytes() bytes.  page_size 16, 32, 64, 128 or 256, head_dim 64 or
+ * 128.  A record holds page_size rows of one kv head so that one contiguous
+ * copy brings what a pass reads:
+ *   NESTED44: page_size/16 base blocks, then page_size/16 refinement blocks.
+ *     base block:  16 K rows of base nibbles (head_dim/2 bytes each), 16 V
+ *       rows, fp16 K scales [16][head_dim/group], fp16 V scales;
+ *     refinement block: 16 K rows of refinement nibbles, 16 V rows.
+ *     Codes and scales as in nq_kv_append, each nibble stored offset by 8
+ *     (0..15), element 2j in the low nibble of byte j.  In 16 rows, 16-byte
+ *     chunk q (counted over rows) lies at line l = q / 8, slot (q % 8) xor
+ *     2 (l % 4): the fragment reads of the attention are then free of bank
+ *     conflicts with the block copied as it lies.
+ *   BF16: page_size/16 blocks of 16 K rows, 16 V rows; 8-element chunk c of
+ *     row r lies at chunk c xor (r % 8) of its row.  group is ignored.
+ */
+typedef enum { NQ_KV_NESTED44 = 0, NQ_KV_BF16 = 1 } nq_kv_format;
+
+typedef struct {
+    int32_t layers, n_pages, page_size, heads_kv, head_dim, group, format, pad;
+    void *data;
+} nq_page_pool;
+
+/*
+ * Which pages the sequences hold.  table int32 [max_seqs][max_pages]: page ids
+ * of slot s in order, -1 past held[s]; held int32 [max_seqs]; ref int32
+ * [n_pages]: how many table entries name a page, 0 = free.  All device memory,
+ * caller-owned, set up by nq_page_map_init and changed by the calls below.
+ * Free pages are taken lowest id first, so the same calls give the same ids.
+ * The calls below are asynchronous and ordered by the stream; calls on one map
+ * must not overlap on the GPU.
+ */
+typedef struct {
+    int32_t max_seqs, max_pages, n_pages, page_size;
+    int32_t *table, *held, *ref;
+} nq_page_map;
+
+NQ_API nq_status nq_page_pool_bytes(int layers, int n_pages, int page_size, int heads_kv, int head_dim, int group,
+                                    int format, size_t *bytes);
+NQ_API nq_status nq_page_map_init(const nq_page_map *map, cudaStream_t stream);
+
+/* Bytes of the device workspace of the next calls for up to n sequences (host-only; no initialisation). */
+NQ_API size_t nq_page_workspace_bytes(const nq_page_map *map, int n);
+
+/*
+ * Before rows first[i] .. last[i]-1 of slot seqs[i] are written: take pages so
+ * that the slot holds ceil(last/page_size) of them, and give it a page of its
+ * own wherever one of those rows lies on a page it shares (copy on write: the
+ * page's other rows are copied in every layer of pool; pool NULL skips the
+ * copies).  Where all holders of a shared page ask in one call, the last of
+ * them in order keeps it.  Requests are served in order; one that the free
+ * pages do not cover, and all after it, change nothing and set
+ * NQ_DEV_POOL_FULL; one with last past max_pages * page_size is left out and
+ * sets NQ_DEV_SEQ_FULL; a slot outside the map or first < 0 is left out and
+ * sets NQ_DEV_BAD_PAGE.  granted (may be NULL): int32 [n], 1 where served.
+ * The slots of one call are distinct.  1 <= n <= max_seqs.
+ */
+NQ_API nq_status nq_page_reserve(const nq_page_map *map, const nq_page_pool *pool, const int32_t *seqs,
+                                 const int32_t *first, const int32_t *last, int n, int32_t *granted, void *ws,
+                                 size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Slot dst[i] becomes a copy of slot src[i]'s first rows[i] rows, sharing their
+ * pages; what dst held is released.  All at once: every src is read as it was
+ * before the call, so that a beam search reorders its states in one call
+ * (sources may repeat and may be destinations; the dst are distinct).  More
+ * rows than src holds, or a slot outside the map, set NQ_DEV_BAD_PAGE (rows are
+ * clamped; that pair is left out).
+ */
+NQ_API nq_status nq_page_fork(const nq_page_map *map, const int32_t *src, const int32_t *dst, const int32_t *rows,
+                              int n, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Slot seqs[i] keeps the pages of its first rows[i] rows and releases the others (rows = 0: all of them). */
+NQ_API nq_status nq_page_truncate(const nq_page_map *map, const int32_t *seqs, const int32_t *rows, int n,
+                                  cudaStream_t stream);
+
+/*
+ * Move the pages in use to the ids 0 .. used-1: the i-th page in use at or past
+ * `used` goes to the i-th free id below it, in every layer; table and ref
+ * follow.  used: int32 [1] device.
+ */
+NQ_API nq_status nq_page_compact(const nq_page_map *map, const nq_page_pool *pool, int32_t *used, void *ws,
+                                 size_t ws_bytes, cudaStream_t stream);
+
+/* Copy pages src[i] to dst[i] in every layer (device int32 [n]); a dst is no
+ * other pair's src or dst.  Ids outside the pool set NQ_DEV_BAD_PAGE. */
+NQ_API nq_status nq_page_copy(const nq_page_pool *pool, const int32_t *src, const int32_t *dst, int n,
+                              cudaStream_t stream);
+
+/*
+ * Store T tokens' K and V rows in layer `layer`: token t is row pos[t] of slot
+ * seqs[t] (int32 [T], device).  k, v: [T][heads_kv][head_dim], q:
+ * [T][heads_q][head_dim] (NULL: none), all of one type dtype with `stride`
+ * elements between tokens (a multiple of 8): pointers into the output of one
+ * fused q|k|v linear.  With rope (NULL: none) k and q are rotated by pos before
+ * they are rounded.  q_out: bf16 [T][heads_q][head_dim].  NESTED44 rows are
+ * quantised like nq_kv_append's.  A row past max_pages * page_size sets
+ * NQ_DEV_SEQ_FULL, a slot or page outside the map NQ_DEV_BAD_PAGE; that row is
+ * dropped.  A non-finite NESTED44 row sets NQ_DEV_NONFINITE (its value is then
+ * unspecified).  No two tokens of a call name the same row.
+ */
+NQ_API nq_status nq_page_append(const nq_page_pool *pool, int layer, const nq_page_map *map, const nq_rope_plan *rope,
+                                const void *q, const void *k, const void *v, int dtype, int64_t stride,
+                                const int32_t *seqs, const int32_t *pos, int T, int heads_q, uint16_t *q_out,
+                                cudaStream_t stream);
+
+/*
+ * The stored values of rows pos[t] of slots seqs[t]: k_out, v_out bf16
+ * [T][heads_kv][head_dim].  NESTED44: planes = 1 the 4-bit view, 2 the 8-bit
+ * view; BF16 ignores planes.  A row that nq_page_append would drop reads as
+ * zeros and is reported alike.
+ */
+NQ_API nq_status nq_page_read(const nq_page_pool *pool, int layer, const nq_page_map *map, const int32_t *seqs,
+                              const int32_t *pos, int T, int planes, uint16_t *k_out, uint16_t *v_out,
+                              cudaStream_t stream);
+
+/* What changes the scores of nq_page_attn (host struct). */
+typedef struct {
+    float scale;            /* > 0 */
+    float softcap;          /* 0: none; else s -> softcap tanh(s / softcap) */
+    int32_t window;         /* 0: none; else a query sees its own row and the window-1 before it */
+    int32_t pad;
+    const float *slopes;    /* NULL, or fp32 [heads_q] device: s -= slope (row of query - row of key) */
+} nq_attn_opts;
+
+/*
+ * Attention of the last M rows of `batch` sequences over their pages:
+ *   out[b][m][h][:] = sum_t softmax_t(f(scale q[b][m][h] . K[t])) V[t],
+ * t = 0 .. len[b]-M+m (causal; len[b] counts the M new rows, already appended),
+ * kv head h / (heads_q / heads_kv), f the options above (cap, then bias).
+ * Sequence b is slot seqs[b] (NULL: slot b); a slot may repeat.  q, out: bf16
+ * [batch][M][heads_q][head_dim], q with q_stride elements between the M rows
+ * (a multiple of 8).  A query that sees no row gives zeros (a length of 0, or
+ * less than M for the first queries).  Rows past len and pages wholly before
+ * the window are never used.  A length past max_pages * page_size is clamped
+ * and sets NQ_DEV_SEQ_FULL, a needed page outside the pool or a slot outside
+ * the map sets NQ_DEV_BAD_PAGE (that output is then unspecified).  planes as
+ * in nq_page_read.  Scores, sums and outputs are held in fp32; probabilities
+ * enter the second product as 16-bit values.
+ */
+NQ_API size_t nq_page_attn_workspace_bytes(int M, int heads_q, int heads_kv, int head_dim);
+NQ_API nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,
+                              int64_t q_stride, int batch, int M, int heads_q, const int32_t *seqs,
+                              const int32_t *len, int planes, const nq_attn_opts *opts, uint16_t *out, void *ws,
+                              size_t ws_bytes, cudaStream_t stream);
 
 /*
  * Greedy acceptance that allocates nothing and takes no workspace: the same

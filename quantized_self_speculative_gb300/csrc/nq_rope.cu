@@ -1,0 +1,501 @@
+// nq_rope.cu -- rotary positions, and storing / reading rows of the paged KV
+// cache (rotated, then quantised or rounded, in one pass over a fused linear's
+// output).
+//
+// A pair turns by a = pos * w.  The rate w / (2 pi) is a 64-bit fraction of a
+// turn, so frac(pos * rate) is one integer product: no precision is lost at
+// far positions, and no table of angles is read.  sin and cos are taken of the
+// fraction's top 32 bits, once per token and lane, and used for every head
+// that the warp handles.
+//
+// One warp takes one token and a run of heads, kBatch rows at a time: all their
+// loads are issued before the first row is turned.  Lane l holds elements
+// E l .. E l + E - 1 (E = D / 32) of a row, so an interleaved pair lies in one
+// lane and a half pair is one shuffle away.  HBM bound for prompts.
+#include <cmath>
+
+#include "nq_page.cuh"
+
+namespace nq {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kBatch = 4;
+
+struct Rope {
+    int rot, layout;
+    float mscale;
+    const unsigned long long *rates;
+};
+
+template <int E> struct Vec { float v[E]; };
+
+template <int E>
+__device__ __forceinline__ Vec<E> load_vec(const float *p)
+{
+    Vec<E> r;
+    if constexpr (E == 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(p);
+        r.v[0] = f.x; r.v[1] = f.y; r.v[2] = f.z; r.v[3] = f.w;
+    } else {
+        const float2 f = *reinterpret_cast<const float2 *>(p);
+        r.v[0] = f.x; r.v[1] = f.y;
+    }
+    return r;
+}
+__device__ __forceinline__ void bf_pair(uint32_t w, float &a, float &b)
+{
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xFFFF0000u);
+}
+template <int E>
+__device__ __forceinline__ Vec<E> load_vec(const __nv_bfloat16 *p)
+{
+    Vec<E> r;
+    if constexpr (E == 4) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        bf_pair(w.x, r.v[0], r.v[1]);
+        bf_pair(w.y, r.v[2], r.v[3]);
+    } else {
+        bf_pair(*reinterpret_cast<const uint32_t *>(p), r.v[0], r.v[1]);
+    }
+    return r;
+}
+__device__ __forceinline__ uint32_t bf_pack(float a, float b)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+template <int E>
+__device__ __forceinline__ void store_vec(float *p, const Vec<E> &x)
+{
+    if constexpr (E == 4) *reinterpret_cast<float4 *>(p) = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
+    else *reinterpret_cast<float2 *>(p) = make_float2(x.v[0], x.v[1]);
+}
+template <int E>
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const Vec<E> &x)
+{
+    if constexpr (E == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(bf_pack(x.v[0], x.v[1]), bf_pack(x.v[2], x.v[3]));
+    else *reinterpret_cast<uint32_t *>(p) = bf_pack(x.v[0], x.v[1]);
+}
+
+// This lane's part of a token's rotation: y[e] = c[e] x[e] + s[e] partner[e].
+template <int E>
+struct Turn {
+    float c[E], s[E];
+    int from;             // lane of the partner (HALF), own lane otherwise
+    bool half, any;
+};
+template <int E>
+__device__ __forceinline__ Turn<E> make_turn(const Rope &R, int pos, int lane, bool inverse)
+{
+    Turn<E> t;
+    t.half = R.layout == NQ_ROPE_HALF;
+    const int e0 = lane * E, hr = R.rot / 2;
+    t.any = e0 < R.rot;
+    t.from = lane;
+    if (t.half && t.any) t.from = e0 < hr ? lane + hr / E : lane - hr / E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        t.c[e] = 1.0f;
+        t.s[e] = 0.0f;
+    }
+    if (!t.any) return t;
+    const bool first = e0 < hr;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = t.half ? (first ? e0 + e : e0 + e - hr) : (e0 + e) / 2;
+        const unsigned long long x = static_cast<unsigned long long>(static_cast<long long>(pos)) * R.rates[i];
+        // half turns in [-1, 1)
+        const float h = __int2float_rn(static_cast<int>(x >> 32)) * 4.656612873077393e-10f;
+        float sn, cs;
+        sincospif(h, &sn, &cs);
+        if (inverse) sn = -sn;
+        const bool minus = t.half ? first : (e & 1) == 0;
+        t.c[e] = R.mscale * cs;
+        t.s[e] = R.mscale * (minus ? -sn : sn);
+    }
+    return t;
+}
+// Every lane of the warp takes part.
+template <int E>
+__device__ __forceinline__ Vec<E> turn(const Turn<E> &t, const Vec<E> &x)
+{
+    Vec<E> y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float p = t.half ? __shfl_sync(0xffffffffu, x.v[e], t.from) : x.v[e ^ 1];
+        y.v[e] = t.any ? fmaf(t.c[e], x.v[e], t.s[e] * p) : x.v[e];
+    }
+    return y;
+}
+
+// ---------------------------------------------------------------- rope
+template <int D, typename TI, typename TO>
+__global__ void __launch_bounds__(kWarps * 32)
+rope_kernel(Rope R, const TI *x, long long xs, const int32_t *__restrict__ pos, int T, int H, int per, int chunks,
+            bool inverse, TO *out, long long os)
+{
+    constexpr int E = D / 32;
+    const long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long t = w / chunks;
+    if (t >= T) return;
+    const int h0 = static_cast<int>(w % chunks) * per, h1 = min(h0 + per, H);
+    const TI *in = x + t * xs + lane * E;
+    TO *to = out + t * os + lane * E;
+    const Turn<E> tn = make_turn<E>(R, pos[t], lane, inverse);
+    for (int h = h0; h < h1; h += kBatch) {
+        Vec<E> v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (h + u < h1) v[u] = load_vec<E>(in + (h + u) * D);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (h + u < h1) store_vec<E>(to + (h + u) * D, turn<E>(tn, v[u]));
+    }
+}
+
+// ---------------------------------------------------------------- append
+struct Row {              // where a token's row lies
+    uint8_t *page;        // record of head 0
+    int r;                // row within the page
+    bool ok;
+};
+__device__ __forceinline__ Row row_of(const Pool &p, const Map &m, int s, int pos, unsigned int *status, bool report)
+{
+    Row w{nullptr, 0, false};
+    if (s < 0 || s >= m.S || pos < 0) {
+        if (report) set_status(status, NQ_DEV_BAD_PAGE);
+        return w;
+    }
+    const int j = pos / m.P;
+    if (j >= m.W) {
+        if (report) set_status(status, NQ_DEV_SEQ_FULL);
+        return w;
+    }
+    const int id = m.table[static_cast<size_t>(s) * m.W + j];
+    if (id < 0 || id >= p.N) {
+        if (report) set_status(status, NQ_DEV_BAD_PAGE);
+        return w;
+    }
+    w.page = p.data + static_cast<size_t>(id) * p.H * p.rec;
+    w.r = pos % m.P;
+    w.ok = true;
+    return w;
+}
+
+// One K (v = 0) or V (v = 1) row of head h, quantised in groups of D / NG.
+template <int D, int NG>
+__device__ __forceinline__ void store_nested(const Pool &p, const Row &w, int h, int v, const Vec<D / 32> &x, int lane,
+                                             unsigned int *status)
+{
+    constexpr int E = D / 32, RB = D / 2;
+    float amax = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        amax = fmaxf(amax, fabsf(x.v[e]));
+        bad |= !(fabsf(x.v[e]) <= 3.4028234663852886e38f);
+    }
+#pragma unroll
+    for (int o = 16 / NG; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const __half sh = __float2half_rn(__fdiv_rn(amax, 7.0f));
+    const float s = __half2float(sh);
+    if (bad || !(s <= 65504.0f)) set_status(status, NQ_DEV_NONFINITE);
+    uint32_t b = 0, r = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        int q4, rr;
+        nested_quantise(x.v[e], s, q4, rr);
+        b |= static_cast<uint32_t>(q4 + 8) << (4 * e);
+        r |= static_cast<uint32_t>(rr + 8) << (4 * e);
+    }
+    const int blk = w.r >> 4, r16 = w.r & 15;
+    uint8_t *rec = w.page + static_cast<size_t>(h) * p.rec;
+    uint8_t *base = rec + blk * p.base_block;
+    const uint32_t at = v * 16 * RB + nib_off(RB, r16, lane * E / 2);
+    uint8_t *resid = rec + p.resid_off + blk * (16 * D);
+    if constexpr (E == 4) {
+        *reinterpret_cast<uint16_t *>(base + at) = static_cast<uint16_t>(b);
+        *reinterpret_cast<uint16_t *>(resid + at) = static_cast<uint16_t>(r);
+    } else {
+        base[at] = static_cast<uint8_t>(b);
+        resid[at] = static_cast<uint8_t>(r);
+    }
+    if (lane % (32 / NG) == 0)
+        *reinterpret_cast<__half *>(base + 32 * RB + v * 32 * NG + (r16 * NG + lane / (32 / NG)) * 2) = sh;
+}
+template <int D>
+__device__ __forceinline__ void store_bf16(const Pool &p, const Row &w, int h, int v, const Vec<D / 32> &x, int lane)
+{
+    constexpr int E = D / 32;
+    uint8_t *rec = w.page + static_cast<size_t>(h) * p.rec + (w.r >> 4) * p.base_block;
+    store_vec<E>(reinterpret_cast<__nv_bfloat16 *>(rec) + v * 16 * D + bf_off(D, w.r & 15, lane * E), x);
+}
+
+// NG = 0: BF16.  Rows of a token in the order q heads, k heads, v heads.
+template <int D, int NG, typename TI>
+__global__ void __launch_bounds__(kWarps * 32)
+append_kernel(Pool p, Map m, Rope R, bool rope, const TI *__restrict__ q, const TI *__restrict__ k,
+              const TI *__restrict__ v, long long stride, const int32_t *__restrict__ seqs,
+              const int32_t *__restrict__ pos, int T, int Hq, int per, int chunks, __nv_bfloat16 *__restrict__ q_out,
+              unsigned int *status)
+{
+    constexpr int E = D / 32;
+    const long long wi = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long t = wi / chunks;
+    if (t >= T) return;
+    const int all = Hq + 2 * p.H, h0 = static_cast<int>(wi % chunks) * per, h1 = min(h0 + per, all);
+    const int ps = pos[t];
+    const Row w = row_of(p, m, seqs[t], ps, status, lane == 0 && h1 > Hq);
+    Turn<E> tn{};
+    if (rope && h0 < Hq + p.H) tn = make_turn<E>(R, ps, lane, false);
+    for (int h = h0; h < h1; h += kBatch) {
+        Vec<E> x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int a = h + u;
+            if (a >= h1) continue;
+            const TI *src = a < Hq ? q + a * D : a < Hq + p.H ? k + (a - Hq) * D : v + (a - Hq - p.H) * D;
+            x[u] = load_vec<E>(src + t * stride + lane * E);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int a = h + u;
+            if (a >= h1) continue;
+            if (rope && a < Hq + p.H) x[u] = turn<E>(tn, x[u]);
+            if (a < Hq) {
+                store_vec<E>(q_out + (t * Hq + a) * D + lane * E, x[u]);
+                continue;
+            }
+            if (!w.ok) continue;
+            const int kv = a >= Hq + p.H, head = a - Hq - kv * p.H;
+            if constexpr (NG == 0) store_bf16<D>(p, w, head, kv, x[u], lane);
+            else store_nested<D, NG>(p, w, head, kv, x[u], lane, status);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- read
+// One warp per (token, head): its K and its V row.
+template <int D, int NG>
+__global__ void __launch_bounds__(kWarps * 32)
+read_kernel(Pool p, Map m, const int32_t *__restrict__ seqs, const int32_t *__restrict__ pos, int T, int planes,
+            __nv_bfloat16 *__restrict__ k_out, __nv_bfloat16 *__restrict__ v_out, unsigned int *status)
+{
+    constexpr int E = D / 32, RB = D / 2;
+    const long long wi = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long t = wi / p.H;
+    if (t >= T) return;
+    const int h = static_cast<int>(wi % p.H);
+    const Row w = row_of(p, m, seqs[t], pos[t], status, lane == 0);
+    Vec<E> x[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[v].v[e] = 0.0f;
+        if (!w.ok) continue;
+        const int blk = w.r >> 4, r16 = w.r & 15;
+        const uint8_t *rec = w.page + static_cast<size_t>(h) * p.rec, *base = rec + blk * p.base_block;
+        if constexpr (NG == 0) {
+            x[v] = load_vec<E>(reinterpret_cast<const __nv_bfloat16 *>(base) + v * 16 * D + bf_off(D, r16, lane * E));
+        } else {
+            const uint32_t at = v * 16 * RB + nib_off(RB, r16, lane * E / 2);
+            const uint8_t *resid = rec + p.resid_off + blk * (16 * D);
+            uint32_t b, r;
+            if constexpr (E == 4) {
+                b = *reinterpret_cast<const uint16_t *>(base + at);
+                r = *reinterpret_cast<const uint16_t *>(resid + at);
+            } else {
+                b = base[at];
+                r = resid[at];
+            }
+            const float s = __half2float(*reinterpret_cast<const __half *>(base + 32 * RB + v * 32 * NG +
+                                                                           (r16 * NG + lane / (32 / NG)) * 2));
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int q4 = static_cast<int>(b >> (4 * e) & 15u) - 8, rr = static_cast<int>(r >> (4 * e) & 15u) - 8;
+                x[v].v[e] = planes == 1 ? s * q4 : s * 0.0625f * (16 * q4 + rr);
+            }
+        }
+    }
+    store_vec<E>(k_out + wi * D + lane * E, x[0]);
+    store_vec<E>(v_out + wi * D + lane * E, x[1]);
+}
+
+// ---------------------------------------------------------------- host side
+nq_status rope_of(const nq_rope_plan *r, int head_dim, Rope &out)
+{
+    if (!r || !r->rates || !(r->layout == NQ_ROPE_HALF || r->layout == NQ_ROPE_INTERLEAVED)) return NQ_ERR_ARG;
+    if (r->rot_dim < 8 || r->rot_dim % 8 != 0 || r->rot_dim > head_dim) return NQ_ERR_SHAPE;
+    if (!aligned16(r->rates)) return NQ_ERR_ALIGN;
+    out = Rope{r->rot_dim, r->layout, r->mscale, reinterpret_cast<const unsigned long long *>(r->rates)};
+    return NQ_OK;
+}
+// Heads per warp: one batch of rows when that fills the machine (16 warps per
+// SM), else fewer, so that a small call spreads over all SMs; more for long
+// prompts, where the sines of a token serve more rows.
+int heads_per_warp(long long T, int heads)
+{
+    int per = 2 * kBatch;
+    while (per > 1 && T * ((heads + per - 1) / per) < 16ll * sm_count()) per /= 2;
+    return per;
+}
+
+template <int D, typename TI, typename TO>
+void launch_rope(const Rope &R, const void *x, long long xs, const int32_t *pos, int T, int H, bool inverse, void *out,
+                 long long os, cudaStream_t s)
+{
+    const int per = heads_per_warp(T, H), chunks = (H + per - 1) / per;
+    const long long warps = static_cast<long long>(T) * chunks;
+    rope_kernel<D, TI, TO><<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(
+        R, static_cast<const TI *>(x), xs, pos, T, H, per, chunks, inverse, static_cast<TO *>(out), os);
+}
+template <int D>
+void launch_rope_t(const Rope &R, const void *x, int xt, long long xs, const int32_t *pos, int T, int H, bool inverse,
+                   void *out, int ot, long long os, cudaStream_t s)
+{
+    using B = __nv_bfloat16;
+    if (xt == NQ_F32) {
+        if (ot == NQ_F32) launch_rope<D, float, float>(R, x, xs, pos, T, H, inverse, out, os, s);
+        else launch_rope<D, float, B>(R, x, xs, pos, T, H, inverse, out, os, s);
+    } else {
+        if (ot == NQ_F32) launch_rope<D, B, float>(R, x, xs, pos, T, H, inverse, out, os, s);
+        else launch_rope<D, B, B>(R, x, xs, pos, T, H, inverse, out, os, s);
+    }
+}
+
+template <int D, int NG, typename TI>
+void launch_append(const Pool &p, const Map &m, const Rope &R, bool rope, const void *q, const void *k, const void *v,
+                   long long stride, const int32_t *seqs, const int32_t *pos, int T, int Hq, void *q_out,
+                   unsigned int *status, cudaStream_t s)
+{
+    const int all = Hq + 2 * p.H, per = heads_per_warp(T, all), chunks = (all + per - 1) / per;
+    const long long warps = static_cast<long long>(T) * chunks;
+    append_kernel<D, NG, TI><<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(
+        p, m, R, rope, static_cast<const TI *>(q), static_cast<const TI *>(k), static_cast<const TI *>(v), stride, seqs,
+        pos, T, Hq, per, chunks, static_cast<__nv_bfloat16 *>(q_out), status);
+}
+
+}  // namespace
+}  // namespace nq
+
+extern "C" nq_status nq_rope_rates(int rot_dim, double theta, int scaling, double factor, int old_len, uint64_t *rates,
+                                   float *mscale)
+{
+    if (!rates || !mscale || !(theta > 1.0) || !std::isfinite(theta)) return NQ_ERR_ARG;
+    if (scaling < NQ_ROPE_NONE || scaling > NQ_ROPE_PARTS) return NQ_ERR_ARG;
+    if (scaling != NQ_ROPE_NONE && !(factor >= 1.0 && std::isfinite(factor))) return NQ_ERR_ARG;
+    if (scaling == NQ_ROPE_PARTS && old_len < 1) return NQ_ERR_ARG;
+    if (rot_dim < 8 || rot_dim % 8 != 0 || rot_dim > 128) return NQ_ERR_SHAPE;
+    const double two_pi = 6.283185307179586476925286766559;
+    if (scaling == NQ_ROPE_NTK) theta *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+    *mscale = scaling == NQ_ROPE_PARTS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double w = std::pow(theta, -2.0 * i / rot_dim);
+        if (scaling == NQ_ROPE_LINEAR) w /= factor;
+        if (scaling == NQ_ROPE_PARTS) {
+            double keep = (old_len * w / two_pi - 1.0) / 31.0;
+            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+            w = w * keep + w / factor * (1.0 - keep);
+        }
+        // w <= 1, so the rate is below 2^64 / 6
+        rates[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(w / two_pi, 64)));
+    }
+    return NQ_OK;
+}
+
+extern "C" nq_status nq_rope(const nq_rope_plan *rope, const void *x, int x_dtype, int64_t x_stride, const int32_t *pos,
+                             int T, int heads, int head_dim, int inverse, void *out, int out_dtype, int64_t out_stride,
+                             cudaStream_t stream)
+{
+    if (!x || !pos || !out || T < 1 || heads < 1) return NQ_ERR_ARG;
+    if (!(x_dtype == NQ_F32 || x_dtype == NQ_BF16) || !(out_dtype == NQ_F32 || out_dtype == NQ_BF16)) return NQ_ERR_ARG;
+    if (!(head_dim == 64 || head_dim == 128) || heads > 65536) return NQ_ERR_SHAPE;
+    const int64_t row = static_cast<int64_t>(heads) * head_dim;
+    if (x_stride < row || out_stride < row || x_stride % 8 != 0 || out_stride % 8 != 0) return NQ_ERR_SHAPE;
+    nq::Rope R;
+    const nq_status st = nq::rope_of(rope, head_dim, R);
+    if (st != NQ_OK) return st;
+    if (!nq::aligned16(x) || !nq::aligned16(out) || !nq::aligned4(pos)) return NQ_ERR_ALIGN;
+    if (x == out && (x_dtype != out_dtype || x_stride != out_stride)) return NQ_ERR_ARG;
+    if (static_cast<double>(T) * heads / nq::kWarps > 2147483000.0) return NQ_ERR_SHAPE;
+    if (head_dim == 128)
+        nq::launch_rope_t<128>(R, x, x_dtype, x_stride, pos, T, heads, inverse != 0, out, out_dtype, out_stride, stream);
+    else
+        nq::launch_rope_t<64>(R, x, x_dtype, x_stride, pos, T, heads, inverse != 0, out, out_dtype, out_stride, stream);
+    return nq::cuda_status(cudaGetLastError());
+}
+
+extern "C" nq_status nq_page_append(const nq_page_pool *pool, int layer, const nq_page_map *map,
+                                    const nq_rope_plan *rope, const void *q, const void *k, const void *v, int dtype,
+                                    int64_t stride, const int32_t *seqs, const int32_t *pos, int T, int heads_q,
+                                    uint16_t *q_out, cudaStream_t stream)
+{
+    nq::Pool p;
+    nq::Map m;
+    nq_status st = nq::pool_map_of(pool, map, p, m, false);
+    if (st != NQ_OK) return st;
+    if (layer < 0 || layer >= pool->layers || !k || !v || !seqs || !pos || T < 1) return NQ_ERR_ARG;
+    if (!(dtype == NQ_F32 || dtype == NQ_BF16)) return NQ_ERR_ARG;
+    if (q ? (heads_q < 1 || !q_out) : (heads_q != 0 || q_out != nullptr)) return NQ_ERR_ARG;
+    if (heads_q > 65536) return NQ_ERR_SHAPE;
+    const int64_t row = static_cast<int64_t>(heads_q > p.H ? heads_q : p.H) * p.D;
+    if (stride < row || stride % 8 != 0) return NQ_ERR_SHAPE;
+    nq::Rope R{};
+    if (rope) {
+        st = nq::rope_of(rope, p.D, R);
+        if (st != NQ_OK) return st;
+    }
+    if (!nq::aligned16(k) || !nq::aligned16(v) || !nq::aligned16(q) || !nq::aligned16(q_out) || !nq::aligned4(seqs) ||
+        !nq::aligned4(pos))
+        return NQ_ERR_ALIGN;
+    if (static_cast<double>(T) * (heads_q + 2.0 * p.H) / nq::kWarps > 2147483000.0) return NQ_ERR_SHAPE;
+    unsigned int *status = nq::device_status_ptr();
+    if (!status) return NQ_ERR_CUDA;
+    p.data += static_cast<size_t>(layer) * p.layer_bytes;
+    auto go = [&](auto d, auto ng) {
+        constexpr int D = decltype(d)::value, NG = decltype(ng)::value;
+        if (dtype == NQ_F32)
+            nq::launch_append<D, NG, float>(p, m, R, rope != nullptr, q, k, v, stride, seqs, pos, T, heads_q, q_out, status, stream);
+        else
+            nq::launch_append<D, NG, __nv_bfloat16>(p, m, R, rope != nullptr, q, k, v, stride, seqs, pos, T, heads_q, q_out, status, stream);
+    };
+    using std::integral_constant;
+    const integral_constant<int, 64> d64;
+    const integral_constant<int, 128> d128;
+    const integral_constant<int, 0> bf;
+    const integral_constant<int, 1> g1;
+    const integral_constant<int, 2> g2;
+    if (p.D == 64) p.NG == 0 ? go(d64, bf) : go(d64, g1);
+    else p.NG == 0 ? go(d128, bf) : p.NG == 1 ? go(d128, g1) : go(d128, g2);
+    return nq::cuda_status(cudaGetLastError());
+}
+
+extern "C" nq_status nq_page_read(const nq_page_pool *pool, int layer, const nq_page_map *map, const int32_t *seqs,
+                                  const int32_t *pos, int T, int planes, uint16_t *k_out, uint16_t *v_out,
+                                  cudaStream_t stream)
+{
+    nq::Pool p;
+    nq::Map m;
+    const nq_status st = nq::pool_map_of(pool, map, p, m, false);
+    if (st != NQ_OK) return st;
+    if (layer < 0 || layer >= pool->layers || !seqs || !pos || !k_out || !v_out || T < 1 || (planes != 1 && planes != 2))
+        return NQ_ERR_ARG;
+    if (!nq::aligned16(k_out) || !nq::aligned16(v_out) || !nq::aligned4(seqs) || !nq::aligned4(pos)) return NQ_ERR_ALIGN;
+    const long long warps = static_cast<long long>(T) * p.H;
+    if (warps / nq::kWarps > 2147483000ll) return NQ_ERR_SHAPE;
+    unsigned int *status = nq::device_status_ptr();
+    if (!status) return NQ_ERR_CUDA;
+    p.data += static_cast<size_t>(layer) * p.layer_bytes;
+    const unsigned grid = static_cast<unsigned>((warps + nq::kWarps - 1) / nq::kWarps);
+    auto *ko = reinterpret_cast<__nv_bfloat16 *>(k_out), *vo = reinterpret_cast<__nv_bfloat16 *>(v_out);
+    auto go = [&](auto *kernel) { kernel<<<grid, nq::kWarps * 32, 0, stream>>>(p, m, seqs, pos, T, planes, ko, vo, status); };
+    if (p.D == 64) go(p.NG == 0 ? nq::read_kernel<64, 0> : nq::read_kernel<64, 1>);
+    else go(p.NG == 0 ? nq::read_kernel<128, 0> : p.NG == 1 ? nq::read_kernel<128, 1> : nq::read_kernel<128, 2>);
+    return nq::cuda_status(cudaGetLastError());
+}

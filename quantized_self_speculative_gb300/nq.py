@@ -21,6 +21,8 @@ LIB_PATH = os.path.join(_HERE, "libnq.so")
 NQ_OK, NQ_ERR_ARG, NQ_ERR_SHAPE, NQ_ERR_ALIGN, NQ_ERR_CUDA = 0, 1, 2, 3, 4
 NQ_ERR_NONFINITE, NQ_ERR_TIMEOUT, NQ_ERR_WORKSPACE, NQ_ERR_TOKEN = 5, 6, 7, 8
 NQ_DEV_NONFINITE, NQ_DEV_BAD_TOKEN, NQ_DEV_TIMEOUT, NQ_DEV_ACT_RANGE, NQ_DEV_SEQ_FULL = 0x1, 0x2, 0x4, 0x8, 0x10
+NQ_DEV_BAD_PAGE, NQ_DEV_POOL_FULL = 0x20, 0x40
+KV_NESTED44, KV_BF16 = 0, 1
 FMT_NESTED44, FMT_INT4, FMT_FP8E4M3_ROW, FMT_FP16 = 0, 1, 2, 3
 
 _lock = threading.Lock()
@@ -43,6 +45,26 @@ class nq_kv_cache(C.Structure):
                 ("max_len", C.c_int32), ("pad", C.c_int32),
                 ("k_base", C.c_void_p), ("k_resid", C.c_void_p), ("k_scales", C.c_void_p),
                 ("v_base", C.c_void_p), ("v_resid", C.c_void_p), ("v_scales", C.c_void_p)]
+
+
+class nq_rope_plan(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("layout", C.c_int32), ("mscale", C.c_float), ("pad", C.c_int32),
+                ("rates", C.c_void_p)]
+
+
+class nq_page_pool(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("layers", "n_pages", "page_size", "heads_kv", "head_dim", "group", "format",
+                                         "pad")] + [("data", C.c_void_p)]
+
+
+class nq_page_map(C.Structure):
+    _fields_ = [("max_seqs", C.c_int32), ("max_pages", C.c_int32), ("n_pages", C.c_int32), ("page_size", C.c_int32),
+                ("table", C.c_void_p), ("held", C.c_void_p), ("ref", C.c_void_p)]
+
+
+class nq_attn_opts(C.Structure):
+    _fields_ = [("scale", C.c_float), ("softcap", C.c_float), ("window", C.c_int32), ("pad", C.c_int32),
+                ("slopes", C.c_void_p)]
 
 
 def lib():
@@ -93,6 +115,27 @@ def lib():
             L.nq_embed_round.argtypes = [vp, i32, i32, vp, vp, i32, i32, vp, vp]
             L.spec_round_commit.argtypes = [vp, vp, i32, i32, vp, vp, i32, vp, vp]
             for name in ("spec_draft_argmax", "nq_embed_rows", "nq_embed_round", "spec_round_commit"):
+                getattr(L, name).restype = i32
+            i64, RP, PP, PM, AO = C.c_int64, C.POINTER(nq_rope_plan), C.POINTER(nq_page_pool), C.POINTER(nq_page_map), C.POINTER(nq_attn_opts)
+            L.nq_rope_rates.argtypes = [i32, C.c_double, i32, C.c_double, i32, vp, C.POINTER(f32)]
+            L.nq_rope.argtypes = [RP, vp, i32, i64, vp, i32, i32, i32, i32, vp, i32, i64, vp]
+            L.nq_page_pool_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, C.POINTER(sz)]
+            L.nq_page_map_init.argtypes = [PM, vp]
+            L.nq_page_workspace_bytes.argtypes = [PM, i32]
+            L.nq_page_workspace_bytes.restype = sz
+            L.nq_page_reserve.argtypes = [PM, PP, vp, vp, vp, i32, vp, vp, sz, vp]
+            L.nq_page_fork.argtypes = [PM, vp, vp, vp, i32, vp, sz, vp]
+            L.nq_page_truncate.argtypes = [PM, vp, vp, i32, vp]
+            L.nq_page_compact.argtypes = [PM, PP, vp, vp, sz, vp]
+            L.nq_page_copy.argtypes = [PP, vp, vp, i32, vp]
+            L.nq_page_append.argtypes = [PP, i32, PM, RP, vp, vp, vp, i32, i64, vp, vp, i32, i32, vp, vp]
+            L.nq_page_read.argtypes = [PP, i32, PM, vp, vp, i32, i32, vp, vp, vp]
+            L.nq_page_attn_workspace_bytes.argtypes = [i32, i32, i32, i32]
+            L.nq_page_attn_workspace_bytes.restype = sz
+            L.nq_page_attn.argtypes = [PP, i32, PM, vp, i64, i32, i32, i32, vp, vp, i32, AO, vp, vp, sz, vp]
+            for name in ("nq_rope_rates", "nq_rope", "nq_page_pool_bytes", "nq_page_map_init", "nq_page_reserve",
+                         "nq_page_fork", "nq_page_truncate", "nq_page_compact", "nq_page_copy", "nq_page_append",
+                         "nq_page_read", "nq_page_attn"):
                 getattr(L, name).restype = i32
             L.nq_selftest_bounded_wait.argtypes = [C.c_uint32, vp]
             L.nq_selftest_bounded_wait.restype = i32
@@ -440,6 +483,232 @@ class KVCache:
         sc = lambda t: t.cpu().numpy().view("uint16").reshape(*sh, self.head_dim // self.group)
         return dict(k_base=p(self.k_base), k_resid=p(self.k_resid), k_scales=sc(self.k_scales),
                     v_base=p(self.v_base), v_resid=p(self.v_resid), v_scales=sc(self.v_scales))
+
+
+# ---------------------------------------------------------------- rotary positions
+_DT = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _heads(t: torch.Tensor, T: int, H: int, D: int, dtype, what: str) -> int:
+    """Address of the heads of T tokens [T][H][D], each token's contiguous."""
+    if not t.is_cuda or t.dtype != dtype or t.shape != (T, H, D) or t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{what} must be a CUDA tensor of {dtype}, shape {(T, H, D)}, contiguous within a token")
+    return t.data_ptr()
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+class Rope:
+    """The rates of a rotation (nq_rope_rates) on the device.  layout "half" or
+    "interleaved"; scaling "none", "linear", "ntk" or "parts"."""
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, old_len: int = 0, device=None):
+        rates = torch.empty(max(rot_dim // 2, 1), dtype=torch.int64)
+        ms = C.c_float()
+        layouts, kinds = ("half", "interleaved"), ("none", "linear", "ntk", "parts")
+        if layout not in layouts or scaling not in kinds:
+            raise ValueError(f"layout is one of {layouts}, scaling one of {kinds}")
+        _check(lib().nq_rope_rates(rot_dim, float(theta), kinds.index(scaling), float(factor), int(old_len),
+                                   rates.data_ptr(), C.byref(ms)), "nq_rope_rates")
+        self.rot_dim, self.mscale = rot_dim, ms.value
+        self.rates = rates.to(device or torch.device("cuda"))
+        self.struct = nq_rope_plan(rot_dim, layouts.index(layout), ms.value, 0, self.rates.data_ptr())
+        self.ref = C.byref(self.struct)
+
+
+def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Tensor] = None, inverse: bool = False,
+         out_dtype=None, stream=None) -> torch.Tensor:
+    """Rotate x [T][heads][head_dim] (fp32 or bf16; tokens may be strided) by pos
+    int32 [T]; out defaults to a new contiguous tensor of out_dtype (x's).
+    inverse turns back: the gradient of the rotation."""
+    if x.dim() != 3 or x.dtype not in _DT:
+        raise ValueError("x must be fp32 or bf16 [T][heads][head_dim]")
+    T, H, D = x.shape
+    if out is None:
+        out = torch.empty((T, H, D), dtype=out_dtype or x.dtype, device=x.device)
+    elif out.dtype not in _DT or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must be fp32 or bf16, of out_dtype")
+    if pos.shape != (T,):
+        raise ValueError("pos must be int32 [T]")
+    if T == 0:
+        return out
+    _check(lib().nq_rope(plan.ref, _heads(x, T, H, D, x.dtype, "x"), _DT[x.dtype], _token_stride(x),
+                         _dev(pos, torch.int32, "pos"), T, H, D, int(inverse), _heads(out, T, H, D, out.dtype, "out"),
+                         _DT[out.dtype], _token_stride(out), _stream(stream)), "nq_rope")
+    return out
+
+
+# ---------------------------------------------------------------- paged KV cache
+class PageMap:
+    """Which pages the sequence slots hold (nq_page_map).  Device tensors int32:
+    table [max_seqs][max_pages], held [max_seqs], ref [n_pages]; those not given
+    are made and cleared.  A given table alone makes a map to append to and
+    read, whose pages the caller keeps."""
+
+    def __init__(self, max_seqs: int, max_pages: int, n_pages: int, page_size: int, table=None, held=None, ref=None,
+                 device=None, stream=None):
+        dev = table.device if table is not None else device or torch.device("cuda")
+        mk = lambda *s: torch.empty(s, dtype=torch.int32, device=dev)  # noqa: E731
+        fresh = table is None
+        if fresh and (held is not None or ref is not None):
+            raise ValueError("held and ref come with a table")
+        if fresh:
+            table, held, ref = mk(max_seqs, max_pages), mk(max_seqs), mk(n_pages)
+        if (held is None) != (ref is None):
+            raise ValueError("held and ref come together")
+        for t, shape in ((table, (max_seqs, max_pages)), (held, (max_seqs,)), (ref, (n_pages,))):
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"table, held and ref must have shapes {(max_seqs, max_pages)}, {(max_seqs,)}, {(n_pages,)}")
+        self.table, self.held, self.ref = table, held, ref
+        self.max_seqs, self.max_pages, self.n_pages, self.page_size = max_seqs, max_pages, n_pages, page_size
+        p = lambda t, what: None if t is None else _dev(t, torch.int32, what)  # noqa: E731
+        self.struct = nq_page_map(max_seqs, max_pages, n_pages, page_size, p(table, "table"), p(held, "held"), p(ref, "ref"))
+        self.ptr = C.byref(self.struct)
+        if fresh:
+            _check(lib().nq_page_map_init(self.ptr, _stream(stream)), "nq_page_map_init")
+
+    def workspace(self, n: int) -> torch.Tensor:
+        need = lib().nq_page_workspace_bytes(self.ptr, n)
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=self.table.device)
+
+    @staticmethod
+    def _list(t: torch.Tensor, n: int, what: str) -> int:
+        if t.shape != (n,):
+            raise ValueError(f"{what} must be int32 [{n}]")
+        return _dev(t, torch.int32, what)
+
+    def reserve(self, pool: Optional["PagePool"], seqs, first, last, granted=None, ws=None, stream=None) -> torch.Tensor:
+        """Pages for rows first[i] .. last[i]-1 of slots seqs[i], shared ones
+        copied first; returns int32 [n], 1 where served."""
+        n = seqs.shape[0]
+        granted = granted if granted is not None else torch.empty(n, dtype=torch.int32, device=seqs.device)
+        ws = ws if ws is not None else self.workspace(n)
+        _check(lib().nq_page_reserve(self.ptr, None if pool is None else pool.ptr, self._list(seqs, n, "seqs"),
+                                     self._list(first, n, "first"), self._list(last, n, "last"), n,
+                                     self._list(granted, n, "granted"), _dev(ws, torch.uint8, "ws"), ws.numel(),
+                                     _stream(stream)), "nq_page_reserve")
+        return granted
+
+    def fork(self, src, dst, rows, ws=None, stream=None) -> None:
+        """Slot dst[i] shares slot src[i]'s first rows[i] rows (all pairs at once)."""
+        n = src.shape[0]
+        ws = ws if ws is not None else self.workspace(n)
+        _check(lib().nq_page_fork(self.ptr, self._list(src, n, "src"), self._list(dst, n, "dst"),
+                                  self._list(rows, n, "rows"), n, _dev(ws, torch.uint8, "ws"), ws.numel(),
+                                  _stream(stream)), "nq_page_fork")
+
+    def truncate(self, seqs, rows, stream=None) -> None:
+        """Slot seqs[i] keeps the pages of its first rows[i] rows."""
+        n = seqs.shape[0]
+        _check(lib().nq_page_truncate(self.ptr, self._list(seqs, n, "seqs"), self._list(rows, n, "rows"), n,
+                                      _stream(stream)), "nq_page_truncate")
+
+    def compact(self, pool: "PagePool", used=None, ws=None, stream=None) -> torch.Tensor:
+        """Move the pages in use to the lowest ids; returns how many (int32 [1])."""
+        used = used if used is not None else torch.empty(1, dtype=torch.int32, device=self.table.device)
+        ws = ws if ws is not None else self.workspace(1)
+        _check(lib().nq_page_compact(self.ptr, pool.ptr, self._list(used, 1, "used"), _dev(ws, torch.uint8, "ws"),
+                                     ws.numel(), _stream(stream)), "nq_page_compact")
+        return used
+
+
+class PagePool:
+    """The pages of all layers (nq_page_pool); data uint8, made here unless given."""
+
+    def __init__(self, layers: int, n_pages: int, page_size: int, heads_kv: int, head_dim: int, fmt: int = KV_NESTED44,
+                 group: int = 128, data: Optional[torch.Tensor] = None, device=None):
+        n = C.c_size_t()
+        _check(lib().nq_page_pool_bytes(layers, n_pages, page_size, heads_kv, head_dim, group, fmt, C.byref(n)),
+               "nq_page_pool_bytes")
+        self.bytes = n.value
+        if data is None:
+            data = torch.zeros(n.value, dtype=torch.uint8, device=device or torch.device("cuda"))
+        if data.numel() != n.value:
+            raise ValueError(f"data must hold {n.value} bytes")
+        self.data, self.layers, self.n_pages, self.page_size = data, layers, n_pages, page_size
+        self.heads_kv, self.head_dim, self.group, self.fmt = heads_kv, head_dim, group, fmt
+        self.struct = nq_page_pool(layers, n_pages, page_size, heads_kv, head_dim, group, fmt, 0,
+                                   _dev(data, torch.uint8, "data"))
+        self.ptr = C.byref(self.struct)
+
+    def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+        """Copy pages src[i] to dst[i] in every layer."""
+        n = src.shape[0]
+        _check(lib().nq_page_copy(self.ptr, PageMap._list(src, n, "src"), PageMap._list(dst, n, "dst"), n,
+                                  _stream(stream)), "nq_page_copy")
+
+    def append(self, layer: int, pmap: PageMap, k: torch.Tensor, v: torch.Tensor, seqs: torch.Tensor, pos: torch.Tensor,
+               rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+               stream=None) -> Optional[torch.Tensor]:
+        """Store k, v [T][heads_kv][head_dim] (fp32 or bf16) as row pos[t] of slot
+        seqs[t], k rotated by pos; with q [T][heads_q][head_dim] returns the
+        rotated queries in bf16.  q, k and v may be columns of one tensor."""
+        T, H, D = k.shape[0], self.heads_kv, self.head_dim
+        if k.dtype not in _DT:
+            raise ValueError("k must be fp32 or bf16")
+        stride = _token_stride(k)
+        Hq = 0 if q is None else q.shape[1]
+        if T > 1 and (v.stride(0) != stride or (q is not None and q.stride(0) != stride)):
+            raise ValueError("q, k and v must have one stride between tokens")
+        if T == 1:
+            stride = max(H, Hq) * D
+        if q is not None and q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        if T == 0:
+            return q_out
+        _check(lib().nq_page_append(self.ptr, layer, pmap.ptr, None if rope is None else rope.ref,
+                                    None if q is None else _heads(q, T, Hq, D, k.dtype, "q"),
+                                    _heads(k, T, H, D, k.dtype, "k"), _heads(v, T, H, D, k.dtype, "v"), _DT[k.dtype],
+                                    stride, PageMap._list(seqs, T, "seqs"), PageMap._list(pos, T, "pos"), T, Hq,
+                                    None if q is None else self._rows(q_out, (T, Hq, D), "q_out"), _stream(stream)),
+               "nq_page_append")
+        return q_out
+
+    @staticmethod
+    def _rows(t: torch.Tensor, shape, what: str) -> int:
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what} must have shape {tuple(shape)}")
+        return _dev(t, torch.bfloat16, what)
+
+    def read(self, layer: int, pmap: PageMap, seqs: torch.Tensor, pos: torch.Tensor, planes: int = 2, k_out=None,
+             v_out=None, stream=None):
+        """The stored K and V rows pos[t] of slots seqs[t] as bf16 [T][heads_kv][head_dim]."""
+        T = seqs.shape[0]
+        shape = (T, self.heads_kv, self.head_dim)
+        mk = lambda t: t if t is not None else torch.empty(shape, dtype=torch.bfloat16, device=seqs.device)  # noqa: E731
+        k_out, v_out = mk(k_out), mk(v_out)
+        if T:
+            _check(lib().nq_page_read(self.ptr, layer, pmap.ptr, PageMap._list(seqs, T, "seqs"),
+                                      PageMap._list(pos, T, "pos"), T, int(planes), self._rows(k_out, shape, "k_out"),
+                                      self._rows(v_out, shape, "v_out"), _stream(stream)), "nq_page_read")
+        return k_out, v_out
+
+    def attention(self, layer: int, pmap: PageMap, q: torch.Tensor, lens: torch.Tensor, planes: int, scale: float,
+                  seqs: Optional[torch.Tensor] = None, softcap: float = 0.0, window: int = 0,
+                  slopes: Optional[torch.Tensor] = None, out=None, ws=None, stream=None) -> torch.Tensor:
+        """Attention of the last M rows of each sequence, q bf16 [batch][M][heads_q]
+        [head_dim]; sequence b is slot seqs[b] (slot b without seqs) of lens[b]
+        rows.  softcap, window and slopes (fp32 [heads_q]) as in nq_attn_opts."""
+        B, M, Hq, D = q.shape
+        if D != self.head_dim:
+            raise ValueError("q must have the pool's head_dim")
+        if slopes is not None and slopes.shape != (Hq,):
+            raise ValueError("slopes must be fp32 [heads_q]")
+        out = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if ws is None:
+            ws = torch.empty(max(lib().nq_page_attn_workspace_bytes(M, Hq, self.heads_kv, D), 16), dtype=torch.uint8,
+                             device=q.device)
+        o = nq_attn_opts(float(scale), float(softcap), int(window), 0,
+                         None if slopes is None else _dev(slopes, torch.float32, "slopes"))
+        _check(lib().nq_page_attn(self.ptr, layer, pmap.ptr, _dev(q, torch.bfloat16, "q"), Hq * D, B, M, Hq,
+                                  None if seqs is None else PageMap._list(seqs, B, "seqs"),
+                                  PageMap._list(lens, B, "lens"), int(planes), C.byref(o),
+                                  self._rows(out, (B, M, Hq, D), "out"), _dev(ws, torch.uint8, "ws"), ws.numel(),
+                                  _stream(stream)), "nq_page_attn")
+        return out
 
 
 def selftest_bounded_wait(limit_us: int, stream=None) -> None:
