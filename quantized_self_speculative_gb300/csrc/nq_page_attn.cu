@@ -2,112 +2,1047 @@
 // paged KV cache.
 //
 // out = sum_t p_t V_t / sum_t p_t, p_t = 2^(s_t - m), s = log2(e) f(scale q.K_t):
-// one pass over the rows with the running maximum m, sum and output, rescaled
-// when m grows.  One CTA of four warps per query vector, warp w takes rows w,
-// w + 4, ..; lane l holds D / 32 of the row's values.
+// one pass over the rows with the running maximum m, sum and output.  Every
+// K/V byte of the view that is read comes from HBM once; that is the bound.
+//
+// Work.  A (sequence, kv head, tile of query vectors) is a segment; its rows
+// are cut into steps of SR rows.  All steps of a call form one flat list,
+// dealt out in equal runs to a persistent grid, so ragged lengths balance
+// whatever they are (they are only known on the device).  The four warps of a
+// CTA take every fourth step of its run; each keeps its own softmax state and
+// its own ring of stages, filled by bulk copies of whole blocks that its lane
+// 0 issues ahead, across segment borders.  At a segment's end the warps' states
+// merge; a segment cut by runs leaves partial states that a second, dependent
+// launch joins.
+//
+// Arithmetic.  S^T = K Q^T and O^T = V^T P^T on the warp MMA (m16n8k16, fp32
+// accumulators) with 16 cache rows or 16 dimensions as M and 8 query vectors
+// as N, so that few queries waste nothing.  P^T goes from S^T's accumulators
+// to the B operand by an 8x8 transpose between lanes (movmatrix).
+// NESTED44: K's codes enter undequantised, an offset nibble (q4 + 8) or byte
+// (16 q4 + r + 136) in the low bits of an fp16 half (code 2^-24), placed by
+// masks; the offset leaves S through the accumulators' start.  The MMA adds such
+// small halves with some 18 bits, which moves a score by 10^-5 or so.  In O that
+// would show where large weights meet codes of zero, so V's codes become the
+// signed numbers themselves: the code under an exponent of 2^10, and one fma on
+// two halves that takes 2^10 and the offset off again.  K's scales multiply S, V's scales multiply P before it is rounded
+// to fp16 (one rounding, 2^-11).  So that no V magnitude underflows there, m is
+// the running maximum of s + log2(scale of V) and P = 2^(s - m) scale <= 2^kSlack.
+// The query is brought to a largest magnitude of 2^10 by a power of two.
+// BF16: K, V and the query as they are, P rounded to bf16 (2^-8); the sum is
+// taken of the rounded P, which takes most of that error out again.
+#include <atomic>
+
+#include "nq_mbar.cuh"
 #include "nq_page.cuh"
 
 namespace nq {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kCombWarps = 8;
+constexpr int kMinRun = 4;              // steps per CTA: one per warp
+constexpr float kLog2e = 1.4426950408889634f;
+// m is only raised when the maximum has grown by 2^kSlack: the accumulators are
+// rarely rescaled, and P stays far inside fp16's range
+constexpr float kSlack = 6.0f;
 
-template <int E>
-__device__ __forceinline__ void row_values(const Pool &p, const uint8_t *rec, int r, int v, int planes, int lane,
-                                           float (&x)[E])
+enum { kBf16 = 0, kKv4 = 1, kKv8 = 2 };
+
+template <int FMT, int D, int NG, int NT>
+struct Geo {
+    static constexpr int RB = D / 2;
+    static constexpr int BASE = FMT == kBf16 ? 64 * D : 16 * D + 64 * NG;   // bytes of a block
+    static constexpr int RESID = FMT == kKv8 ? 16 * D : 0;
+    static constexpr int BLKS = FMT == kBf16 && D == 128 ? 1 : 2;           // blocks of 16 rows per step
+    static constexpr int SR = 16 * BLKS;
+    static constexpr int STAGE = BLKS * (BASE + RESID);
+    // CTAs per SM and stages: as much in flight as shared memory holds beside
+    // the merge buffers (three CTAs where two stages fit, two where 128
+    // accumulators leave registers for no more)
+    static constexpr int MERGE = D * NT / 4 * 128;                          // accumulators of one warp
+    static constexpr int QF = NT == 4 ? D / 16 * NT * 32 * 8 : 0;           // query fragments in shared memory
+    static constexpr int FIX = 2 * MERGE + QF + 2 * 8 * NT * 8;
+    static constexpr int fit(int ctas) { return (233472 / ctas - 1024 - 512 - FIX) / (kWarps * STAGE); }
+    static constexpr int CTAS = NT == 4 || fit(3) < 2 ? 2 : 3;
+    static constexpr int STAGES_FIT = fit(CTAS);
+    static constexpr int STAGES = STAGES_FIT > 6 ? 6 : STAGES_FIT;
+    static constexpr int RING = kWarps * STAGES * STAGE;
+    static constexpr int SMEM = RING + FIX;
+    static_assert(STAGES >= 2, "ring");
+};
+
+struct Args {
+    Pool p;
+    Map m;
+    const __nv_bfloat16 *q;
+    long long q_stride;
+    int B, M, Hq, G, QT;                // G query heads per kv head, QT tiles per (sequence, kv head)
+    const int32_t *seqs, *len;
+    float scale, softcap;
+    int window;
+    const float *slopes;
+    __nv_bfloat16 *out;
+    int4 *info;                         // per CTA: the segment it leaves to later CTAs
+    float *part_o, *part_ml;
+    unsigned int *status;
+};
+
+// ---------------------------------------------------------------- small pieces
+template <int FMT>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    constexpr int D = 32 * E, RB = D / 2;
-    const int blk = r >> 4, r16 = r & 15;
-    const uint8_t *base = rec + blk * p.base_block;
-    if (p.NG == 0) {
-        const auto *src = reinterpret_cast<const __nv_bfloat16 *>(base) + v * 16 * D + bf_off(D, r16, lane * E);
+    if constexpr (FMT == kBf16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+                     "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        mma_f16(d, a0, a1, a2, a3, b0, b1);
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_h(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_b(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), absolute error about 2^-22 cap
+__device__ __forceinline__ float capped(float x, float cap, float inv2)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(x * inv2)));
+    return cap * fmaf(-2.0f, r, 1.0f);
+}
+// max over the eight lanes of a query column, sum likewise
+__device__ __forceinline__ float col_max(float x)
+{
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float col_sum(float x)
+{
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// Nibbles i (low half) and i + 4 (high half) of a word as fp16 halves: KV4
+// (q4 + 8) 2^-24, 16 times that for odd i (the other operand or the output
+// carries the 1/16); KV8 (16 q4 + r + 136) 2^-24, whose even and odd code bytes
+// are formed once per word.
+template <int FMT>
+struct Codes {
+    uint32_t e, o;
+    __device__ __forceinline__ Codes(uint32_t b, uint32_t r)
+    {
+        if constexpr (FMT == kKv8) {
+            e = ((b << 4) & 0xF0F0F0F0u) | (r & 0x0F0F0F0Fu);
+            o = (b & 0xF0F0F0F0u) | ((r >> 4) & 0x0F0F0F0Fu);
+        } else {
+            e = b;
+            o = b >> 8;
+        }
+    }
+    __device__ __forceinline__ uint32_t pair(int i) const
+    {
+        if constexpr (FMT == kKv8) {
+            const uint32_t x = i & 1 ? o : e;
+            return i >= 2 ? __byte_perm(x, 0u, 0x4341) : x & 0x00FF00FFu;
+        } else {
+            const uint32_t x = i >= 2 ? o : e;
+            return i & 1 ? x & 0x00F000F0u : x & 0x000F000Fu;
+        }
+    }
+    // the same pair as signed numbers, q4 or 16 q4 + r, exact
+    __device__ __forceinline__ uint32_t value(int i) const
+    {
+        uint32_t x;
+        if constexpr (FMT == kKv8) {
+            x = __byte_perm(i & 1 ? o : e, 0x64646464u, i >= 2 ? 0x4341 : 0x4240);               // 1024 + code
+            asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xE488E488u));                        // - 1160
+        } else {
+            x = i >= 2 ? o : e;
+            x = i & 1 ? (x & 0x00F000F0u) | 0x64006400u : (x & 0x000F000Fu) | 0x64006400u;       // 1024 + code (16 code)
+            if (i & 1) asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(x) : "r"(0x2C002C00u), "r"(0xD480D480u));   // / 16 - 72
+            else asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xE408E408u));                   // - 1032
+        }
+        return x;
+    }
+};
+template <int FMT> __host__ __device__ constexpr float odd_scale() { return FMT == kKv4 ? 16.0f : 1.0f; }
+
+// ---------------------------------------------------------------- sequences
+// The rows [lo, hi) of a sequence that any of its queries sees, lo a multiple
+// of SR, as steps.
+struct Seq {
+    int slot, lo, hi, steps;
+};
+template <int SR>
+__device__ __forceinline__ Seq seq_of(const Args &A, int b, bool report)
+{
+    Seq s;
+    s.slot = A.seqs ? A.seqs[b] : b;
+    const long long cap = static_cast<long long>(A.m.W) * A.m.P;
+    int n = A.len[b];
+    if (n > cap) {
+        n = static_cast<int>(cap);
+        if (report) set_status(A.status, NQ_DEV_SEQ_FULL);
+    }
+    if (s.slot < 0 || s.slot >= A.m.S) {
+        n = 0;
+        s.slot = 0;
+        if (report) set_status(A.status, NQ_DEV_BAD_PAGE);
+    }
+    s.hi = max(n, 0);
+    // the first query's own row is hi - M
+    s.lo = A.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(s.hi) - A.M - A.window + 1)) / SR * SR : 0;
+    s.steps = s.hi > s.lo ? (s.hi - s.lo + SR - 1) / SR : 0;
+    return s;
+}
+
+// A position in the flat list: step `at` of segment (b, seg); [begin, end) the
+// run's steps of this segment, in flat numbers.
+template <int SR>
+struct Walk {
+    int b, seg;
+    Seq s;
+    int base, end, stop;                // flat number of the segment's step 0; end of its part; end of the run
+    __device__ __forceinline__ void open(const Args &A, int b0, int b_base, int f0, int f1)
+    {
+        b = b0;
+        s = seq_of<SR>(A, b, false);
+        seg = (f0 - b_base) / s.steps;
+        base = b_base + seg * s.steps;
+        stop = f1;
+        end = min(base + s.steps, stop);
+    }
+    // to the next segment (only called while end < stop)
+    __device__ __forceinline__ void next(const Args &A, int segs)
+    {
+        base += s.steps;
+        if (++seg == segs) {
+            seg = 0;
+            do s = seq_of<SR>(A, ++b, false);
+            while (s.steps == 0);
+        }
+        end = min(base + s.steps, stop);
+    }
+};
+
+// ---------------------------------------------------------------- the kernel
+template <int FMT, int D, int NG, int NT>
+__global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NG, NT>::CTAS))
+attn_kernel(const __grid_constant__ Args A)
+{
+    using Q = Geo<FMT, D, NG, NT>;
+    constexpr int SR = Q::SR, BLKS = Q::BLKS, RB = Q::RB, KS = D / 16;
+    constexpr int JB = NT == 1 ? BLKS : 1;                       // blocks per softmax step
+    constexpr int NACC = FMT != kBf16 && D == 128 && (NG == 2 || NT == 1) ? 2 : 1;
+    constexpr int NGX = FMT == kBf16 ? 1 : NG;
+    constexpr int OFF = FMT == kKv8 ? 136 : 8;
+    constexpr int TILES = D / 16;
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ __align__(8) unsigned long long bars[kWarps * Q::STAGES];
+    __shared__ int sh_sum[kWarps], sh_base, sh_b, abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int segs = A.p.H * A.QT;
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    // ---- this CTA's run [f0, f1) of the flat list of steps, and the sequence it starts in
+    if (threadIdx.x < kWarps * Q::STAGES) mbar_init(smem_u32(bars + threadIdx.x), 1);
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    const int per_thread = (A.B + kThreads - 1) / kThreads, b_lo = min(static_cast<int>(threadIdx.x) * per_thread, A.B),
+              b_hi = min(b_lo + per_thread, A.B);
+    int mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += seq_of<SR>(A, b, blockIdx.x == 0).steps * segs;
+    int incl = mine;
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = __bfloat162float(src[e]);
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh_sum[warp] = incl;
+    __syncthreads();
+    int total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sh_sum[w];
+        total += sh_sum[w];
+    }
+    const int grid = gridDim.x, per = max(total / grid + (total % grid != 0), kMinRun);
+    const int f0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * per, static_cast<long long>(total))),
+              f1 = total - f0 < per ? total : f0 + per;
+    if (f0 < f1 && f0 >= before && f0 < before + mine) {
+        int at = before;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const int n = seq_of<SR>(A, b, false).steps * segs;
+            if (f0 < at + n) {
+                sh_b = b;
+                sh_base = at;
+                break;
+            }
+            at += n;
+        }
+    }
+    // sequences of which no query sees a row
+    for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
+        if (seq_of<SR>(A, b, false).steps != 0) continue;
+        const size_t n = static_cast<size_t>(A.M) * A.Hq * (D / 8);
+        uint4 *o = reinterpret_cast<uint4 *>(A.out) + b * n;
+        for (size_t i = threadIdx.x; i < n; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    if (f0 >= f1) {
+        if (threadIdx.x == 0) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
         return;
     }
-    const uint32_t at = v * 16 * RB + nib_off(RB, r16, lane * E / 2);
-    const uint8_t *resid = rec + p.resid_off + blk * (16 * D);
-    const float s = __half2float(
-        *reinterpret_cast<const __half *>(base + 32 * RB + v * 32 * p.NG + (r16 * p.NG + lane / (32 / p.NG)) * 2));
+
+    // ---- the ring: lane 0 issues, `fill` walks ahead of `use`
+    unsigned char *ring = sm + warp * (Q::STAGES * Q::STAGE);
+    const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(bars + warp * Q::STAGES);
+    float *merge = reinterpret_cast<float *>(sm + Q::RING);                      // [2][accumulator][lane]
+    float *merge_ml = merge + 2 * Q::MERGE / 4;                                  // [2][column][m, l]
+    uint2 *qf_s = reinterpret_cast<uint2 *>(merge_ml + 2 * 8 * NT * 2);          // [k step][tile][lane]
+    Walk<SR> fill, use;
+    use.open(A, sh_b, sh_base, f0, f1);
+    fill = use;
+    // flat numbers congruent to the warp's
+    int ff = f0 + ((warp - (f0 & 3)) & 3), fu = ff;
+    int id[BLKS];
+    bool more = true;
+    auto look = [&]() {                       // page ids of step ff
+        while (more && ff >= fill.end) {
+            if (fill.end >= fill.stop) more = false;
+            else fill.next(A, segs);
+        }
+        if (!more) return;
+        const int row = fill.s.lo + (ff - fill.base) * SR;
+        const int32_t *tab = A.m.table + static_cast<size_t>(fill.s.slot) * A.m.W;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int q4 = (base[at + e / 2] >> (4 * (e & 1)) & 15) - 8;
-        const int rr = planes == 2 ? (resid[at + e / 2] >> (4 * (e & 1)) & 15) - 8 : 0;
-        x[e] = s * (q4 + rr * 0.0625f);
+        for (int k = 0; k < BLKS; ++k) id[k] = row + 16 * k < fill.s.hi ? tab[(row + 16 * k) / A.m.P] : -1;
+    };
+    auto issue = [&](int st) {                // step ff into stage st, then on to the next
+        if (!more) return;
+        const int row = fill.s.lo + (ff - fill.base) * SR, head = fill.seg / A.QT;
+        if (lane == 0) {
+            const int n = min(BLKS, (fill.s.hi - row + 15) >> 4);
+            const uint32_t bar = bar_s + 8 * st;
+            mbar_expect_tx(bar, n * (Q::BASE + Q::RESID));
+#pragma unroll
+            for (int k = 0; k < BLKS; ++k) {
+                if (k >= n) continue;
+                if (id[k] < 0 || id[k] >= A.p.N) {
+                    set_status(A.status, NQ_DEV_BAD_PAGE);
+                    id[k] = 0;
+                }
+                const int blk = ((row + 16 * k) & (A.m.P - 1)) >> 4;
+                const uint8_t *rec = A.p.data + (static_cast<size_t>(id[k]) * A.p.H + head) * A.p.rec;
+                const uint32_t dst = ring_s + st * Q::STAGE + k * (Q::BASE + Q::RESID);
+                bulk_g2s(dst, rec + blk * Q::BASE, Q::BASE, bar);
+                if constexpr (FMT == kKv8) bulk_g2s(dst + Q::BASE, rec + A.p.resid_off + blk * Q::RESID, Q::RESID, bar);
+            }
+        }
+        ff += kWarps;
+        look();
+    };
+    look();
+#pragma unroll
+    for (int st = 0; st < Q::STAGES; ++st) issue(st);
+
+    int stage = 0;
+    uint32_t phase = 0;
+    const float inv2 = A.softcap > 0.0f ? 2.0f / A.softcap : 0.0f;               // 2^(2 log2(e) x / cap), x in base 2
+    const float cap2 = A.softcap * kLog2e;
+    for (;;) {
+        // ================================================= a segment (part)
+        const int kvh = use.seg / A.QT, v0 = (use.seg % A.QT) * 8 * NT, nv = min(8 * NT, A.M * A.G - v0);
+        const int m_lo = v0 / A.G, m_hi = (v0 + nv - 1) / A.G;
+        // ---- queries: fragments (column g of each tile), factors and limits of columns 2t, 2t + 1
+        uint32_t qf[NT == 4 ? 1 : KS][NT == 4 ? 1 : NT][2];
+        float cq[NT][2], start[NT][NGX][2], slope2[NT][2];
+        int own[NT][2];                       // row of the query itself; rows (own - window, own] are seen
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int v = v0 + 8 * nt + g;
+            const bool valid = v < v0 + nv;
+            const int m = valid ? v / A.G : 0, hq = kvh * A.G + (valid ? v % A.G : 0);
+            const __nv_bfloat16 *qr = A.q + (static_cast<long long>(use.b) * A.M + m) * A.q_stride + hq * D;
+            uint32_t fr[KS][2];
+            float f = 1.0f;
+            if constexpr (FMT == kBf16) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    fr[k][0] = valid ? *reinterpret_cast<const uint32_t *>(qr + 16 * k + 2 * t) : 0u;
+                    fr[k][1] = valid ? *reinterpret_cast<const uint32_t *>(qr + 16 * k + 2 * t + 8) : 0u;
+                }
+            } else {
+                // 8 values per word w of the lane's K bytes, in the words' order
+                float x[D / 32][8], top = 0.0f;
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    const int d = NG == 2 ? 64 * (w >> 1) + 16 * t + 8 * (w & 1) : (D == 128 ? 32 : 16) * t + 8 * w;
+                    const uint4 r = valid ? *reinterpret_cast<const uint4 *>(qr + d) : make_uint4(0, 0, 0, 0);
+                    const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[w][2 * j] = __uint_as_float(rw[j] << 16);
+                        x[w][2 * j + 1] = __uint_as_float(rw[j] & 0xFFFF0000u);
+                        top = fmaxf(top, fmaxf(fabsf(x[w][2 * j]), fabsf(x[w][2 * j + 1])));
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int up = min(137 - static_cast<int>(__float_as_uint(top) >> 23), 120);   // largest to [2^10, 2^11)
+                const float to = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                float sum[NGX] = {};
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        x[w][j] = __half2float(__float2half_rn(x[w][j] * to));
+                        sum[NG == 2 ? w >> 1 : 0] += x[w][j];
+                    }
+                    constexpr float odd = 1.0f / odd_scale<FMT>();
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        fr[2 * w + s][0] = pack_h(x[w][2 * s], x[w][2 * s + 4]);
+                        fr[2 * w + s][1] = pack_h(x[w][2 * s + 1] * odd, x[w][2 * s + 5] * odd);
+                    }
+                }
+#pragma unroll
+                for (int gr = 0; gr < NGX; ++gr) {
+                    sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
+                    sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        start[nt][gr][c] = -static_cast<float>(OFF) * 5.9604644775390625e-08f *
+                                           __shfl_sync(0xffffffffu, sum[gr], 4 * (2 * t + c));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int vc = min(v0 + 8 * nt + 2 * t + c, v0 + nv - 1);
+                const float fc = FMT == kBf16 ? 1.0f : __shfl_sync(0xffffffffu, f, 4 * (2 * t + c));
+                // undo the codes' 2^-24 (and, for KV8, the 16) and the query's power of two
+                cq[nt][c] = A.scale * kLog2e * fc * (FMT == kBf16 ? 1.0f : FMT == kKv8 ? 1048576.0f : 16777216.0f);
+                own[nt][c] = use.s.hi - A.M + vc / A.G;
+                slope2[nt][c] = A.slopes ? A.slopes[kvh * A.G + vc % A.G] * kLog2e : 0.0f;
+            }
+            if constexpr (NT == 4) {
+                if (warp == nt) {
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) qf_s[(k * NT + nt) * 32 + lane] = make_uint2(fr[k][0], fr[k][1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    qf[k][nt][0] = fr[k][0];
+                    qf[k][nt][1] = fr[k][1];
+                }
+            }
+        }
+        if constexpr (NT == 4) __syncthreads();
+        auto qfrag = [&](int k, int nt, uint32_t &b0, uint32_t &b1) {
+            if constexpr (NT == 4) {
+                const uint2 r = qf_s[(k * NT + nt) * 32 + lane];
+                b0 = r.x;
+                b1 = r.y;
+            } else {
+                b0 = qf[k][nt][0];
+                b1 = qf[k][nt][1];
+            }
+        };
+        // rows that every query of the tile sees: no mask needed there
+        const int all_hi = use.s.hi - A.M + m_lo + 1, all_lo = A.window > 0 ? use.s.hi - A.M + m_hi - A.window + 1 : 0;
+        // rows that any of them sees
+        const int any_hi = use.s.hi - A.M + m_hi + 1, any_lo = A.window > 0 ? use.s.hi - A.M + m_lo - A.window + 1 : 0;
+
+        float o[TILES][NT][4], mref[NT][2], lsum[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
+            mref[nt][0] = mref[nt][1] = -INFINITY;
+            lsum[nt][0] = lsum[nt][1] = 0.0f;
+        }
+
+        // ================================================= its steps
+        for (; fu < use.end; fu += kWarps) {
+            mbar_wait(bar_s + 8 * stage, phase, &abort_flag, A.status);
+            const int row0 = use.s.lo + (fu - use.base) * SR;
+            const unsigned char *sp = ring + stage * Q::STAGE;
+            auto blocks = [&](auto mask_c, int j0) {
+                constexpr bool MASK = decltype(mask_c)::value;
+                // ---- S^T
+                float acc[JB][NT][NACC][4];
+#pragma unroll
+                for (int j = 0; j < JB; ++j)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int h = 0; h < NACC; ++h)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                acc[j][nt][h][e] = FMT != kBf16 && (NG == 2 || h == 0) ? start[nt][NG == 2 ? h : 0][e & 1] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                    const unsigned char *bp = sp + (j0 + j) * (Q::BASE + Q::RESID);
+                    if constexpr (FMT == kBf16) {
+                        const int r = (lane & 7) + 8 * ((lane >> 3) & 1);
+                        const uint32_t at = smem_u32(bp) + r * 2 * D;
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            uint32_t a0, a1, a2, a3, b0, b1;
+                            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
+                                         : "r"(at + (((2 * k + (lane >> 4)) ^ (r & 7)) << 4)) : "memory");
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                qfrag(k, nt, b0, b1);
+                                mma<FMT>(acc[j][nt][0], a0, a1, a2, a3, b0, b1);
+                            }
+                        }
+                    } else {
+                        constexpr int NW = D / 32;
+                        uint32_t kb[2][NW], kr[2][NW];
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            const int r = g + 8 * rr;
+                            if constexpr (D == 128 && NG == 1) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(bp + nib_off(RB, r, 16 * t));
+                                kb[rr][0] = x.x; kb[rr][1] = x.y; kb[rr][2] = x.z; kb[rr][3] = x.w;
+                                if constexpr (FMT == kKv8) {
+                                    const uint4 y = *reinterpret_cast<const uint4 *>(bp + Q::BASE + nib_off(RB, r, 16 * t));
+                                    kr[rr][0] = y.x; kr[rr][1] = y.y; kr[rr][2] = y.z; kr[rr][3] = y.w;
+                                }
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < D / 64; ++h) {
+                                    const uint2 x = *reinterpret_cast<const uint2 *>(bp + nib_off(RB, r, 32 * h + 8 * t));
+                                    kb[rr][2 * h] = x.x; kb[rr][2 * h + 1] = x.y;
+                                    if constexpr (FMT == kKv8) {
+                                        const uint2 y = *reinterpret_cast<const uint2 *>(bp + Q::BASE + nib_off(RB, r, 32 * h + 8 * t));
+                                        kr[rr][2 * h] = y.x; kr[rr][2 * h + 1] = y.y;
+                                    }
+                                }
+                            }
+                            if constexpr (FMT != kKv8) {
+#pragma unroll
+                                for (int w = 0; w < NW; ++w) kr[rr][w] = 0u;
+                            }
+                        }
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) {
+                            const Codes<FMT> c0(kb[0][w], kr[0][w]), c1(kb[1][w], kr[1][w]);
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                const uint32_t a0 = c0.pair(2 * s), a1 = c1.pair(2 * s), a2 = c0.pair(2 * s + 1), a3 = c1.pair(2 * s + 1);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    uint32_t b0, b1;
+                                    qfrag(2 * w + s, nt, b0, b1);
+                                    mma<FMT>(acc[j][nt][NACC == 2 ? w >> 1 : 0], a0, a1, a2, a3, b0, b1);
+                                }
+                            }
+                        }
+                    }
+                }
+                // ---- scales of the rows g, g + 8 of each block; log2 of V's
+                float sk[JB][2][NGX], sv[JB][2][NGX], lv[JB][2];
+                if constexpr (FMT != kBf16) {
+#pragma unroll
+                    for (int j = 0; j < JB; ++j) {
+                        const __half *sc = reinterpret_cast<const __half *>(sp + (j0 + j) * (Q::BASE + Q::RESID) + 32 * RB);
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            float top = 0.0f;
+#pragma unroll
+                            for (int gr = 0; gr < NGX; ++gr) {
+                                sk[j][rr][gr] = __half2float(sc[(g + 8 * rr) * NG + gr]);
+                                sv[j][rr][gr] = __half2float(sc[16 * NG + (g + 8 * rr) * NG + gr]);
+                                top = fmaxf(top, sv[j][rr][gr]);
+                            }
+                            lv[j][rr] = lg2(fmaxf(top, 3.7252902984619140625e-09f));   // a scale of 0 has codes of 0
+                        }
+                    }
+                }
+                // ---- softmax
+                uint32_t pb[JB][NT][NGX][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float s[JB][2][2];
+                    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int j = 0; j < JB; ++j)
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float x;
+                                const int e = 2 * rr + c;
+                                if constexpr (FMT == kBf16) x = acc[j][nt][0][e];
+                                else if constexpr (NG == 2) x = fmaf(sk[j][rr][1], acc[j][nt][1][e], sk[j][rr][0] * acc[j][nt][0][e]);
+                                else x = sk[j][rr][0] * (NACC == 2 ? acc[j][nt][0][e] + acc[j][nt][NACC - 1][e] : acc[j][nt][0][e]);
+                                x *= cq[nt][c];
+                                if (A.softcap > 0.0f) x = capped(x, cap2, inv2);
+                                const int key = row0 + 16 * (j0 + j) + g + 8 * rr;
+                                if (A.slopes) x = fmaf(slope2[nt][c], static_cast<float>(key - own[nt][c]), x);
+                                if constexpr (MASK)
+                                    if (key > own[nt][c] || (A.window > 0 && key <= own[nt][c] - A.window)) x = -INFINITY;
+                                s[j][rr][c] = x;
+                                float y = x;
+                                if constexpr (FMT != kBf16) y = MASK && x == -INFINITY ? x : x + lv[j][rr];
+                                top[c] = fmaxf(top[c], y);
+                            }
+                    float alpha[2];
+                    bool grow = false;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        top[c] = col_max(top[c]);
+                        alpha[c] = 1.0f;
+                        if (top[c] > mref[nt][c] + kSlack) {
+                            alpha[c] = mref[nt][c] == -INFINITY ? 0.0f : ex2(mref[nt][c] - top[c]);
+                            mref[nt][c] = top[c];
+                            grow = true;
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            lsum[nt][c] *= alpha[c];
+#pragma unroll
+                            for (int i = 0; i < TILES; ++i) {
+                                o[i][nt][c] *= alpha[c];
+                                o[i][nt][2 + c] *= alpha[c];
+                            }
+                        }
+                    }
+                    const float mr[2] = {mref[nt][0] == -INFINITY ? 0.0f : mref[nt][0], mref[nt][1] == -INFINITY ? 0.0f : mref[nt][1]};
+#pragma unroll
+                    for (int j = 0; j < JB; ++j)
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            const float e0 = ex2(s[j][rr][0] - mr[0]), e1 = ex2(s[j][rr][1] - mr[1]);
+                            if constexpr (FMT == kBf16) {
+                                const uint32_t p = pack_b(e0, e1);
+                                lsum[nt][0] += __uint_as_float(p << 16);
+                                lsum[nt][1] += __uint_as_float(p & 0xFFFF0000u);
+                                pb[j][nt][0][rr] = transpose8(p);
+                            } else {
+                                lsum[nt][0] += e0;
+                                lsum[nt][1] += e1;
+#pragma unroll
+                                for (int gr = 0; gr < NGX; ++gr) {
+                                    float p0 = e0 * sv[j][rr][gr], p1 = e1 * sv[j][rr][gr];
+                                    if constexpr (MASK) {       // a masked row's scale may be anything
+                                        if (s[j][rr][0] == -INFINITY) p0 = 0.0f;
+                                        if (s[j][rr][1] == -INFINITY) p1 = 0.0f;
+                                    }
+                                    pb[j][nt][gr][rr] = transpose8(pack_h(p0, p1));
+                                }
+                            }
+                        }
+                }
+                // ---- O^T
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                    const unsigned char *bp = sp + (j0 + j) * (Q::BASE + Q::RESID);
+                    if constexpr (FMT == kBf16) {
+                        const int r = (lane & 7) + 8 * (lane >> 4), blk0 = row0 + 16 * (j0 + j);
+                        const uint32_t at = smem_u32(bp) + 32 * D + r * 2 * D;
+                        auto product = [&](uint32_t k0, uint32_t k1, int only) {   // V rows kept; one query row alone, or all
+#pragma unroll
+                            for (int i = 0; i < TILES; ++i) {
+                                uint32_t a0, a1, a2, a3;
+                                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
+                                             : "r"(at + (((2 * i + ((lane >> 3) & 1)) ^ (r & 7)) << 4)) : "memory");
+                                if constexpr (MASK) {
+                                    a0 &= k0; a1 &= k0; a2 &= k1; a3 &= k1;
+                                }
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    if (MASK && only >= 0) {          // 0 times infinity must not reach the other columns
+                                        float one[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                                        mma<FMT>(one, a0, a1, a2, a3, pb[j][nt][0][0], pb[j][nt][0][1]);
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            if ((v0 + 8 * nt + 2 * t + (e & 1)) / A.G == only) o[i][nt][e] += one[e];
+                                    } else {
+                                        mma<FMT>(o[i][nt], a0, a1, a2, a3, pb[j][nt][0][0], pb[j][nt][0][1]);
+                                    }
+                                }
+                            }
+                        };
+                        if constexpr (MASK) {
+                            // P is 0 where a query does not see a row, but 0 times NaN or infinity is not:
+                            // rows that no query sees (they may hold anything) leave V's fragments.  A
+                            // non-finite row that only some queries see is rare; then query row by query row.
+                            auto kept = [&](int lo, int hi, int k) {
+                                const int a = blk0 + 2 * t + 8 * k;
+                                return (a >= lo && a < hi ? 0x0000FFFFu : 0u) | (a + 1 >= lo && a + 1 < hi ? 0xFFFF0000u : 0u);
+                            };
+                            bool bad = false;
+                            if (m_hi > m_lo) {
+                                const int rr = lane >> 1, key = blk0 + rr;
+                                if (key >= any_lo && key < any_hi && !(key >= all_lo && key < all_hi)) {
+                                    const uint4 *x = reinterpret_cast<const uint4 *>(bp + 32 * D + rr * 2 * D) + (lane & 1) * (D / 16);
+#pragma unroll 4
+                                    for (int i = 0; i < D / 16; ++i) {
+                                        const uint4 y = x[i];
+                                        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                                        for (int u = 0; u < 4; ++u)
+                                            bad |= (w[u] & 0x7F80u) == 0x7F80u || (w[u] & 0x7F800000u) == 0x7F800000u;
+                                    }
+                                }
+                            }
+                            if (__any_sync(0xffffffffu, bad)) {
+                                for (int m = m_lo; m <= m_hi; ++m) {
+                                    const int hi = use.s.hi - A.M + m + 1, lo = A.window > 0 ? hi - A.window : 0;
+                                    product(kept(lo, hi, 0), kept(lo, hi, 1), m);
+                                }
+                            } else {
+                                product(kept(any_lo, any_hi, 0), kept(any_lo, any_hi, 1), -1);
+                            }
+                        } else {
+                            product(0u, 0u, -1);
+                        }
+                    } else {
+                        constexpr int NW = D / 64;
+                        uint32_t vb[4][NW], vr[4][NW];
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const int r = 2 * t + (kk & 1) + 8 * (kk >> 1);
+                            if constexpr (D == 128 && NG == 1) {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(bp + 16 * RB + nib_off(RB, r, 8 * g));
+                                vb[kk][0] = x.x; vb[kk][1] = x.y;
+                                if constexpr (FMT == kKv8) {
+                                    const uint2 y = *reinterpret_cast<const uint2 *>(bp + Q::BASE + 16 * RB + nib_off(RB, r, 8 * g));
+                                    vr[kk][0] = y.x; vr[kk][1] = y.y;
+                                }
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < NW; ++h) {
+                                    vb[kk][h] = *reinterpret_cast<const uint32_t *>(bp + 16 * RB + nib_off(RB, r, 32 * h + 4 * g));
+                                    if constexpr (FMT == kKv8)
+                                        vr[kk][h] = *reinterpret_cast<const uint32_t *>(bp + Q::BASE + 16 * RB + nib_off(RB, r, 32 * h + 4 * g));
+                                }
+                            }
+                            if constexpr (FMT != kKv8) {
+#pragma unroll
+                                for (int h = 0; h < NW; ++h) vr[kk][h] = 0u;
+                            }
+                        }
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) {
+                            // nibbles of rows 2t | 2t + 1 and 2t + 8 | 2t + 9 side by side
+                            const Codes<FMT> x0(__byte_perm(vb[0][w], vb[1][w], 0x5410), __byte_perm(vr[0][w], vr[1][w], 0x5410)),
+                                x1(__byte_perm(vb[0][w], vb[1][w], 0x7632), __byte_perm(vr[0][w], vr[1][w], 0x7632)),
+                                y0(__byte_perm(vb[2][w], vb[3][w], 0x5410), __byte_perm(vr[2][w], vr[3][w], 0x5410)),
+                                y1(__byte_perm(vb[2][w], vb[3][w], 0x7632), __byte_perm(vr[2][w], vr[3][w], 0x7632));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t a0 = x0.value(i), a1 = x1.value(i), a2 = y0.value(i), a3 = y1.value(i);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma<FMT>(o[4 * w + i][nt], a0, a1, a2, a3, pb[j][nt][NG == 2 ? w : 0][0], pb[j][nt][NG == 2 ? w : 0][1]);
+                            }
+                        }
+                    }
+                }
+            };
+#pragma unroll
+            for (int j0 = 0; j0 < BLKS; j0 += JB) {
+                const int a = row0 + 16 * j0;
+                if (a >= any_hi) break;                          // not copied, or seen by no query
+                if (a >= all_lo && a + 16 * JB <= all_hi) blocks(std::false_type{}, j0);
+                else blocks(std::true_type{}, j0);
+            }
+            // the stage was read through the generic proxy, the next copy writes through the async one
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            issue(stage);
+            if (++stage == Q::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+
+        // ================================================= the segment's end: the warps merge
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            lsum[nt][0] = col_sum(lsum[nt][0]);
+            lsum[nt][1] = col_sum(lsum[nt][1]);
+        }
+        auto put = [&](int buf) {
+            float *d = merge + buf * (Q::MERGE / 4) + lane;
+#pragma unroll
+            for (int i = 0; i < TILES; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[((i * NT + nt) * 4 + e) * 32] = o[i][nt][e];
+            if (g == 0) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        merge_ml[(buf * 8 * NT + 8 * nt + 2 * t + c) * 2] = mref[nt][c];
+                        merge_ml[(buf * 8 * NT + 8 * nt + 2 * t + c) * 2 + 1] = lsum[nt][c];
+                    }
+            }
+        };
+        auto take = [&](int buf) {
+            const float *d = merge + buf * (Q::MERGE / 4) + lane;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float fa[2], fb[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float mb = merge_ml[(buf * 8 * NT + 8 * nt + 2 * t + c) * 2], lb = merge_ml[(buf * 8 * NT + 8 * nt + 2 * t + c) * 2 + 1];
+                    const float mn = fmaxf(mref[nt][c], mb), mz = mn == -INFINITY ? 0.0f : mn;
+                    fa[c] = ex2(mref[nt][c] - mz);
+                    fb[c] = ex2(mb - mz);
+                    mref[nt][c] = mn;
+                    lsum[nt][c] = lsum[nt][c] * fa[c] + lb * fb[c];
+                }
+#pragma unroll
+                for (int i = 0; i < TILES; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[i][nt][e] = o[i][nt][e] * fa[e & 1] + d[((i * NT + nt) * 4 + e) * 32] * fb[e & 1];
+            }
+        };
+        __syncthreads();                      // warp 0 is done with the buffers of the segment before
+        if (warp >= 2) put(warp - 2);
+        __syncthreads();
+        if (warp < 2) take(warp);
+        __syncthreads();
+        if (warp == 1) put(0);
+        __syncthreads();
+        if (warp == 0) {
+            take(0);
+            const bool starts = use.base >= f0, ends = use.base + use.s.steps <= f1, whole = starts && ends;
+            if (!ends && starts && lane == 0)
+                A.info[blockIdx.x] = make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / per, 0);
+            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0);
+            constexpr float unit = FMT == kKv8 ? 0.0625f : 1.0f;                 // KV8's codes are 16 times the value
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int col = 8 * nt + 2 * t + c;
+                    if (col >= nv) continue;
+                    const float f = unit * (!whole ? 1.0f : lsum[nt][c] == 0.0f ? 0.0f : 1.0f / lsum[nt][c]);
+                    const int v = v0 + col;
+                    __nv_bfloat16 *to = A.out + ((static_cast<size_t>(use.b) * A.M + v / A.G) * A.Hq + kvh * A.G + v % A.G) * D;
+                    float *po = A.part_o + (slot * 8 * NT + col) * D;
+                    if (!whole && g == 0) {
+                        A.part_ml[(slot * 8 * NT + col) * 2] = mref[nt][c];
+                        A.part_ml[(slot * 8 * NT + col) * 2 + 1] = lsum[nt][c];
+                    }
+                    if constexpr (FMT == kBf16) {
+#pragma unroll
+                        for (int i = 0; i < TILES; ++i)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                if (whole) to[16 * i + 8 * r + g] = __float2bfloat16_rn(o[i][nt][2 * r + c] * f);
+                                else po[16 * i + 8 * r + g] = o[i][nt][2 * r + c] * f;
+                            }
+                    } else {
+                        // a lane's eight values of word w: dimensions d .. d + 7
+#pragma unroll
+                        for (int w = 0; w < D / 64; ++w) {
+                            const int d = D == 128 && NG == 1 ? 16 * g + 8 * w : 64 * w + 8 * g;
+                            float x[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                x[i] = o[4 * w + i][nt][c] * f;
+                                x[4 + i] = o[4 * w + i][nt][2 + c] * f;
+                            }
+                            if (whole) {
+                                *reinterpret_cast<uint4 *>(to + d) = make_uint4(pack_b(x[0], x[1]), pack_b(x[2], x[3]),
+                                                                                pack_b(x[4], x[5]), pack_b(x[6], x[7]));
+                            } else {
+                                *reinterpret_cast<float4 *>(po + d) = make_float4(x[0], x[1], x[2], x[3]);
+                                *reinterpret_cast<float4 *>(po + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                            }
+                        }
+                    }
+                }
+        }
+        if (use.end >= use.stop) {
+            // the run ends with its last segment, or inside one that an earlier run began
+            if (threadIdx.x == 0 && (use.base + use.s.steps <= f1 || use.base < f0)) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            break;
+        }
+        use.next(A, segs);
     }
 }
 
-template <int E>
-__global__ void __launch_bounds__(kWarps * 32)
-attn_kernel(Pool p, Map m, const __nv_bfloat16 *__restrict__ q, long long q_stride, int M, int Hq,
-            const int32_t *__restrict__ seqs, const int32_t *__restrict__ len, int planes, nq_attn_opts o,
-            __nv_bfloat16 *__restrict__ out, unsigned int *status)
+// ---------------------------------------------------------------- joining
+// CTA (i, v): query vector v of the segment that run i begins and later runs
+// end (if there is one): out = sum_r 2^(m_r - M) o_r / sum_r 2^(m_r - M) l_r
+// over the runs' partial states, eight warps taking every eighth.
+template <int D, int NV>
+__global__ void __launch_bounds__(kCombWarps * 32)
+join_kernel(const __grid_constant__ Args A)
 {
-    constexpr int D = 32 * E;
-    __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int hq = blockIdx.x, mi = blockIdx.y, b = blockIdx.z, h = hq / (Hq / p.H);
-    const int slot = seqs ? seqs[b] : b;
-    const long long cap = static_cast<long long>(m.W) * m.P;
-    int L = len[b];
-    if (L > cap) {
-        if (threadIdx.x == 0) set_status(status, NQ_DEV_SEQ_FULL);
-        L = static_cast<int>(cap);
-    }
-    if (slot < 0 || slot >= m.S) {
-        if (threadIdx.x == 0) set_status(status, NQ_DEV_BAD_PAGE);
-        L = 0;
-    }
-    const int at = L - M + mi, lo = o.window > 0 ? max(0, at - o.window + 1) : 0;
-    const __nv_bfloat16 *qr = q + (static_cast<long long>(b) * M + mi) * q_stride + hq * D + lane * E;
-    float qv[E], acc[E], mx = -INFINITY, l = 0.0f;
+    constexpr int E = D / 32;
+    __shared__ float sm_m[kCombWarps], sm_l[kCombWarps], sm_o[kCombWarps][D];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 in = A.info[blockIdx.x];
+    if (in.x < 0) return;
+    const int kvh = in.y / A.QT, v = (in.y % A.QT) * NV + blockIdx.y;
+    if (v >= A.M * A.G) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x, n = in.z - first + 1;
+    float m = -INFINITY, l = 0.0f, o[E] = {};
+    constexpr int U = 4;
+    for (int r0 = warp; r0 < n; r0 += kCombWarps * U) {
+        float mm[U], ll[U], oo[U][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qv[e] = __bfloat162float(qr[e]);
-        acc[e] = 0.0f;
-    }
-    for (int t = lo + warp; t <= at; t += kWarps) {
-        const int id = m.table[static_cast<size_t>(slot) * m.W + t / m.P];
-        if (id < 0 || id >= p.N) {
-            set_status(status, NQ_DEV_BAD_PAGE);
-            continue;
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * kCombWarps;
+            mm[u] = -INFINITY;
+            ll[u] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) oo[u][e] = 0.0f;
+            if (r < n) {
+                const size_t at = (2 * static_cast<size_t>(first + r) + (r == 0 ? 1 : 0)) * NV + blockIdx.y;
+                mm[u] = A.part_ml[at * 2];
+                ll[u] = A.part_ml[at * 2 + 1];
+                const float *p = A.part_o + at * D + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; ++e) oo[u][e] = p[e];
+            }
         }
-        const uint8_t *rec = p.data + (static_cast<size_t>(id) * p.H + h) * p.rec;
-        float kv[E], vv[E], s = 0.0f;
-        row_values<E>(p, rec, t % m.P, 0, planes, lane, kv);
-        row_values<E>(p, rec, t % m.P, 1, planes, lane, vv);
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(qv[e], kv[e], s);
+        for (int u = 0; u < U; ++u) {
+            const float mn = fmaxf(m, mm[u]), mz = mn == -INFINITY ? 0.0f : mn, a = ex2(m - mz), f = ex2(mm[u] - mz);
+            l = l * a + ll[u] * f;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= o.scale;
-        if (o.softcap > 0.0f) s = o.softcap * tanhf(s / o.softcap);
-        if (o.slopes) s -= o.slopes[hq] * static_cast<float>(at - t);
-        const float mn = fmaxf(mx, s), a = mx == -INFINITY ? 0.0f : expf(mx - mn), e1 = expf(s - mn);
-        mx = mn;
-        l = fmaf(l, a, e1);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], a, e1 * vv[e]);
+            for (int e = 0; e < E; ++e) o[e] = o[e] * a + oo[u][e] * f;
+            m = mn;
+        }
     }
     if (lane == 0) {
-        sm_m[warp] = mx;
+        sm_m[warp] = m;
         sm_l[warp] = l;
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = acc[e];
+    for (int e = 0; e < E; ++e) sm_o[warp][lane * E + e] = o[e];
     __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-        float M2 = -INFINITY, num = 0.0f, den = 0.0f;
-        for (int w = 0; w < kWarps; ++w) M2 = fmaxf(M2, sm_m[w]);
-        for (int w = 0; w < kWarps; ++w) {
-            if (sm_m[w] == -INFINITY) continue;
-            const float f = expf(sm_m[w] - M2);
-            num = fmaf(f, sm_o[w][d], num);
-            den = fmaf(f, sm_l[w], den);
-        }
-        const float r = at < lo ? 0.0f : num / den;
-        out[((static_cast<long long>(b) * M + mi) * Hq + hq) * D + d] = __float2bfloat16_rn(r);
+    if (threadIdx.x >= D / 2) return;
+    float M2 = -INFINITY, x0 = 0.0f, x1 = 0.0f, den = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCombWarps; ++w) M2 = fmaxf(M2, sm_m[w]);
+    if (M2 == -INFINITY) M2 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCombWarps; ++w) {
+        const float f = ex2(sm_m[w] - M2);
+        x0 = fmaf(f, sm_o[w][2 * threadIdx.x], x0);
+        x1 = fmaf(f, sm_o[w][2 * threadIdx.x + 1], x1);
+        den = fmaf(f, sm_l[w], den);
     }
+    const float f = den == 0.0f ? 0.0f : 1.0f / den;
+    const size_t row = (static_cast<size_t>(in.x) * A.M + v / A.G) * A.Hq + kvh * A.G + v % A.G;
+    reinterpret_cast<uint32_t *>(A.out + row * D)[threadIdx.x] = pack_b(x0 * f, x1 * f);
+}
+
+// ---------------------------------------------------------------- host side
+template <int FMT, int D, int NG, int NT>
+cudaError_t launch(Args A, cudaStream_t s)
+{
+    using Q = Geo<FMT, D, NG, NT>;
+    static std::atomic<bool> done[64];          // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev].load()) {
+        e = cudaFuncSetAttribute(attn_kernel<FMT, D, NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::SMEM);
+        if (e != cudaSuccess) return e;
+        done[dev].store(true);
+    }
+    const int grid = sm_count() * Q::CTAS;
+    attn_kernel<FMT, D, NG, NT><<<grid, kThreads, Q::SMEM, s>>>(A);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int nv = A.M * A.G < 8 * NT ? A.M * A.G : 8 * NT;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, nv);
+    cfg.blockDim = dim3(kCombWarps * 32);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, 8 * NT>, A);
+}
+template <int FMT, int D, int NG>
+cudaError_t launch_nt(int nt, const Args &A, cudaStream_t s)
+{
+    return nt == 1 ? launch<FMT, D, NG, 1>(A, s) : nt == 2 ? launch<FMT, D, NG, 2>(A, s) : launch<FMT, D, NG, 4>(A, s);
+}
+template <int FMT>
+cudaError_t launch_d(int nt, const Args &A, cudaStream_t s)
+{
+    if (A.p.D == 64) return launch_nt<FMT, 64, 1>(nt, A, s);
+    if constexpr (FMT != kBf16)
+        if (A.p.NG == 2) return launch_nt<FMT, 128, 2>(nt, A, s);
+    return launch_nt<FMT, 128, 1>(nt, A, s);
+}
+
+// Query vectors per tile: the fewest tiles of 8 that hold them, at most four
+// (the accumulators of more do not fit the registers).
+int tiles_of(int vectors) { return vectors <= 8 ? 1 : vectors <= 16 ? 2 : 4; }
+constexpr int kMaxCtas = 3;
+
+// Workspace: info, then partial states for two segments per CTA.
+struct Ws {
+    size_t info, ml, o, total;
+};
+Ws ws_of(int vectors, int D)
+{
+    const size_t ctas = static_cast<size_t>(kMaxCtas) * sm_count(), cols = 2 * ctas * 8 * tiles_of(vectors);
+    Ws w;
+    w.info = 0;
+    w.ml = ctas * sizeof(int4);
+    w.o = w.ml + cols * 8;
+    w.total = w.o + cols * D * 4;
+    return w;
 }
 
 }  // namespace
@@ -116,7 +1051,8 @@ attn_kernel(Pool p, Map m, const __nv_bfloat16 *__restrict__ q, long long q_stri
 extern "C" size_t nq_page_attn_workspace_bytes(int M, int heads_q, int heads_kv, int head_dim)
 {
     if (M < 1 || heads_kv < 1 || heads_q < heads_kv || heads_q % heads_kv != 0 || !(head_dim == 64 || head_dim == 128)) return 0;
-    return 16;
+    if (static_cast<long long>(M) * (heads_q / heads_kv) > 65536) return 0;
+    return nq::ws_of(M * (heads_q / heads_kv), head_dim).total;
 }
 
 extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,
@@ -124,25 +1060,46 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
                                   const int32_t *len, int planes, const nq_attn_opts *opts, uint16_t *out, void *ws,
                                   size_t ws_bytes, cudaStream_t stream)
 {
-    nq::Pool p;
-    nq::Map m;
-    const nq_status st = nq::pool_map_of(pool, map, p, m, false);
+    nq::Args A{};
+    const nq_status st = nq::pool_map_of(pool, map, A.p, A.m, false);
     if (st != NQ_OK) return st;
+    const nq::Pool &p = A.p;
     if (layer < 0 || layer >= pool->layers || !q || !len || !out || !opts || batch < 1 || M < 1) return NQ_ERR_ARG;
-    if (heads_q < p.H || heads_q % p.H != 0 || (planes != 1 && planes != 2) || (!seqs && batch > m.S)) return NQ_ERR_ARG;
+    if (heads_q < p.H || heads_q % p.H != 0 || (planes != 1 && planes != 2) || (!seqs && batch > A.m.S)) return NQ_ERR_ARG;
     if (!(opts->scale > 0.0f) || !(opts->softcap >= 0.0f) || opts->window < 0) return NQ_ERR_ARG;
-    if (M > 65535 || batch > 65535 || heads_q > 65536) return NQ_ERR_SHAPE;
+    const int G = heads_q / p.H;
+    if (static_cast<long long>(M) * G > 65536) return NQ_ERR_SHAPE;
     if (q_stride < static_cast<int64_t>(heads_q) * p.D || q_stride % 8 != 0) return NQ_ERR_SHAPE;
     if (!nq::aligned16(q) || !nq::aligned16(out) || !nq::aligned16(ws) || !nq::aligned4(seqs) || !nq::aligned4(len) ||
         !nq::aligned4(opts->slopes))
         return NQ_ERR_ALIGN;
-    if (!ws || ws_bytes < nq_page_attn_workspace_bytes(M, heads_q, p.H, p.D)) return NQ_ERR_WORKSPACE;
-    unsigned int *status = nq::device_status_ptr();
-    if (!status) return NQ_ERR_CUDA;
-    p.data += static_cast<size_t>(layer) * p.layer_bytes;
-    auto *kernel = p.D == 128 ? nq::attn_kernel<4> : nq::attn_kernel<2>;
-    kernel<<<dim3(heads_q, M, batch), nq::kWarps * 32, 0, stream>>>(
-        p, m, reinterpret_cast<const __nv_bfloat16 *>(q), q_stride, M, heads_q, seqs, len, planes, *opts,
-        reinterpret_cast<__nv_bfloat16 *>(out), status);
-    return nq::cuda_status(cudaGetLastError());
+    const nq::Ws w = nq::ws_of(M * G, p.D);
+    if (!ws || ws_bytes < w.total) return NQ_ERR_WORKSPACE;
+    A.status = nq::device_status_ptr();
+    if (!A.status) return NQ_ERR_CUDA;
+    A.p.data += static_cast<size_t>(layer) * p.layer_bytes;
+    A.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    A.q_stride = q_stride;
+    A.B = batch;
+    A.M = M;
+    A.Hq = heads_q;
+    A.G = G;
+    const int nt = nq::tiles_of(M * G);
+    A.QT = (M * G + 8 * nt - 1) / (8 * nt);
+    // the kernel numbers the steps of all segments in 32 bits
+    if (static_cast<double>(batch) * p.H * A.QT * (static_cast<double>(A.m.W) * A.m.P / 16 + 2) > 2.0e9) return NQ_ERR_SHAPE;
+    A.seqs = seqs;
+    A.len = len;
+    A.scale = opts->scale;
+    A.softcap = opts->softcap;
+    A.window = opts->window;
+    A.slopes = opts->slopes;
+    A.out = reinterpret_cast<__nv_bfloat16 *>(out);
+    uint8_t *wb = static_cast<uint8_t *>(ws);
+    A.info = reinterpret_cast<int4 *>(wb + w.info);
+    A.part_ml = reinterpret_cast<float *>(wb + w.ml);
+    A.part_o = reinterpret_cast<float *>(wb + w.o);
+    const cudaError_t e = p.NG == 0 ? nq::launch_d<nq::kBf16>(nt, A, stream)
+                          : planes == 1 ? nq::launch_d<nq::kKv4>(nt, A, stream) : nq::launch_d<nq::kKv8>(nt, A, stream);
+    return nq::cuda_status(e);
 }

@@ -39,6 +39,7 @@
 // copies and MMAs, frees its tensor memory (kept if the MMA drain itself gave
 // up, since MMAs might still write it) and returns.
 #include "nq_internal.cuh"
+#include "nq_mbar.cuh"
 
 #include <cuda.h>           // CUtensorMap (types only; the encoder is fetched through the runtime)
 #include <cudaTypedefs.h>
@@ -58,7 +59,6 @@ constexpr int kTcKBWide = 256;         // inputs per k-block when the padded M i
 constexpr int kTcMaxP = 64;            // linears per launch (two 128-byte tensor maps each)
 constexpr int kTcThreads = 736;        // warps 0-15 decode, 16-19 epilogue, 20 B copy, 21 MMA, 22 weight loads
 constexpr int kTmemCols = 512;
-constexpr unsigned long long kWaitNs = 2000000000ull;   // 2 s per wait
 
 struct TcProb {
     const uint8_t *base;
@@ -77,77 +77,6 @@ struct TcBatch {
 };
 
 // ---------------------------------------------------------------- PTX wrappers
-__device__ __forceinline__ uint32_t smem_u32(const void *p)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-// try_wait with a suspend-time hint: a waiting warp sleeps (up to 10 ms) until
-// the phase completes instead of spinning and taking issue slots from the
-// warps that do the work.
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(10000000u) : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ unsigned long long global_ns()
-{
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-// Wait for the phase of `bar` with the given parity.  Gives up after
-// limit_ns (sets the CTA's abort flag and NQ_DEV_TIMEOUT) or when another
-// role of the CTA has given up; returns false then.
-__device__ __noinline__ bool mbar_wait_until(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                             unsigned int *status, unsigned long long limit_ns)
-{
-    const unsigned long long t0 = global_ns();
-    for (;;) {
-        if (mbar_try(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (global_ns() - t0 > limit_ns) {
-            *abort_flag = 1;
-            set_status(status, NQ_DEV_TIMEOUT);
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                               unsigned int *status)
-{
-    return mbar_wait_until(bar, parity, abort_flag, status, kWaitNs);
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                          unsigned int *status)
-{
-    return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort_flag, status);
-}
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
-}
 // One lane of a converged warp (the warp's loop state stays warp-uniform, so
 // descriptors and addresses live in uniform registers for tcgen05 issue).
 __device__ __forceinline__ bool elect_one()
