@@ -13,7 +13,7 @@
 // its own ring of stages, filled by bulk copies of whole blocks that its lane
 // 0 issues ahead, across segment borders.  At a segment's end the warps' states
 // merge; a segment cut by runs leaves partial states that a second, dependent
-// launch joins.
+// launch joins.  More than 16 query vectors per kv head: nq_page_attn_wide.cu.
 //
 // Arithmetic.  S^T = K Q^T and O^T = V^T P^T on the warp MMA (m16n8k16, fp32
 // accumulators) with 16 cache rows or 16 dimensions as M and 8 query vectors
@@ -33,368 +33,106 @@
 // taken of the rounded P, which takes most of that error out again.
 #include <atomic>
 
-#include "nq_mbar.cuh"
-#include "nq_page.cuh"
+#include "nq_page_attn.cuh"
 
 namespace nq {
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCombWarps = 8;
+constexpr int kJoinWarps = 8;
 constexpr int kMinRun = 4;              // steps per CTA: one per warp
-constexpr float kLog2e = 1.4426950408889634f;
-// m is only raised when the maximum has grown by 2^kSlack: the accumulators are
-// rarely rescaled, and P stays far inside fp16's range
-constexpr float kSlack = 6.0f;
-
-enum { kBf16 = 0, kKv4 = 1, kKv8 = 2 };
 
 template <int FMT, int D, int NG, int NT>
 struct Geo {
-    static constexpr int RB = D / 2;
-    static constexpr int BASE = FMT == kBf16 ? 64 * D : 16 * D + 64 * NG;   // bytes of a block
-    static constexpr int RESID = FMT == kKv8 ? 16 * D : 0;
-    static constexpr int BLKS = FMT == kBf16 && D == 128 ? 1 : 2;           // blocks of 16 rows per step
+    static constexpr int BASE = block_base(FMT, D, NG), RESID = block_resid(FMT, D);
+    // blocks of 16 rows per step.  Two share one maximum and give the MMA four
+    // chains: 116 us against 148 with one (KV4, 131072 rows of 32 heads)
+    static constexpr int BLKS = FMT == kBf16 && D == 128 ? 1 : 2;
     static constexpr int SR = 16 * BLKS;
     static constexpr int STAGE = BLKS * (BASE + RESID);
     // CTAs per SM and stages: as much in flight as shared memory holds beside
-    // the merge buffers (three CTAs where two stages fit, two where 128
-    // accumulators leave registers for no more)
+    // the merge buffers, three CTAs where two stages fit
     static constexpr int MERGE = D * NT / 4 * 128;                          // accumulators of one warp
-    static constexpr int QF = NT == 4 ? D / 16 * NT * 32 * 8 : 0;           // query fragments in shared memory
-    static constexpr int FIX = 2 * MERGE + QF + 2 * 8 * NT * 8;
+    static constexpr int FIX = 2 * MERGE + 2 * 8 * NT * 8;
     static constexpr int fit(int ctas) { return (233472 / ctas - 1024 - 512 - FIX) / (kWarps * STAGE); }
-    static constexpr int CTAS = NT == 4 || fit(3) < 2 ? 2 : 3;
-    static constexpr int STAGES_FIT = fit(CTAS);
-    static constexpr int STAGES = STAGES_FIT > 6 ? 6 : STAGES_FIT;
+    static constexpr int CTAS = fit(3) < 2 ? 2 : 3;
+    static constexpr int STAGES = fit(CTAS) > 6 ? 6 : fit(CTAS);
     static constexpr int RING = kWarps * STAGES * STAGE;
     static constexpr int SMEM = RING + FIX;
     static_assert(STAGES >= 2, "ring");
 };
 
-struct Args {
-    Pool p;
-    Map m;
-    const __nv_bfloat16 *q;
-    long long q_stride;
-    int B, M, Hq, G, QT;                // G query heads per kv head, QT tiles per (sequence, kv head)
-    const int32_t *seqs, *len;
-    float scale, softcap;
-    int window;
-    const float *slopes;
-    __nv_bfloat16 *out;
-    int4 *info;                         // per CTA: the segment it leaves to later CTAs
-    float *part_o, *part_ml;
-    unsigned int *status;
-};
-
-// ---------------------------------------------------------------- small pieces
-template <int FMT>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    if constexpr (FMT == kBf16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
-                     "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        mma_f16(d, a0, a1, a2, a3, b0, b1);
-}
-__device__ __forceinline__ uint32_t transpose8(uint32_t x)
-{
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_h(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_b(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float lg2(float x)
-{
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), absolute error about 2^-22 cap
-__device__ __forceinline__ float capped(float x, float cap, float inv2)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(x * inv2)));
-    return cap * fmaf(-2.0f, r, 1.0f);
-}
-// max over the eight lanes of a query column, sum likewise
-__device__ __forceinline__ float col_max(float x)
-{
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-}
-__device__ __forceinline__ float col_sum(float x)
-{
-    x += __shfl_xor_sync(0xffffffffu, x, 4);
-    x += __shfl_xor_sync(0xffffffffu, x, 8);
-    return x + __shfl_xor_sync(0xffffffffu, x, 16);
-}
-
-// Nibbles i (low half) and i + 4 (high half) of a word as fp16 halves: KV4
-// (q4 + 8) 2^-24, 16 times that for odd i (the other operand or the output
-// carries the 1/16); KV8 (16 q4 + r + 136) 2^-24, whose even and odd code bytes
-// are formed once per word.
-template <int FMT>
-struct Codes {
-    uint32_t e, o;
-    __device__ __forceinline__ Codes(uint32_t b, uint32_t r)
-    {
-        if constexpr (FMT == kKv8) {
-            e = ((b << 4) & 0xF0F0F0F0u) | (r & 0x0F0F0F0Fu);
-            o = (b & 0xF0F0F0F0u) | ((r >> 4) & 0x0F0F0F0Fu);
-        } else {
-            e = b;
-            o = b >> 8;
-        }
-    }
-    __device__ __forceinline__ uint32_t pair(int i) const
-    {
-        if constexpr (FMT == kKv8) {
-            const uint32_t x = i & 1 ? o : e;
-            return i >= 2 ? __byte_perm(x, 0u, 0x4341) : x & 0x00FF00FFu;
-        } else {
-            const uint32_t x = i >= 2 ? o : e;
-            return i & 1 ? x & 0x00F000F0u : x & 0x000F000Fu;
-        }
-    }
-    // the same pair as signed numbers, q4 or 16 q4 + r, exact
-    __device__ __forceinline__ uint32_t value(int i) const
-    {
-        uint32_t x;
-        if constexpr (FMT == kKv8) {
-            x = __byte_perm(i & 1 ? o : e, 0x64646464u, i >= 2 ? 0x4341 : 0x4240);               // 1024 + code
-            asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xE488E488u));                        // - 1160
-        } else {
-            x = i >= 2 ? o : e;
-            x = i & 1 ? (x & 0x00F000F0u) | 0x64006400u : (x & 0x000F000Fu) | 0x64006400u;       // 1024 + code (16 code)
-            if (i & 1) asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(x) : "r"(0x2C002C00u), "r"(0xD480D480u));   // / 16 - 72
-            else asm("add.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(0xE408E408u));                   // - 1032
-        }
-        return x;
-    }
-};
-template <int FMT> __host__ __device__ constexpr float odd_scale() { return FMT == kKv4 ? 16.0f : 1.0f; }
-
-// ---------------------------------------------------------------- sequences
-// The rows [lo, hi) of a sequence that any of its queries sees, lo a multiple
-// of SR, as steps.
-struct Seq {
-    int slot, lo, hi, steps;
-};
-template <int SR>
-__device__ __forceinline__ Seq seq_of(const Args &A, int b, bool report)
-{
-    Seq s;
-    s.slot = A.seqs ? A.seqs[b] : b;
-    const long long cap = static_cast<long long>(A.m.W) * A.m.P;
-    int n = A.len[b];
-    if (n > cap) {
-        n = static_cast<int>(cap);
-        if (report) set_status(A.status, NQ_DEV_SEQ_FULL);
-    }
-    if (s.slot < 0 || s.slot >= A.m.S) {
-        n = 0;
-        s.slot = 0;
-        if (report) set_status(A.status, NQ_DEV_BAD_PAGE);
-    }
-    s.hi = max(n, 0);
-    // the first query's own row is hi - M
-    s.lo = A.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(s.hi) - A.M - A.window + 1)) / SR * SR : 0;
-    s.steps = s.hi > s.lo ? (s.hi - s.lo + SR - 1) / SR : 0;
-    return s;
-}
-
-// A position in the flat list: step `at` of segment (b, seg); [begin, end) the
-// run's steps of this segment, in flat numbers.
-template <int SR>
-struct Walk {
-    int b, seg;
-    Seq s;
-    int base, end, stop;                // flat number of the segment's step 0; end of its part; end of the run
-    __device__ __forceinline__ void open(const Args &A, int b0, int b_base, int f0, int f1)
-    {
-        b = b0;
-        s = seq_of<SR>(A, b, false);
-        seg = (f0 - b_base) / s.steps;
-        base = b_base + seg * s.steps;
-        stop = f1;
-        end = min(base + s.steps, stop);
-    }
-    // to the next segment (only called while end < stop)
-    __device__ __forceinline__ void next(const Args &A, int segs)
-    {
-        base += s.steps;
-        if (++seg == segs) {
-            seg = 0;
-            do s = seq_of<SR>(A, ++b, false);
-            while (s.steps == 0);
-        }
-        end = min(base + s.steps, stop);
-    }
-};
-
-// ---------------------------------------------------------------- the kernel
-template <int FMT, int D, int NG, int NT>
+// X: scores are capped or biased.
+template <int FMT, int D, int NG, int NT, bool X>
 __global__ void __launch_bounds__(kThreads, (Geo<FMT, D, NG, NT>::CTAS))
-attn_kernel(const __grid_constant__ Args A)
+attn_kernel(const __grid_constant__ AttnArgs A)
 {
     using Q = Geo<FMT, D, NG, NT>;
-    constexpr int SR = Q::SR, BLKS = Q::BLKS, RB = Q::RB, KS = D / 16;
-    constexpr int JB = NT == 1 ? BLKS : 1;                       // blocks per softmax step
+    constexpr int SR = Q::SR, BLKS = Q::BLKS, RB = D / 2, KS = D / 16;
+    constexpr int JB = FMT == kBf16 ? 1 : BLKS;                  // blocks per softmax step
     constexpr int NACC = FMT != kBf16 && D == 128 && (NG == 2 || NT == 1) ? 2 : 1;
     constexpr int NGX = FMT == kBf16 ? 1 : NG;
     constexpr int OFF = FMT == kKv8 ? 136 : 8;
     constexpr int TILES = D / 16;
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ __align__(8) unsigned long long bars[kWarps * Q::STAGES];
-    __shared__ int sh_sum[kWarps], sh_base, sh_b, abort_flag;
+    __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int segs = A.p.H * A.QT;
     asm volatile("griddepcontrol.launch_dependents;");
-
-    // ---- this CTA's run [f0, f1) of the flat list of steps, and the sequence it starts in
     if (threadIdx.x < kWarps * Q::STAGES) mbar_init(smem_u32(bars + threadIdx.x), 1);
     if (threadIdx.x == 0) {
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const int per_thread = (A.B + kThreads - 1) / kThreads, b_lo = min(static_cast<int>(threadIdx.x) * per_thread, A.B),
-              b_hi = min(b_lo + per_thread, A.B);
-    int mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += seq_of<SR>(A, b, blockIdx.x == 0).steps * segs;
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sh_sum[warp] = incl;
-    __syncthreads();
-    int total = 0, before = incl - mine;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sh_sum[w];
-        total += sh_sum[w];
-    }
-    const int grid = gridDim.x, per = max(total / grid + (total % grid != 0), kMinRun);
-    const int f0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * per, static_cast<long long>(total))),
-              f1 = total - f0 < per ? total : f0 + per;
-    if (f0 < f1 && f0 >= before && f0 < before + mine) {
-        int at = before;
-        for (int b = b_lo; b < b_hi; ++b) {
-            const int n = seq_of<SR>(A, b, false).steps * segs;
-            if (f0 < at + n) {
-                sh_b = b;
-                sh_base = at;
-                break;
-            }
-            at += n;
-        }
-    }
-    // sequences of which no query sees a row
-    for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
-        if (seq_of<SR>(A, b, false).steps != 0) continue;
-        const size_t n = static_cast<size_t>(A.M) * A.Hq * (D / 8);
-        uint4 *o = reinterpret_cast<uint4 *>(A.out) + b * n;
-        for (size_t i = threadIdx.x; i < n; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
-    }
-    __syncthreads();
-    if (f0 >= f1) {
+    const Run run = find_run<SR, kThreads, D>(A, segs, kMinRun);
+    if (run.f0 >= run.f1) {
         if (threadIdx.x == 0) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
         return;
     }
 
-    // ---- the ring: lane 0 issues, `fill` walks ahead of `use`
     unsigned char *ring = sm + warp * (Q::STAGES * Q::STAGE);
-    const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(bars + warp * Q::STAGES);
+    const uint32_t bar_s = smem_u32(bars + warp * Q::STAGES);
     float *merge = reinterpret_cast<float *>(sm + Q::RING);                      // [2][accumulator][lane]
     float *merge_ml = merge + 2 * Q::MERGE / 4;                                  // [2][column][m, l]
-    uint2 *qf_s = reinterpret_cast<uint2 *>(merge_ml + 2 * 8 * NT * 2);          // [k step][tile][lane]
-    Walk<SR> fill, use;
-    use.open(A, sh_b, sh_base, f0, f1);
-    fill = use;
-    // flat numbers congruent to the warp's
-    int ff = f0 + ((warp - (f0 & 3)) & 3), fu = ff;
-    int id[BLKS];
-    bool more = true;
-    auto look = [&]() {                       // page ids of step ff
-        while (more && ff >= fill.end) {
-            if (fill.end >= fill.stop) more = false;
-            else fill.next(A, segs);
-        }
-        if (!more) return;
-        const int row = fill.s.lo + (ff - fill.base) * SR;
-        const int32_t *tab = A.m.table + static_cast<size_t>(fill.s.slot) * A.m.W;
-#pragma unroll
-        for (int k = 0; k < BLKS; ++k) id[k] = row + 16 * k < fill.s.hi ? tab[(row + 16 * k) / A.m.P] : -1;
-    };
-    auto issue = [&](int st) {                // step ff into stage st, then on to the next
-        if (!more) return;
-        const int row = fill.s.lo + (ff - fill.base) * SR, head = fill.seg / A.QT;
-        if (lane == 0) {
-            const int n = min(BLKS, (fill.s.hi - row + 15) >> 4);
-            const uint32_t bar = bar_s + 8 * st;
-            mbar_expect_tx(bar, n * (Q::BASE + Q::RESID));
-#pragma unroll
-            for (int k = 0; k < BLKS; ++k) {
-                if (k >= n) continue;
-                if (id[k] < 0 || id[k] >= A.p.N) {
-                    set_status(A.status, NQ_DEV_BAD_PAGE);
-                    id[k] = 0;
-                }
-                const int blk = ((row + 16 * k) & (A.m.P - 1)) >> 4;
-                const uint8_t *rec = A.p.data + (static_cast<size_t>(id[k]) * A.p.H + head) * A.p.rec;
-                const uint32_t dst = ring_s + st * Q::STAGE + k * (Q::BASE + Q::RESID);
-                bulk_g2s(dst, rec + blk * Q::BASE, Q::BASE, bar);
-                if constexpr (FMT == kKv8) bulk_g2s(dst + Q::BASE, rec + A.p.resid_off + blk * Q::RESID, Q::RESID, bar);
-            }
-        }
-        ff += kWarps;
-        look();
-    };
-    look();
-#pragma unroll
-    for (int st = 0; st < Q::STAGES; ++st) issue(st);
-
-    int stage = 0;
+    Walk<SR> use;
+    use.open(A, run.b, run.base, run.f0, run.f1);
+    int fu = run.f0 + ((warp - (run.f0 & 3)) & 3);               // flat numbers congruent to the warp's
+    Feed<FMT, D, NG, BLKS, kWarps> feed;
+    feed.start(A, use, segs, fu, smem_u32(ring), bar_s);
+    int stage = 0, next_stage = 0, filled = 0;                   // stages that hold or await a step
     uint32_t phase = 0;
-    const float inv2 = A.softcap > 0.0f ? 2.0f / A.softcap : 0.0f;               // 2^(2 log2(e) x / cap), x in base 2
+    auto fill = [&]() {
+#pragma unroll 1
+        for (; filled < Q::STAGES && feed.left > 0; ++filled) {
+            feed.issue(A, segs, next_stage);
+            if (++next_stage == Q::STAGES) next_stage = 0;
+        }
+    };
+    bool fresh = true;                        // a segment (part) begins
+    int kvh, v0, nv, all_hi, all_lo, any_hi, any_lo, m_lo, m_hi;
+    uint32_t qf[KS][NT][2];
+    float cq[NT][2], start[NT][NGX][2], slope2[NT][2], o[TILES][NT][4], mref[NT][2], lsum[NT][2];
+    int own[NT][2];                           // row of the query itself; rows (own - window, own] are seen
+    const float inv2 = X && A.softcap > 0.0f ? 2.0f / A.softcap : 0.0f;          // 2^(2 log2(e) x / cap), x in base 2
     const float cap2 = A.softcap * kLog2e;
     for (;;) {
+        fill();
+        if (fresh) {
         // ================================================= a segment (part)
-        const int kvh = use.seg / A.QT, v0 = (use.seg % A.QT) * 8 * NT, nv = min(8 * NT, A.M * A.G - v0);
-        const int m_lo = v0 / A.G, m_hi = (v0 + nv - 1) / A.G;
+        fresh = false;
+        kvh = use.seg / A.QT;
+        v0 = (use.seg - kvh * A.QT) * 8 * NT;
+        nv = min(8 * NT, A.M * A.G - v0);
+        m_lo = row_of_vector(A, v0);
+        m_hi = row_of_vector(A, v0 + nv - 1);
         // ---- queries: fragments (column g of each tile), factors and limits of columns 2t, 2t + 1
-        uint32_t qf[NT == 4 ? 1 : KS][NT == 4 ? 1 : NT][2];
-        float cq[NT][2], start[NT][NGX][2], slope2[NT][2];
-        int own[NT][2];                       // row of the query itself; rows (own - window, own] are seen
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int v = v0 + 8 * nt + g;
             const bool valid = v < v0 + nv;
-            const int m = valid ? v / A.G : 0, hq = kvh * A.G + (valid ? v % A.G : 0);
+            const int m = valid ? row_of_vector(A, v) : 0, hq = kvh * A.G + (valid ? v - m * A.G : 0);
             const __nv_bfloat16 *qr = A.q + (static_cast<long long>(use.b) * A.M + m) * A.q_stride + hq * D;
             uint32_t fr[KS][2];
             float f = 1.0f;
@@ -455,39 +193,23 @@ attn_kernel(const __grid_constant__ Args A)
                 const float fc = FMT == kBf16 ? 1.0f : __shfl_sync(0xffffffffu, f, 4 * (2 * t + c));
                 // undo the codes' 2^-24 (and, for KV8, the 16) and the query's power of two
                 cq[nt][c] = A.scale * kLog2e * fc * (FMT == kBf16 ? 1.0f : FMT == kKv8 ? 1048576.0f : 16777216.0f);
-                own[nt][c] = use.s.hi - A.M + vc / A.G;
-                slope2[nt][c] = A.slopes ? A.slopes[kvh * A.G + vc % A.G] * kLog2e : 0.0f;
+                const int mc = row_of_vector(A, vc);
+                own[nt][c] = use.s.hi - A.M + mc;
+                slope2[nt][c] = X && A.slopes ? A.slopes[kvh * A.G + vc - mc * A.G] * kLog2e : 0.0f;
             }
-            if constexpr (NT == 4) {
-                if (warp == nt) {
 #pragma unroll
-                    for (int k = 0; k < KS; ++k) qf_s[(k * NT + nt) * 32 + lane] = make_uint2(fr[k][0], fr[k][1]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    qf[k][nt][0] = fr[k][0];
-                    qf[k][nt][1] = fr[k][1];
-                }
+            for (int k = 0; k < KS; ++k) {
+                qf[k][nt][0] = fr[k][0];
+                qf[k][nt][1] = fr[k][1];
             }
         }
-        if constexpr (NT == 4) __syncthreads();
-        auto qfrag = [&](int k, int nt, uint32_t &b0, uint32_t &b1) {
-            if constexpr (NT == 4) {
-                const uint2 r = qf_s[(k * NT + nt) * 32 + lane];
-                b0 = r.x;
-                b1 = r.y;
-            } else {
-                b0 = qf[k][nt][0];
-                b1 = qf[k][nt][1];
-            }
-        };
         // rows that every query of the tile sees: no mask needed there
-        const int all_hi = use.s.hi - A.M + m_lo + 1, all_lo = A.window > 0 ? use.s.hi - A.M + m_hi - A.window + 1 : 0;
+        all_hi = use.s.hi - A.M + m_lo + 1;
+        all_lo = A.window > 0 ? use.s.hi - A.M + m_hi - A.window + 1 : 0;
         // rows that any of them sees
-        const int any_hi = use.s.hi - A.M + m_hi + 1, any_lo = A.window > 0 ? use.s.hi - A.M + m_lo - A.window + 1 : 0;
+        any_hi = use.s.hi - A.M + m_hi + 1;
+        any_lo = A.window > 0 ? use.s.hi - A.M + m_lo - A.window + 1 : 0;
 
-        float o[TILES][NT][4], mref[NT][2], lsum[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -495,45 +217,73 @@ attn_kernel(const __grid_constant__ Args A)
             mref[nt][0] = mref[nt][1] = -INFINITY;
             lsum[nt][0] = lsum[nt][1] = 0.0f;
         }
+        }
 
-        // ================================================= its steps
-        for (; fu < use.end; fu += kWarps) {
+        // ================================================= the warp's next step of it
+        if (fu < use.end) {
             mbar_wait(bar_s + 8 * stage, phase, &abort_flag, A.status);
             const int row0 = use.s.lo + (fu - use.base) * SR;
             const unsigned char *sp = ring + stage * Q::STAGE;
-            auto blocks = [&](auto mask_c, int j0) {
-                constexpr bool MASK = decltype(mask_c)::value;
+            const bool masked = row0 < all_lo || row0 + SR > all_hi;
+#pragma unroll
+            for (int j0 = 0; j0 < BLKS; j0 += JB) {
+                if (row0 + 16 * j0 >= any_hi) break;             // not copied, or seen by no query
+                // ---- scales of the rows g, g + 8 of each block; log2 of V's
+                float sk[JB][2][NGX], sv[JB][2][NGX], lv[JB][2];
+                if constexpr (FMT != kBf16) {
+#pragma unroll
+                    for (int j = 0; j < JB; ++j) {
+                        const __half *sc = reinterpret_cast<const __half *>(sp + (j0 + j) * Q::BASE + 32 * RB);
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            const int r = g + 8 * rr;
+#pragma unroll
+                            for (int gr = 0; gr < NGX; ++gr) {
+                                sk[j][rr][gr] = __half2float(sc[r * NG + gr]);
+                                sv[j][rr][gr] = __half2float(sc[16 * NG + r * NG + gr]);
+                            }
+                        }
+                    }
+                    if (masked) {                                // a row that no query sees may hold anything
+#pragma unroll
+                        for (int j = 0; j < JB; ++j)
+#pragma unroll
+                            for (int rr = 0; rr < 2; ++rr) {
+                                const int key = row0 + 16 * (j0 + j) + g + 8 * rr;
+#pragma unroll
+                                for (int gr = 0; gr < NGX; ++gr)
+                                    if (key < any_lo || key >= any_hi) sk[j][rr][gr] = sv[j][rr][gr] = 0.0f;
+                            }
+                    }
+#pragma unroll
+                    for (int j = 0; j < JB; ++j)
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr)           // a scale of 0 has codes of 0
+                            lv[j][rr] = lg2(fmaxf(NGX == 2 ? fmaxf(sv[j][rr][0], sv[j][rr][NGX - 1]) : sv[j][rr][0], 3.7252902984619140625e-09f));
+                }
                 // ---- S^T
                 float acc[JB][NT][NACC][4];
 #pragma unroll
-                for (int j = 0; j < JB; ++j)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int h = 0; h < NACC; ++h)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[j][nt][h][e] = FMT != kBf16 && (NG == 2 || h == 0) ? start[nt][NG == 2 ? h : 0][e & 1] : 0.0f;
-#pragma unroll
                 for (int j = 0; j < JB; ++j) {
-                    const unsigned char *bp = sp + (j0 + j) * (Q::BASE + Q::RESID);
                     if constexpr (FMT == kBf16) {
+                        const unsigned char *bp = sp + (j0 + j) * Q::BASE;
                         const int r = (lane & 7) + 8 * ((lane >> 3) & 1);
                         const uint32_t at = smem_u32(bp) + r * 2 * D;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
-                            uint32_t a0, a1, a2, a3, b0, b1;
+                            uint32_t a0, a1, a2, a3;
                             asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                                          : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3)
                                          : "r"(at + (((2 * k + (lane >> 4)) ^ (r & 7)) << 4)) : "memory");
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                qfrag(k, nt, b0, b1);
-                                mma<FMT>(acc[j][nt][0], a0, a1, a2, a3, b0, b1);
+                                if (k == 0) mma_from<FMT>(acc[j][nt][0], a0, a1, a2, a3, qf[k][nt][0], qf[k][nt][1], 0.0f, 0.0f);
+                                else mma<FMT>(acc[j][nt][0], a0, a1, a2, a3, qf[k][nt][0], qf[k][nt][1]);
                             }
                         }
                     } else {
                         constexpr int NW = D / 32;
+                        const unsigned char *bp = sp + (j0 + j) * Q::BASE, *rp = sp + BLKS * Q::BASE + (j0 + j) * Q::RESID;
                         uint32_t kb[2][NW], kr[2][NW];
 #pragma unroll
                         for (int rr = 0; rr < 2; ++rr) {
@@ -542,7 +292,7 @@ attn_kernel(const __grid_constant__ Args A)
                                 const uint4 x = *reinterpret_cast<const uint4 *>(bp + nib_off(RB, r, 16 * t));
                                 kb[rr][0] = x.x; kb[rr][1] = x.y; kb[rr][2] = x.z; kb[rr][3] = x.w;
                                 if constexpr (FMT == kKv8) {
-                                    const uint4 y = *reinterpret_cast<const uint4 *>(bp + Q::BASE + nib_off(RB, r, 16 * t));
+                                    const uint4 y = *reinterpret_cast<const uint4 *>(rp + nib_off(RB, r, 16 * t));
                                     kr[rr][0] = y.x; kr[rr][1] = y.y; kr[rr][2] = y.z; kr[rr][3] = y.w;
                                 }
                             } else {
@@ -551,7 +301,7 @@ attn_kernel(const __grid_constant__ Args A)
                                     const uint2 x = *reinterpret_cast<const uint2 *>(bp + nib_off(RB, r, 32 * h + 8 * t));
                                     kb[rr][2 * h] = x.x; kb[rr][2 * h + 1] = x.y;
                                     if constexpr (FMT == kKv8) {
-                                        const uint2 y = *reinterpret_cast<const uint2 *>(bp + Q::BASE + nib_off(RB, r, 32 * h + 8 * t));
+                                        const uint2 y = *reinterpret_cast<const uint2 *>(rp + nib_off(RB, r, 32 * h + 8 * t));
                                         kr[rr][2 * h] = y.x; kr[rr][2 * h + 1] = y.y;
                                     }
                                 }
@@ -564,35 +314,23 @@ attn_kernel(const __grid_constant__ Args A)
 #pragma unroll
                         for (int w = 0; w < NW; ++w) {
                             const Codes<FMT> c0(kb[0][w], kr[0][w]), c1(kb[1][w], kr[1][w]);
+                            constexpr int per_acc = NW / NACC;
+                            const int h = w / per_acc;           // the accumulator; its first products start from the offset's
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
                                 const uint32_t a0 = c0.pair(2 * s), a1 = c1.pair(2 * s), a2 = c0.pair(2 * s + 1), a3 = c1.pair(2 * s + 1);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
-                                    uint32_t b0, b1;
-                                    qfrag(2 * w + s, nt, b0, b1);
-                                    mma<FMT>(acc[j][nt][NACC == 2 ? w >> 1 : 0], a0, a1, a2, a3, b0, b1);
+                                    const uint32_t b0 = qf[2 * w + s][nt][0], b1 = qf[2 * w + s][nt][1];
+                                    if (w % per_acc == 0 && s == 0) {
+                                        const bool off = NG == 2 || h == 0;
+                                        mma_from<FMT>(acc[j][nt][h], a0, a1, a2, a3, b0, b1, off ? start[nt][NG == 2 ? h : 0][0] : 0.0f,
+                                                      off ? start[nt][NG == 2 ? h : 0][1] : 0.0f);
+                                    } else {
+                                        mma<FMT>(acc[j][nt][h], a0, a1, a2, a3, b0, b1);
+                                    }
                                 }
                             }
-                        }
-                    }
-                }
-                // ---- scales of the rows g, g + 8 of each block; log2 of V's
-                float sk[JB][2][NGX], sv[JB][2][NGX], lv[JB][2];
-                if constexpr (FMT != kBf16) {
-#pragma unroll
-                    for (int j = 0; j < JB; ++j) {
-                        const __half *sc = reinterpret_cast<const __half *>(sp + (j0 + j) * (Q::BASE + Q::RESID) + 32 * RB);
-#pragma unroll
-                        for (int rr = 0; rr < 2; ++rr) {
-                            float top = 0.0f;
-#pragma unroll
-                            for (int gr = 0; gr < NGX; ++gr) {
-                                sk[j][rr][gr] = __half2float(sc[(g + 8 * rr) * NG + gr]);
-                                sv[j][rr][gr] = __half2float(sc[16 * NG + (g + 8 * rr) * NG + gr]);
-                                top = fmaxf(top, sv[j][rr][gr]);
-                            }
-                            lv[j][rr] = lg2(fmaxf(top, 3.7252902984619140625e-09f));   // a scale of 0 has codes of 0
                         }
                     }
                 }
@@ -600,8 +338,8 @@ attn_kernel(const __grid_constant__ Args A)
                 uint32_t pb[JB][NT][NGX][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float s[JB][2][2];
-                    float top[2] = {-INFINITY, -INFINITY};
+                    // scores in base 2 (X), or what cq makes scores of; y: with the log2 of V's scale
+                    float s[JB][2][2], y[JB][2][2];
 #pragma unroll
                     for (int j = 0; j < JB; ++j)
 #pragma unroll
@@ -613,26 +351,38 @@ attn_kernel(const __grid_constant__ Args A)
                                 if constexpr (FMT == kBf16) x = acc[j][nt][0][e];
                                 else if constexpr (NG == 2) x = fmaf(sk[j][rr][1], acc[j][nt][1][e], sk[j][rr][0] * acc[j][nt][0][e]);
                                 else x = sk[j][rr][0] * (NACC == 2 ? acc[j][nt][0][e] + acc[j][nt][NACC - 1][e] : acc[j][nt][0][e]);
-                                x *= cq[nt][c];
-                                if (A.softcap > 0.0f) x = capped(x, cap2, inv2);
-                                const int key = row0 + 16 * (j0 + j) + g + 8 * rr;
-                                if (A.slopes) x = fmaf(slope2[nt][c], static_cast<float>(key - own[nt][c]), x);
-                                if constexpr (MASK)
-                                    if (key > own[nt][c] || (A.window > 0 && key <= own[nt][c] - A.window)) x = -INFINITY;
+                                if constexpr (X) {
+                                    x *= cq[nt][c];
+                                    if (A.softcap > 0.0f) x = capped(x, cap2, inv2);
+                                    const int key = row0 + 16 * (j0 + j) + g + 8 * rr;
+                                    if (A.slopes) x = fmaf(slope2[nt][c], static_cast<float>(key - own[nt][c]), x);
+                                }
                                 s[j][rr][c] = x;
-                                float y = x;
-                                if constexpr (FMT != kBf16) y = MASK && x == -INFINITY ? x : x + lv[j][rr];
-                                top[c] = fmaxf(top[c], y);
+                                y[j][rr][c] = FMT == kBf16 ? (X ? x : x * cq[nt][c]) : X ? x + lv[j][rr] : fmaf(x, cq[nt][c], lv[j][rr]);
                             }
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < JB; ++j)
+#pragma unroll
+                            for (int rr = 0; rr < 2; ++rr)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const int key = row0 + 16 * (j0 + j) + g + 8 * rr;
+                                    if (key > own[nt][c] || (A.window > 0 && key <= own[nt][c] - A.window)) s[j][rr][c] = y[j][rr][c] = -INFINITY;
+                                }
+                    }
                     float alpha[2];
                     bool grow = false;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        top[c] = col_max(top[c]);
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < JB; ++j) top = fmaxf(top, fmaxf(y[j][0][c], y[j][1][c]));
+                        top = col_max(top);
                         alpha[c] = 1.0f;
-                        if (top[c] > mref[nt][c] + kSlack) {
-                            alpha[c] = mref[nt][c] == -INFINITY ? 0.0f : ex2(mref[nt][c] - top[c]);
-                            mref[nt][c] = top[c];
+                        if (top > mref[nt][c] + kSlack) {
+                            alpha[c] = ex2(mref[nt][c] - top);   // 0 at the first rows
+                            mref[nt][c] = top;
                             grow = true;
                         }
                     }
@@ -652,7 +402,8 @@ attn_kernel(const __grid_constant__ Args A)
                     for (int j = 0; j < JB; ++j)
 #pragma unroll
                         for (int rr = 0; rr < 2; ++rr) {
-                            const float e0 = ex2(s[j][rr][0] - mr[0]), e1 = ex2(s[j][rr][1] - mr[1]);
+                            const float e0 = ex2(X ? s[j][rr][0] - mr[0] : fmaf(s[j][rr][0], cq[nt][0], -mr[0])),
+                                        e1 = ex2(X ? s[j][rr][1] - mr[1] : fmaf(s[j][rr][1], cq[nt][1], -mr[1]));
                             if constexpr (FMT == kBf16) {
                                 const uint32_t p = pack_b(e0, e1);
                                 lsum[nt][0] += __uint_as_float(p << 16);
@@ -662,25 +413,19 @@ attn_kernel(const __grid_constant__ Args A)
                                 lsum[nt][0] += e0;
                                 lsum[nt][1] += e1;
 #pragma unroll
-                                for (int gr = 0; gr < NGX; ++gr) {
-                                    float p0 = e0 * sv[j][rr][gr], p1 = e1 * sv[j][rr][gr];
-                                    if constexpr (MASK) {       // a masked row's scale may be anything
-                                        if (s[j][rr][0] == -INFINITY) p0 = 0.0f;
-                                        if (s[j][rr][1] == -INFINITY) p1 = 0.0f;
-                                    }
-                                    pb[j][nt][gr][rr] = transpose8(pack_h(p0, p1));
-                                }
+                                for (int gr = 0; gr < NGX; ++gr) pb[j][nt][gr][rr] = transpose8(pack_h(e0 * sv[j][rr][gr], e1 * sv[j][rr][gr]));
                             }
                         }
                 }
                 // ---- O^T
 #pragma unroll
                 for (int j = 0; j < JB; ++j) {
-                    const unsigned char *bp = sp + (j0 + j) * (Q::BASE + Q::RESID);
+                    const unsigned char *bp = sp + (j0 + j) * Q::BASE;
                     if constexpr (FMT == kBf16) {
                         const int r = (lane & 7) + 8 * (lane >> 4), blk0 = row0 + 16 * (j0 + j);
                         const uint32_t at = smem_u32(bp) + 32 * D + r * 2 * D;
-                        auto product = [&](uint32_t k0, uint32_t k1, int only) {   // V rows kept; one query row alone, or all
+                        auto product = [&](auto mask_c, uint32_t k0, uint32_t k1, int only) {   // V rows kept; one query row alone, or all
+                            constexpr bool MASK = decltype(mask_c)::value;
 #pragma unroll
                             for (int i = 0; i < TILES; ++i) {
                                 uint32_t a0, a1, a2, a3;
@@ -697,14 +442,14 @@ attn_kernel(const __grid_constant__ Args A)
                                         mma<FMT>(one, a0, a1, a2, a3, pb[j][nt][0][0], pb[j][nt][0][1]);
 #pragma unroll
                                         for (int e = 0; e < 4; ++e)
-                                            if ((v0 + 8 * nt + 2 * t + (e & 1)) / A.G == only) o[i][nt][e] += one[e];
+                                            if (row_of_vector(A, v0 + 8 * nt + 2 * t + (e & 1)) == only) o[i][nt][e] += one[e];
                                     } else {
                                         mma<FMT>(o[i][nt], a0, a1, a2, a3, pb[j][nt][0][0], pb[j][nt][0][1]);
                                     }
                                 }
                             }
                         };
-                        if constexpr (MASK) {
+                        if (masked) {
                             // P is 0 where a query does not see a row, but 0 times NaN or infinity is not:
                             // rows that no query sees (they may hold anything) leave V's fragments.  A
                             // non-finite row that only some queries see is rare; then query row by query row.
@@ -730,16 +475,17 @@ attn_kernel(const __grid_constant__ Args A)
                             if (__any_sync(0xffffffffu, bad)) {
                                 for (int m = m_lo; m <= m_hi; ++m) {
                                     const int hi = use.s.hi - A.M + m + 1, lo = A.window > 0 ? hi - A.window : 0;
-                                    product(kept(lo, hi, 0), kept(lo, hi, 1), m);
+                                    product(std::true_type{}, kept(lo, hi, 0), kept(lo, hi, 1), m);
                                 }
                             } else {
-                                product(kept(any_lo, any_hi, 0), kept(any_lo, any_hi, 1), -1);
+                                product(std::true_type{}, kept(any_lo, any_hi, 0), kept(any_lo, any_hi, 1), -1);
                             }
                         } else {
-                            product(0u, 0u, -1);
+                            product(std::false_type{}, 0u, 0u, -1);
                         }
                     } else {
                         constexpr int NW = D / 64;
+                        const unsigned char *rp = sp + BLKS * Q::BASE + (j0 + j) * Q::RESID;
                         uint32_t vb[4][NW], vr[4][NW];
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
@@ -748,7 +494,7 @@ attn_kernel(const __grid_constant__ Args A)
                                 const uint2 x = *reinterpret_cast<const uint2 *>(bp + 16 * RB + nib_off(RB, r, 8 * g));
                                 vb[kk][0] = x.x; vb[kk][1] = x.y;
                                 if constexpr (FMT == kKv8) {
-                                    const uint2 y = *reinterpret_cast<const uint2 *>(bp + Q::BASE + 16 * RB + nib_off(RB, r, 8 * g));
+                                    const uint2 y = *reinterpret_cast<const uint2 *>(rp + 16 * RB + nib_off(RB, r, 8 * g));
                                     vr[kk][0] = y.x; vr[kk][1] = y.y;
                                 }
                             } else {
@@ -756,7 +502,7 @@ attn_kernel(const __grid_constant__ Args A)
                                 for (int h = 0; h < NW; ++h) {
                                     vb[kk][h] = *reinterpret_cast<const uint32_t *>(bp + 16 * RB + nib_off(RB, r, 32 * h + 4 * g));
                                     if constexpr (FMT == kKv8)
-                                        vr[kk][h] = *reinterpret_cast<const uint32_t *>(bp + Q::BASE + 16 * RB + nib_off(RB, r, 32 * h + 4 * g));
+                                        vr[kk][h] = *reinterpret_cast<const uint32_t *>(rp + 16 * RB + nib_off(RB, r, 32 * h + 4 * g));
                                 }
                             }
                             if constexpr (FMT != kKv8) {
@@ -781,22 +527,17 @@ attn_kernel(const __grid_constant__ Args A)
                         }
                     }
                 }
-            };
-#pragma unroll
-            for (int j0 = 0; j0 < BLKS; j0 += JB) {
-                const int a = row0 + 16 * j0;
-                if (a >= any_hi) break;                          // not copied, or seen by no query
-                if (a >= all_lo && a + 16 * JB <= all_hi) blocks(std::false_type{}, j0);
-                else blocks(std::true_type{}, j0);
             }
             // the stage was read through the generic proxy, the next copy writes through the async one
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            issue(stage);
+            --filled;
+            fu += kWarps;
             if (++stage == Q::STAGES) {
                 stage = 0;
                 phase ^= 1u;
             }
+            if (fu < use.end) continue;
         }
 
         // ================================================= the segment's end: the warps merge
@@ -844,18 +585,18 @@ attn_kernel(const __grid_constant__ Args A)
                         o[i][nt][e] = o[i][nt][e] * fa[e & 1] + d[((i * NT + nt) * 4 + e) * 32] * fb[e & 1];
             }
         };
-        __syncthreads();                      // warp 0 is done with the buffers of the segment before
-        if (warp >= 2) put(warp - 2);
-        __syncthreads();
-        if (warp < 2) take(warp);
-        __syncthreads();
-        if (warp == 1) put(0);
-        __syncthreads();
+        // warps 2, 3 to 0, 1, then 1 to 0; the first barrier also frees the buffers of the segment before
+#pragma unroll 1
+        for (int half = 2; half > 0; half >>= 1) {
+            __syncthreads();
+            if (warp >= half && warp < 2 * half) put(warp - half);
+            __syncthreads();
+            if (warp < half) take(warp);
+        }
         if (warp == 0) {
-            take(0);
-            const bool starts = use.base >= f0, ends = use.base + use.s.steps <= f1, whole = starts && ends;
+            const bool starts = use.base >= run.f0, ends = use.base + use.s.steps <= run.f1, whole = starts && ends;
             if (!ends && starts && lane == 0)
-                A.info[blockIdx.x] = make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / per, 0);
+                A.info[blockIdx.x] = make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / run.per, 0);
             const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0);
             constexpr float unit = FMT == kKv8 ? 0.0625f : 1.0f;                 // KV8's codes are 16 times the value
 #pragma unroll
@@ -865,8 +606,8 @@ attn_kernel(const __grid_constant__ Args A)
                     const int col = 8 * nt + 2 * t + c;
                     if (col >= nv) continue;
                     const float f = unit * (!whole ? 1.0f : lsum[nt][c] == 0.0f ? 0.0f : 1.0f / lsum[nt][c]);
-                    const int v = v0 + col;
-                    __nv_bfloat16 *to = A.out + ((static_cast<size_t>(use.b) * A.M + v / A.G) * A.Hq + kvh * A.G + v % A.G) * D;
+                    const int v = v0 + col, m = row_of_vector(A, v);
+                    __nv_bfloat16 *to = A.out + ((static_cast<size_t>(use.b) * A.M + m) * A.Hq + kvh * A.G + v - m * A.G) * D;
                     float *po = A.part_o + (slot * 8 * NT + col) * D;
                     if (!whole && g == 0) {
                         A.part_ml[(slot * 8 * NT + col) * 2] = mref[nt][c];
@@ -904,10 +645,11 @@ attn_kernel(const __grid_constant__ Args A)
         }
         if (use.end >= use.stop) {
             // the run ends with its last segment, or inside one that an earlier run began
-            if (threadIdx.x == 0 && (use.base + use.s.steps <= f1 || use.base < f0)) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            if (threadIdx.x == 0 && (use.base + use.s.steps <= run.f1 || use.base < run.f0)) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
             break;
         }
         use.next(A, segs);
+        fresh = true;
     }
 }
 
@@ -916,11 +658,11 @@ attn_kernel(const __grid_constant__ Args A)
 // end (if there is one): out = sum_r 2^(m_r - M) o_r / sum_r 2^(m_r - M) l_r
 // over the runs' partial states, eight warps taking every eighth.
 template <int D, int NV>
-__global__ void __launch_bounds__(kCombWarps * 32)
-join_kernel(const __grid_constant__ Args A)
+__global__ void __launch_bounds__(kJoinWarps * 32)
+join_kernel(const __grid_constant__ AttnArgs A)
 {
     constexpr int E = D / 32;
-    __shared__ float sm_m[kCombWarps], sm_l[kCombWarps], sm_o[kCombWarps][D];
+    __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps], sm_o[kJoinWarps][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 in = A.info[blockIdx.x];
     if (in.x < 0) return;
@@ -929,11 +671,11 @@ join_kernel(const __grid_constant__ Args A)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x, n = in.z - first + 1;
     float m = -INFINITY, l = 0.0f, o[E] = {};
     constexpr int U = 4;
-    for (int r0 = warp; r0 < n; r0 += kCombWarps * U) {
+    for (int r0 = warp; r0 < n; r0 += kJoinWarps * U) {
         float mm[U], ll[U], oo[U][E];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * kCombWarps;
+            const int r = r0 + u * kJoinWarps;
             mm[u] = -INFINITY;
             ll[u] = 0.0f;
 #pragma unroll
@@ -966,23 +708,24 @@ join_kernel(const __grid_constant__ Args A)
     if (threadIdx.x >= D / 2) return;
     float M2 = -INFINITY, x0 = 0.0f, x1 = 0.0f, den = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kCombWarps; ++w) M2 = fmaxf(M2, sm_m[w]);
+    for (int w = 0; w < kJoinWarps; ++w) M2 = fmaxf(M2, sm_m[w]);
     if (M2 == -INFINITY) M2 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kCombWarps; ++w) {
+    for (int w = 0; w < kJoinWarps; ++w) {
         const float f = ex2(sm_m[w] - M2);
         x0 = fmaf(f, sm_o[w][2 * threadIdx.x], x0);
         x1 = fmaf(f, sm_o[w][2 * threadIdx.x + 1], x1);
         den = fmaf(f, sm_l[w], den);
     }
     const float f = den == 0.0f ? 0.0f : 1.0f / den;
-    const size_t row = (static_cast<size_t>(in.x) * A.M + v / A.G) * A.Hq + kvh * A.G + v % A.G;
+    const int mv = row_of_vector(A, v);
+    const size_t row = (static_cast<size_t>(in.x) * A.M + mv) * A.Hq + kvh * A.G + v - mv * A.G;
     reinterpret_cast<uint32_t *>(A.out + row * D)[threadIdx.x] = pack_b(x0 * f, x1 * f);
 }
 
 // ---------------------------------------------------------------- host side
-template <int FMT, int D, int NG, int NT>
-cudaError_t launch(Args A, cudaStream_t s)
+template <int FMT, int D, int NG, int NT, bool X>
+cudaError_t launch(AttnArgs A, cudaStream_t s)
 {
     using Q = Geo<FMT, D, NG, NT>;
     static std::atomic<bool> done[64];          // per device
@@ -991,12 +734,12 @@ cudaError_t launch(Args A, cudaStream_t s)
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev].load()) {
-        e = cudaFuncSetAttribute(attn_kernel<FMT, D, NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::SMEM);
+        e = cudaFuncSetAttribute(attn_kernel<FMT, D, NG, NT, X>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::SMEM);
         if (e != cudaSuccess) return e;
         done[dev].store(true);
     }
     const int grid = sm_count() * Q::CTAS;
-    attn_kernel<FMT, D, NG, NT><<<grid, kThreads, Q::SMEM, s>>>(A);
+    attn_kernel<FMT, D, NG, NT, X><<<grid, kThreads, Q::SMEM, s>>>(A);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int nv = A.M * A.G < 8 * NT ? A.M * A.G : 8 * NT;
@@ -1005,19 +748,20 @@ cudaError_t launch(Args A, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, nv);
-    cfg.blockDim = dim3(kCombWarps * 32);
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, join_kernel<D, 8 * NT>, A);
 }
 template <int FMT, int D, int NG>
-cudaError_t launch_nt(int nt, const Args &A, cudaStream_t s)
+cudaError_t launch_nt(int nt, const AttnArgs &A, cudaStream_t s)
 {
-    return nt == 1 ? launch<FMT, D, NG, 1>(A, s) : nt == 2 ? launch<FMT, D, NG, 2>(A, s) : launch<FMT, D, NG, 4>(A, s);
+    if (A.softcap > 0.0f || A.slopes) return nt == 1 ? launch<FMT, D, NG, 1, true>(A, s) : launch<FMT, D, NG, 2, true>(A, s);
+    return nt == 1 ? launch<FMT, D, NG, 1, false>(A, s) : launch<FMT, D, NG, 2, false>(A, s);
 }
 template <int FMT>
-cudaError_t launch_d(int nt, const Args &A, cudaStream_t s)
+cudaError_t launch_d(int nt, const AttnArgs &A, cudaStream_t s)
 {
     if (A.p.D == 64) return launch_nt<FMT, 64, 1>(nt, A, s);
     if constexpr (FMT != kBf16)
@@ -1027,8 +771,8 @@ cudaError_t launch_d(int nt, const Args &A, cudaStream_t s)
 
 // Query vectors per tile: the fewest tiles of 8 that hold them, at most four
 // (the accumulators of more do not fit the registers).
-int tiles_of(int vectors) { return vectors <= 8 ? 1 : vectors <= 16 ? 2 : 4; }
-constexpr int kMaxCtas = 3;
+int tiles_of(int vectors) { return vectors <= 8 ? 1 : 2; }
+constexpr int kMaxCtas = 4;
 
 // Workspace: info, then partial states for two segments per CTA.
 struct Ws {
@@ -1060,7 +804,7 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
                                   const int32_t *len, int planes, const nq_attn_opts *opts, uint16_t *out, void *ws,
                                   size_t ws_bytes, cudaStream_t stream)
 {
-    nq::Args A{};
+    nq::AttnArgs A{};
     const nq_status st = nq::pool_map_of(pool, map, A.p, A.m, false);
     if (st != NQ_OK) return st;
     const nq::Pool &p = A.p;
@@ -1084,6 +828,7 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
     A.M = M;
     A.Hq = heads_q;
     A.G = G;
+    A.g_mul = static_cast<unsigned>((0x100000000ull + G - 1) / G);
     const int nt = nq::tiles_of(M * G);
     A.QT = (M * G + 8 * nt - 1) / (8 * nt);
     // the kernel numbers the steps of all segments in 32 bits

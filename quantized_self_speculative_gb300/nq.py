@@ -156,9 +156,17 @@ def _check(status: int, what: str):
         raise NQError(status, what)
 
 
+# the current stream's handle without a Stream object around it (3 us less per call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or _raw_device is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_raw_device())
 
 
 def _dev(t: torch.Tensor, dtype, what: str) -> int:
@@ -491,13 +499,15 @@ _DT = {torch.float32: 0, torch.bfloat16: 1}
 
 def _heads(t: torch.Tensor, T: int, H: int, D: int, dtype, what: str) -> int:
     """Address of the heads of T tokens [T][H][D], each token's contiguous."""
-    if not t.is_cuda or t.dtype != dtype or t.shape != (T, H, D) or t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    st = t.stride()
+    if not t.is_cuda or t.dtype is not dtype or t.shape != (T, H, D) or st[2] != 1 or (st[1] != D and H > 1):
         raise ValueError(f"{what} must be a CUDA tensor of {dtype}, shape {(T, H, D)}, contiguous within a token")
     return t.data_ptr()
 
 
 def _token_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    T, H, D = t.shape
+    return t.stride(0) if T > 1 else H * D
 
 
 class Rope:
@@ -567,12 +577,15 @@ class PageMap:
         p = lambda t, what: None if t is None else _dev(t, torch.int32, what)  # noqa: E731
         self.struct = nq_page_map(max_seqs, max_pages, n_pages, page_size, p(table, "table"), p(held, "held"), p(ref, "ref"))
         self.ptr = C.byref(self.struct)
+        self._ws_bytes = {}              # workspace size by the number of sequences
         if fresh:
             _check(lib().nq_page_map_init(self.ptr, _stream(stream)), "nq_page_map_init")
 
     def workspace(self, n: int) -> torch.Tensor:
-        need = lib().nq_page_workspace_bytes(self.ptr, n)
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=self.table.device)
+        need = self._ws_bytes.get(n)
+        if need is None:
+            need = self._ws_bytes[n] = max(lib().nq_page_workspace_bytes(self.ptr, n), 16)
+        return torch.empty(need, dtype=torch.uint8, device=self.table.device)
 
     @staticmethod
     def _list(t: torch.Tensor, n: int, what: str) -> int:
@@ -633,6 +646,7 @@ class PagePool:
         self.struct = nq_page_pool(layers, n_pages, page_size, heads_kv, head_dim, group, fmt, 0,
                                    _dev(data, torch.uint8, "data"))
         self.ptr = C.byref(self.struct)
+        self._attn_bytes = {}            # workspace size by (M, heads_q)
 
     def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Copy pages src[i] to dst[i] in every layer."""
@@ -697,10 +711,13 @@ class PagePool:
             raise ValueError("q must have the pool's head_dim")
         if slopes is not None and slopes.shape != (Hq,):
             raise ValueError("slopes must be fp32 [heads_q]")
-        out = out if out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if out is None:
+            out = torch.empty_like(q)
         if ws is None:
-            ws = torch.empty(max(lib().nq_page_attn_workspace_bytes(M, Hq, self.heads_kv, D), 16), dtype=torch.uint8,
-                             device=q.device)
+            need = self._attn_bytes.get((M, Hq))
+            if need is None:
+                need = self._attn_bytes[M, Hq] = max(lib().nq_page_attn_workspace_bytes(M, Hq, self.heads_kv, D), 16)
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         o = nq_attn_opts(float(scale), float(softcap), int(window), 0,
                          None if slopes is None else _dev(slopes, torch.float32, "slopes"))
         _check(lib().nq_page_attn(self.ptr, layer, pmap.ptr, _dev(q, torch.bfloat16, "q"), Hq * D, B, M, Hq,
