@@ -52,11 +52,11 @@ struct Geo {
     static constexpr int SR = 16 * BLKS;
     static constexpr int STAGE = BLKS * (BASE + RESID);
     // CTAs per SM and stages: as much in flight as shared memory holds beside
-    // the merge buffers, three CTAs where two stages fit
+    // the merge buffers, three CTAs where registers and two stages fit
     static constexpr int MERGE = D * NT / 4 * 128;                          // accumulators of one warp
     static constexpr int FIX = 2 * MERGE + 2 * 8 * NT * 8;
     static constexpr int fit(int ctas) { return (233472 / ctas - 1024 - 512 - FIX) / (kWarps * STAGE); }
-    static constexpr int CTAS = fit(3) < 2 ? 2 : 3;
+    static constexpr int CTAS = NT == 2 || fit(3) < 2 ? 2 : 3;
     static constexpr int STAGES = fit(CTAS) > 6 ? 6 : fit(CTAS);
     static constexpr int RING = kWarps * STAGES * STAGE;
     static constexpr int SMEM = RING + FIX;
@@ -113,10 +113,11 @@ attn_kernel(const __grid_constant__ AttnArgs A)
     bool fresh = true;                        // a segment (part) begins
     int kvh, v0, nv, all_hi, all_lo, any_hi, any_lo, m_lo, m_hi;
     uint32_t qf[KS][NT][2];
-    float cq[NT][2], start[NT][NGX][2], slope2[NT][2], o[TILES][NT][4], mref[NT][2], lsum[NT][2];
+    float cq[NT][2], start[NT][NGX][2], slope2[NT][2], o[TILES][NT][4], mref[NT][2], mz[NT][2], lsum[NT][2];   // mz: mref, 0 for -infinity
     int own[NT][2];                           // row of the query itself; rows (own - window, own] are seen
     const float inv2 = X && A.softcap > 0.0f ? 2.0f / A.softcap : 0.0f;          // 2^(2 log2(e) x / cap), x in base 2
     const float cap2 = A.softcap * kLog2e;
+    const unsigned window = A.window > 0 ? A.window : 0x7fffffffu;
     for (;;) {
         fill();
         if (fresh) {
@@ -215,6 +216,7 @@ attn_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
             for (int i = 0; i < TILES; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
             mref[nt][0] = mref[nt][1] = -INFINITY;
+            mz[nt][0] = mz[nt][1] = 0.0f;
             lsum[nt][0] = lsum[nt][1] = 0.0f;
         }
         }
@@ -249,10 +251,12 @@ attn_kernel(const __grid_constant__ AttnArgs A)
                         for (int j = 0; j < JB; ++j)
 #pragma unroll
                             for (int rr = 0; rr < 2; ++rr) {
-                                const int key = row0 + 16 * (j0 + j) + g + 8 * rr;
+                                const bool none = static_cast<unsigned>(row0 + 16 * (j0 + j) + g + 8 * rr - any_lo) >= static_cast<unsigned>(any_hi - any_lo);
 #pragma unroll
-                                for (int gr = 0; gr < NGX; ++gr)
-                                    if (key < any_lo || key >= any_hi) sk[j][rr][gr] = sv[j][rr][gr] = 0.0f;
+                                for (int gr = 0; gr < NGX; ++gr) {
+                                    sk[j][rr][gr] = none ? 0.0f : sk[j][rr][gr];
+                                    sv[j][rr][gr] = none ? 0.0f : sv[j][rr][gr];
+                                }
                             }
                     }
 #pragma unroll
@@ -367,43 +371,41 @@ attn_kernel(const __grid_constant__ AttnArgs A)
                             for (int rr = 0; rr < 2; ++rr)
 #pragma unroll
                                 for (int c = 0; c < 2; ++c) {
-                                    const int key = row0 + 16 * (j0 + j) + g + 8 * rr;
-                                    if (key > own[nt][c] || (A.window > 0 && key <= own[nt][c] - A.window)) s[j][rr][c] = y[j][rr][c] = -INFINITY;
+                                    // before the window, or (negative) after the query's own row
+                                    const bool hidden = static_cast<unsigned>(own[nt][c] - (row0 + 16 * (j0 + j) + g + 8 * rr)) >= window;
+                                    s[j][rr][c] = hidden ? -INFINITY : s[j][rr][c];
+                                    y[j][rr][c] = hidden ? -INFINITY : y[j][rr][c];
                                 }
                     }
-                    float alpha[2];
-                    bool grow = false;
+                    float top[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float top = -INFINITY;
+                        top[c] = fmaxf(y[0][0][c], y[0][1][c]);
 #pragma unroll
-                        for (int j = 0; j < JB; ++j) top = fmaxf(top, fmaxf(y[j][0][c], y[j][1][c]));
-                        top = col_max(top);
-                        alpha[c] = 1.0f;
-                        if (top > mref[nt][c] + kSlack) {
-                            alpha[c] = ex2(mref[nt][c] - top);   // 0 at the first rows
-                            mref[nt][c] = top;
-                            grow = true;
-                        }
+                        for (int j = 1; j < JB; ++j) top[c] = fmaxf(top[c], fmaxf(y[j][0][c], y[j][1][c]));
+                        top[c] = col_max(top[c]);
                     }
-                    if (__any_sync(0xffffffffu, grow)) {
+                    if (__any_sync(0xffffffffu, top[0] > mref[nt][0] + kSlack || top[1] > mref[nt][1] + kSlack)) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            lsum[nt][c] *= alpha[c];
+                            const float mn = top[c] > mref[nt][c] + kSlack ? top[c] : mref[nt][c];
+                            const float alpha = ex2(mref[nt][c] == -INFINITY ? -INFINITY : mref[nt][c] - mn);   // nothing yet: 0
+                            mref[nt][c] = mn;
+                            mz[nt][c] = mn == -INFINITY ? 0.0f : mn;
+                            lsum[nt][c] *= alpha;
 #pragma unroll
                             for (int i = 0; i < TILES; ++i) {
-                                o[i][nt][c] *= alpha[c];
-                                o[i][nt][2 + c] *= alpha[c];
+                                o[i][nt][c] *= alpha;
+                                o[i][nt][2 + c] *= alpha;
                             }
                         }
                     }
-                    const float mr[2] = {mref[nt][0] == -INFINITY ? 0.0f : mref[nt][0], mref[nt][1] == -INFINITY ? 0.0f : mref[nt][1]};
 #pragma unroll
                     for (int j = 0; j < JB; ++j)
 #pragma unroll
                         for (int rr = 0; rr < 2; ++rr) {
-                            const float e0 = ex2(X ? s[j][rr][0] - mr[0] : fmaf(s[j][rr][0], cq[nt][0], -mr[0])),
-                                        e1 = ex2(X ? s[j][rr][1] - mr[1] : fmaf(s[j][rr][1], cq[nt][1], -mr[1]));
+                            const float e0 = ex2(X ? s[j][rr][0] - mz[nt][0] : fmaf(s[j][rr][0], cq[nt][0], -mz[nt][0])),
+                                        e1 = ex2(X ? s[j][rr][1] - mz[nt][1] : fmaf(s[j][rr][1], cq[nt][1], -mz[nt][1]));
                             if constexpr (FMT == kBf16) {
                                 const uint32_t p = pack_b(e0, e1);
                                 lsum[nt][0] += __uint_as_float(p << 16);
@@ -725,7 +727,7 @@ join_kernel(const __grid_constant__ AttnArgs A)
 
 // ---------------------------------------------------------------- host side
 template <int FMT, int D, int NG, int NT, bool X>
-cudaError_t launch(AttnArgs A, cudaStream_t s)
+cudaError_t launch(const AttnArgs &A, cudaStream_t s, int *grid)
 {
     using Q = Geo<FMT, D, NG, NT>;
     static std::atomic<bool> done[64];          // per device
@@ -738,51 +740,60 @@ cudaError_t launch(AttnArgs A, cudaStream_t s)
         if (e != cudaSuccess) return e;
         done[dev].store(true);
     }
-    const int grid = sm_count() * Q::CTAS;
-    attn_kernel<FMT, D, NG, NT, X><<<grid, kThreads, Q::SMEM, s>>>(A);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const int nv = A.M * A.G < 8 * NT ? A.M * A.G : 8 * NT;
+    *grid = sm_count() * Q::CTAS;
+    attn_kernel<FMT, D, NG, NT, X><<<*grid, kThreads, Q::SMEM, s>>>(A);
+    return cudaGetLastError();
+}
+template <int FMT, int D, int NG>
+cudaError_t launch_x(int nt, const AttnArgs &A, cudaStream_t s, int *grid)
+{
+    if (A.softcap > 0.0f || A.slopes) return nt == 1 ? launch<FMT, D, NG, 1, true>(A, s, grid) : launch<FMT, D, NG, 2, true>(A, s, grid);
+    return nt == 1 ? launch<FMT, D, NG, 1, false>(A, s, grid) : launch<FMT, D, NG, 2, false>(A, s, grid);
+}
+template <int FMT>
+cudaError_t launch_d(int nt, const AttnArgs &A, cudaStream_t s, int *grid)
+{
+    if (A.p.D == 64) return launch_x<FMT, 64, 1>(nt, A, s, grid);
+    if constexpr (FMT != kBf16)
+        if (A.p.NG == 2) return launch_x<FMT, 128, 2>(nt, A, s, grid);
+    return launch_x<FMT, 128, 1>(nt, A, s, grid);
+}
+
+template <int D, int NV>
+cudaError_t launch_join(const AttnArgs &A, int grid, cudaStream_t s)
+{
+    // a programmatic dependent launch: it overlaps the end of the kernel before it
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, nv);
+    cfg.gridDim = dim3(grid, A.M * A.G < NV ? A.M * A.G : NV);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, 8 * NT>, A);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, NV>, A);
 }
-template <int FMT, int D, int NG>
-cudaError_t launch_nt(int nt, const AttnArgs &A, cudaStream_t s)
+template <int D>
+cudaError_t join(int cols, const AttnArgs &A, int grid, cudaStream_t s)
 {
-    if (A.softcap > 0.0f || A.slopes) return nt == 1 ? launch<FMT, D, NG, 1, true>(A, s) : launch<FMT, D, NG, 2, true>(A, s);
-    return nt == 1 ? launch<FMT, D, NG, 1, false>(A, s) : launch<FMT, D, NG, 2, false>(A, s);
-}
-template <int FMT>
-cudaError_t launch_d(int nt, const AttnArgs &A, cudaStream_t s)
-{
-    if (A.p.D == 64) return launch_nt<FMT, 64, 1>(nt, A, s);
-    if constexpr (FMT != kBf16)
-        if (A.p.NG == 2) return launch_nt<FMT, 128, 2>(nt, A, s);
-    return launch_nt<FMT, 128, 1>(nt, A, s);
+    return cols == 8 ? launch_join<D, 8>(A, grid, s) : cols == 16 ? launch_join<D, 16>(A, grid, s)
+         : cols == 32 ? launch_join<D, 32>(A, grid, s) : launch_join<D, 64>(A, grid, s);
 }
 
-// Query vectors per tile: the fewest tiles of 8 that hold them, at most four
-// (the accumulators of more do not fit the registers).
-int tiles_of(int vectors) { return vectors <= 8 ? 1 : 2; }
+// Query vectors per tile: the fewest columns that hold them.  Up to 16 a warp
+// holds them all and decodes for itself; more share a CTA's decoded steps.
+int cols_of(int vectors) { return vectors <= 8 ? 8 : vectors <= 16 ? 16 : vectors <= 32 ? 32 : 64; }
 constexpr int kMaxCtas = 4;
 
-// Workspace: info, then partial states for two segments per CTA.
+// Workspace: info, then partial states of two segments per CTA.
 struct Ws {
-    size_t info, ml, o, total;
+    size_t ml, o, total;
 };
 Ws ws_of(int vectors, int D)
 {
-    const size_t ctas = static_cast<size_t>(kMaxCtas) * sm_count(), cols = 2 * ctas * 8 * tiles_of(vectors);
+    const size_t ctas = static_cast<size_t>(kMaxCtas) * sm_count(), cols = 2 * ctas * cols_of(vectors);
     Ws w;
-    w.info = 0;
     w.ml = ctas * sizeof(int4);
     w.o = w.ml + cols * 8;
     w.total = w.o + cols * D * 4;
@@ -829,8 +840,8 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
     A.Hq = heads_q;
     A.G = G;
     A.g_mul = static_cast<unsigned>((0x100000000ull + G - 1) / G);
-    const int nt = nq::tiles_of(M * G);
-    A.QT = (M * G + 8 * nt - 1) / (8 * nt);
+    const int cols = nq::cols_of(M * G);
+    A.QT = (M * G + cols - 1) / cols;
     // the kernel numbers the steps of all segments in 32 bits
     if (static_cast<double>(batch) * p.H * A.QT * (static_cast<double>(A.m.W) * A.m.P / 16 + 2) > 2.0e9) return NQ_ERR_SHAPE;
     A.seqs = seqs;
@@ -841,10 +852,16 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
     A.slopes = opts->slopes;
     A.out = reinterpret_cast<__nv_bfloat16 *>(out);
     uint8_t *wb = static_cast<uint8_t *>(ws);
-    A.info = reinterpret_cast<int4 *>(wb + w.info);
+    A.info = reinterpret_cast<int4 *>(wb);
     A.part_ml = reinterpret_cast<float *>(wb + w.ml);
     A.part_o = reinterpret_cast<float *>(wb + w.o);
-    const cudaError_t e = p.NG == 0 ? nq::launch_d<nq::kBf16>(nt, A, stream)
-                          : planes == 1 ? nq::launch_d<nq::kKv4>(nt, A, stream) : nq::launch_d<nq::kKv8>(nt, A, stream);
-    return nq::cuda_status(e);
+    const int fmt = p.NG == 0 ? nq::kBf16 : planes == 1 ? nq::kKv4 : nq::kKv8;
+    int grid = 0;
+    cudaError_t e;
+    if (cols > 16) e = nq::attn_wide(fmt, A, cols, stream, &grid);
+    else if (fmt == nq::kBf16) e = nq::launch_d<nq::kBf16>(cols / 8, A, stream, &grid);
+    else if (fmt == nq::kKv4) e = nq::launch_d<nq::kKv4>(cols / 8, A, stream, &grid);
+    else e = nq::launch_d<nq::kKv8>(cols / 8, A, stream, &grid);
+    if (e != cudaSuccess) return NQ_ERR_CUDA;
+    return nq::cuda_status(p.D == 128 ? nq::join<128>(cols, A, grid, stream) : nq::join<64>(cols, A, grid, stream));
 }

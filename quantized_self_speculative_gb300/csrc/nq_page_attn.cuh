@@ -34,9 +34,9 @@ struct AttnArgs {
 // Query row of vector v = row * G + head of the group (v, G <= 2^16).
 __device__ __forceinline__ int row_of_vector(const AttnArgs &A, int v) { return A.G == 1 ? v : __umulhi(v, A.g_mul); }
 
-// More than 16 query vectors per kv head (nq_page_attn_wide.cu): runs of its own
-// grid; *cols the columns of a tile.
-cudaError_t attn_wide(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);
+// More than 16 query vectors per kv head (nq_page_attn_wide.cu): launches tiles
+// of `cols` columns (32 or 64), *grid CTAs.
+cudaError_t attn_wide(int fmt, const AttnArgs &A, int cols, cudaStream_t s, int *grid);
 // Bytes of a block of 16 rows: base (or bf16), and refinement where it is read.
 __host__ __device__ constexpr int block_base(int fmt, int D, int NG) { return fmt == kBf16 ? 64 * D : 16 * D + 64 * NG; }
 __host__ __device__ constexpr int block_resid(int fmt, int D) { return fmt == kKv8 ? 16 * D : 0; }
