@@ -87,34 +87,37 @@ struct Turn {
     int from;             // lane of the partner (HALF), own lane otherwise
     bool half, any;
 };
+// Lane l takes the sines of pairs A l .. A l + A - 1 (A = E / 2: two for 128
+// values), which are its own in the interleaved layout; in halves a lane's E
+// pairs come from two (one) other lanes.
 template <int E>
 __device__ __forceinline__ Turn<E> make_turn(const Rope &R, int pos, int lane, bool inverse)
 {
+    constexpr int A = E / 2;
     Turn<E> t;
     t.half = R.layout == NQ_ROPE_HALF;
     const int e0 = lane * E, hr = R.rot / 2;
     t.any = e0 < R.rot;
-    t.from = lane;
-    if (t.half && t.any) t.from = e0 < hr ? lane + hr / E : lane - hr / E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        t.c[e] = 1.0f;
-        t.s[e] = 0.0f;
-    }
-    if (!t.any) return t;
     const bool first = e0 < hr;
+    t.from = !t.half || !t.any ? lane : first ? lane + hr / E : lane - hr / E;
+    float cs[A], sn[A];
+#pragma unroll
+    for (int k = 0; k < A; ++k) {
+        const int i = A * lane + k;
+        const unsigned long long x = static_cast<unsigned long long>(static_cast<long long>(pos)) * (i < hr ? R.rates[i] : 0ull);
+        // half turns in [-1, 1)
+        sincospif(__int2float_rn(static_cast<int>(x >> 32)) * 4.656612873077393e-10f, &sn[k], &cs[k]);
+        cs[k] *= R.mscale;
+        sn[k] *= inverse ? -R.mscale : R.mscale;
+    }
+    const int i0 = t.any && !first ? e0 - hr : e0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int i = t.half ? (first ? e0 + e : e0 + e - hr) : (e0 + e) / 2;
-        const unsigned long long x = static_cast<unsigned long long>(static_cast<long long>(pos)) * R.rates[i];
-        // half turns in [-1, 1)
-        const float h = __int2float_rn(static_cast<int>(x >> 32)) * 4.656612873077393e-10f;
-        float sn, cs;
-        sincospif(h, &sn, &cs);
-        if (inverse) sn = -sn;
-        const bool minus = t.half ? first : (e & 1) == 0;
-        t.c[e] = R.mscale * cs;
-        t.s[e] = R.mscale * (minus ? -sn : sn);
+        const int src = (i0 + e) / A & 31;
+        const float hc = __shfl_sync(0xffffffffu, cs[e % A], src), hs = __shfl_sync(0xffffffffu, sn[e % A], src);
+        const float c = t.half ? hc : cs[e / 2], q = t.half ? hs : sn[e / 2];
+        t.c[e] = t.any ? c : 1.0f;
+        t.s[e] = !t.any ? 0.0f : (t.half ? first : (e & 1) == 0) ? -q : q;
     }
     return t;
 }
@@ -126,7 +129,8 @@ __device__ __forceinline__ Vec<E> turn(const Turn<E> &t, const Vec<E> &x)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const float p = t.half ? __shfl_sync(0xffffffffu, x.v[e], t.from) : x.v[e ^ 1];
-        y.v[e] = t.any ? fmaf(t.c[e], x.v[e], t.s[e] * p) : x.v[e];
+        const float z = fmaf(t.c[e], x.v[e], t.s[e] * p);
+        y.v[e] = t.any ? z : x.v[e];           // also where the partner, unused, is not finite
     }
     return y;
 }
@@ -186,32 +190,49 @@ __device__ __forceinline__ Row row_of(const Pool &p, const Map &m, int s, int po
     return w;
 }
 
+// nested_quantise's codes of w, offset by 8, given rs = 1 / s rounded.  The
+// quotient is the correctly rounded one (Markstein: q + (w - q s) / s in fused
+// operations, s having 11 significant bits) wherever it is not far below the
+// codes' resolution; rounding to whole numbers by adding 1.5 2^23.
+__device__ __forceinline__ void codes_of(float w, float s, float rs, uint32_t &q4, uint32_t &r)
+{
+    const float q = w * rs, x = __fmaf_rn(__fmaf_rn(-q, s, w), rs, q);
+    const float a = fminf(fmaxf(__fadd_rn(__fadd_rn(x, 12582912.0f), -12582912.0f), -8.0f), 7.0f);
+    const float e = __fmul_rn(__fsub_rn(x, a), 16.0f);
+    const float b = fminf(fmaxf(__fadd_rn(__fadd_rn(e, 12582912.0f), -12582912.0f), -8.0f), 7.0f);
+    q4 = __float_as_uint(__fadd_rn(a, 8388616.0f)) & 15u;        // 2^23 + 8 + a: the low bits are a + 8
+    r = __float_as_uint(__fadd_rn(b, 8388616.0f)) & 15u;
+}
+
 // One K (v = 0) or V (v = 1) row of head h, quantised in groups of D / NG.
 template <int D, int NG>
 __device__ __forceinline__ void store_nested(const Pool &p, const Row &w, int h, int v, const Vec<D / 32> &x, int lane,
                                              unsigned int *status)
 {
     constexpr int E = D / 32, RB = D / 2;
-    float amax = 0.0f;
-    bool bad = false;
+    float amax = 0.0f, nan = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         amax = fmaxf(amax, fabsf(x.v[e]));
-        bad |= !(fabsf(x.v[e]) <= 3.4028234663852886e38f);
+        nan = __fmaf_rn(x.v[e], 0.0f, nan);                      // NaN if any value is not finite
     }
 #pragma unroll
     for (int o = 16 / NG; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const __half sh = __float2half_rn(__fdiv_rn(amax, 7.0f));
+    // absmax / 7, correctly rounded as above
+    const float q7 = amax * 0.142857142857142857f;
+    const __half sh = __float2half_rn(__fmaf_rn(__fmaf_rn(-q7, 7.0f, amax), 0.142857142857142857f, q7));
     const float s = __half2float(sh);
-    if (bad || !(s <= 65504.0f)) set_status(status, NQ_DEV_NONFINITE);
+    if (!(nan == 0.0f) || !(s <= 65504.0f)) set_status(status, NQ_DEV_NONFINITE);
+    const float rs = __frcp_rn(s);
     uint32_t b = 0, r = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        int q4, rr;
-        nested_quantise(x.v[e], s, q4, rr);
-        b |= static_cast<uint32_t>(q4 + 8) << (4 * e);
-        r |= static_cast<uint32_t>(rr + 8) << (4 * e);
+        uint32_t q4, rr;
+        codes_of(x.v[e], s, rs, q4, rr);
+        b |= q4 << (4 * e);
+        r |= rr << (4 * e);
     }
+    if (s == 0.0f) b = r = 0x8888u;                              // zeros
     const int blk = w.r >> 4, r16 = w.r & 15;
     uint8_t *rec = w.page + static_cast<size_t>(h) * p.rec;
     uint8_t *base = rec + blk * p.base_block;
@@ -280,51 +301,76 @@ append_kernel(Pool p, Map m, Rope R, bool rope, const TI *__restrict__ q, const 
 }
 
 // ---------------------------------------------------------------- read
-// One warp per (token, head): its K and its V row.
+// One warp per token and run of heads: their K and V rows.
 template <int D, int NG>
 __global__ void __launch_bounds__(kWarps * 32)
-read_kernel(Pool p, Map m, const int32_t *__restrict__ seqs, const int32_t *__restrict__ pos, int T, int planes,
-            __nv_bfloat16 *__restrict__ k_out, __nv_bfloat16 *__restrict__ v_out, unsigned int *status)
+read_kernel(Pool p, Map m, const int32_t *__restrict__ seqs, const int32_t *__restrict__ pos, int T, int planes, int per,
+            int chunks, __nv_bfloat16 *__restrict__ k_out, __nv_bfloat16 *__restrict__ v_out, unsigned int *status)
 {
-    constexpr int E = D / 32, RB = D / 2;
-    const long long wi = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    constexpr int E = D / 32, RB = D / 2, U = 4;
+    const unsigned wi = blockIdx.x * kWarps + (threadIdx.x >> 5), t = wi / chunks;
     const int lane = threadIdx.x & 31;
-    const long long t = wi / p.H;
-    if (t >= T) return;
-    const int h = static_cast<int>(wi % p.H);
+    if (t >= static_cast<unsigned>(T)) return;
+    const int h0 = static_cast<int>(wi - t * chunks) * per, h1 = min(h0 + per, p.H);
     const Row w = row_of(p, m, seqs[t], pos[t], status, lane == 0);
-    Vec<E> x[2];
+    const int blk = w.r >> 4, r16 = w.r & 15;
+    const uint8_t *base = w.page + blk * p.base_block, *resid = w.page + p.resid_off + blk * (16 * D);
+    const uint32_t at = NG == 0 ? 2 * bf_off(D, r16, lane * E) : nib_off(RB, r16, lane * E / 2);
+    const uint32_t sat = 32 * RB + (r16 * NG + lane * NG / 32) * 2;
+    for (int h = h0; h < h1; h += U) {        // the loads of U rows of K and of V before the first is used
+        uint32_t b[U][2][2];
+        unsigned short sc[U][2];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
+        for (int u = 0; u < U; ++u) {
+            if (!w.ok || h + u >= h1) continue;
+            const size_t rec = static_cast<size_t>(h + u) * p.rec;
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[v].v[e] = 0.0f;
-        if (!w.ok) continue;
-        const int blk = w.r >> 4, r16 = w.r & 15;
-        const uint8_t *rec = w.page + static_cast<size_t>(h) * p.rec, *base = rec + blk * p.base_block;
-        if constexpr (NG == 0) {
-            x[v] = load_vec<E>(reinterpret_cast<const __nv_bfloat16 *>(base) + v * 16 * D + bf_off(D, r16, lane * E));
-        } else {
-            const uint32_t at = v * 16 * RB + nib_off(RB, r16, lane * E / 2);
-            const uint8_t *resid = rec + p.resid_off + blk * (16 * D);
-            uint32_t b, r;
-            if constexpr (E == 4) {
-                b = *reinterpret_cast<const uint16_t *>(base + at);
-                r = *reinterpret_cast<const uint16_t *>(resid + at);
-            } else {
-                b = base[at];
-                r = resid[at];
+            for (int v = 0; v < 2; ++v) {
+                if constexpr (NG == 0) {
+                    const uint8_t *src = base + rec + v * 32 * D + at;
+                    if constexpr (E == 4) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                        b[u][v][0] = x.x;
+                        b[u][v][1] = x.y;
+                    } else {
+                        b[u][v][0] = *reinterpret_cast<const uint32_t *>(src);
+                    }
+                } else {
+                    sc[u][v] = *reinterpret_cast<const unsigned short *>(base + rec + sat + v * 32 * NG);
+                    if constexpr (E == 4) {
+                        b[u][v][0] = *reinterpret_cast<const uint16_t *>(base + rec + v * 16 * RB + at);
+                        b[u][v][1] = planes == 2 ? *reinterpret_cast<const uint16_t *>(resid + rec + v * 16 * RB + at) : 0x8888u;
+                    } else {
+                        b[u][v][0] = base[rec + v * 16 * RB + at];
+                        b[u][v][1] = planes == 2 ? resid[rec + v * 16 * RB + at] : 0x8888u;
+                    }
+                }
             }
-            const float s = __half2float(*reinterpret_cast<const __half *>(base + 32 * RB + v * 32 * NG +
-                                                                           (r16 * NG + lane / (32 / NG)) * 2));
+        }
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int q4 = static_cast<int>(b >> (4 * e) & 15u) - 8, rr = static_cast<int>(r >> (4 * e) & 15u) - 8;
-                x[v].v[e] = planes == 1 ? s * q4 : s * 0.0625f * (16 * q4 + rr);
+        for (int u = 0; u < U; ++u) {
+            if (h + u >= h1) continue;
+            const size_t to = (static_cast<size_t>(t) * p.H + h + u) * D + lane * E;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                Vec<E> x;
+                if constexpr (NG == 0) {
+                    bf_pair(b[u][v][0], x.v[0], x.v[1]);
+                    if constexpr (E == 4) bf_pair(b[u][v][1], x.v[2], x.v[3]);
+                } else {
+                    const float s = __half2float(__ushort_as_half(sc[u][v])) * 0.0625f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        x.v[e] = s * static_cast<float>(static_cast<int>(16 * (b[u][v][0] >> (4 * e) & 15u) + (b[u][v][1] >> (4 * e) & 15u)) - 136);
+                }
+                if (!w.ok) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x.v[e] = 0.0f;
+                }
+                store_vec<E>((v ? v_out : k_out) + to, x);
             }
         }
     }
-    store_vec<E>(k_out + wi * D + lane * E, x[0]);
-    store_vec<E>(v_out + wi * D + lane * E, x[1]);
 }
 
 // ---------------------------------------------------------------- host side
@@ -336,12 +382,12 @@ nq_status rope_of(const nq_rope_plan *r, int head_dim, Rope &out)
     out = Rope{r->rot_dim, r->layout, r->mscale, reinterpret_cast<const unsigned long long *>(r->rates)};
     return NQ_OK;
 }
-// Heads per warp: one batch of rows when that fills the machine (16 warps per
-// SM), else fewer, so that a small call spreads over all SMs; more for long
-// prompts, where the sines of a token serve more rows.
+// Heads per warp: many for prompts, where the sines of a token serve them all,
+// and down to one, so that a small call spreads over the machine (16 warps per
+// SM).  At 16384 tokens of 32 heads: 61 us with runs of 8.
 int heads_per_warp(long long T, int heads)
 {
-    int per = 2 * kBatch;
+    int per = 32;
     while (per > 1 && T * ((heads + per - 1) / per) < 16ll * sm_count()) per /= 2;
     return per;
 }
@@ -488,13 +534,14 @@ extern "C" nq_status nq_page_read(const nq_page_pool *pool, int layer, const nq_
         return NQ_ERR_ARG;
     if (!nq::aligned16(k_out) || !nq::aligned16(v_out) || !nq::aligned4(seqs) || !nq::aligned4(pos)) return NQ_ERR_ALIGN;
     const long long warps = static_cast<long long>(T) * p.H;
-    if (warps / nq::kWarps > 2147483000ll) return NQ_ERR_SHAPE;
+    if (warps > 4294960000ll) return NQ_ERR_SHAPE;
     unsigned int *status = nq::device_status_ptr();
     if (!status) return NQ_ERR_CUDA;
     p.data += static_cast<size_t>(layer) * p.layer_bytes;
-    const unsigned grid = static_cast<unsigned>((warps + nq::kWarps - 1) / nq::kWarps);
+    const int per = nq::heads_per_warp(T, p.H), chunks = (p.H + per - 1) / per;
+    const unsigned grid = static_cast<unsigned>((static_cast<long long>(T) * chunks + nq::kWarps - 1) / nq::kWarps);
     auto *ko = reinterpret_cast<__nv_bfloat16 *>(k_out), *vo = reinterpret_cast<__nv_bfloat16 *>(v_out);
-    auto go = [&](auto *kernel) { kernel<<<grid, nq::kWarps * 32, 0, stream>>>(p, m, seqs, pos, T, planes, ko, vo, status); };
+    auto go = [&](auto *kernel) { kernel<<<grid, nq::kWarps * 32, 0, stream>>>(p, m, seqs, pos, T, planes, per, chunks, ko, vo, status); };
     if (p.D == 64) go(p.NG == 0 ? nq::read_kernel<64, 0> : nq::read_kernel<64, 1>);
     else go(p.NG == 0 ? nq::read_kernel<128, 0> : p.NG == 1 ? nq::read_kernel<128, 1> : nq::read_kernel<128, 2>);
     return nq::cuda_status(cudaGetLastError());
