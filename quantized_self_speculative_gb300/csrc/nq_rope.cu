@@ -125,12 +125,18 @@ __device__ __forceinline__ Turn<E> make_turn(const Rope &R, int pos, int lane, b
 template <int E>
 __device__ __forceinline__ Vec<E> turn(const Turn<E> &t, const Vec<E> &x)
 {
-    Vec<E> y;
+    Vec<E> y, q;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const float p = t.half ? __shfl_sync(0xffffffffu, x.v[e], t.from) : x.v[e ^ 1];
-        const float z = fmaf(t.c[e], x.v[e], t.s[e] * p);
-        y.v[e] = t.any ? z : x.v[e];           // also where the partner, unused, is not finite
+        q.v[e] = p;
+    }
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        const float2 z = f2_unpack(f2_fma(f2_pack(t.c[e], t.c[e + 1]), f2_pack(x.v[e], x.v[e + 1]),
+                                          f2_fma(f2_pack(t.s[e], t.s[e + 1]), f2_pack(q.v[e], q.v[e + 1]), f2_pack(0.0f, 0.0f))));
+        y.v[e] = t.any ? z.x : x.v[e];         // also where the partner, unused, is not finite
+        y.v[e + 1] = t.any ? z.y : x.v[e + 1];
     }
     return y;
 }
@@ -190,18 +196,26 @@ __device__ __forceinline__ Row row_of(const Pool &p, const Map &m, int s, int po
     return w;
 }
 
-// nested_quantise's codes of w, offset by 8, given rs = 1 / s rounded.  The
-// quotient is the correctly rounded one (Markstein: q + (w - q s) / s in fused
-// operations, s having 11 significant bits) wherever it is not far below the
-// codes' resolution; rounding to whole numbers by adding 1.5 2^23.
-__device__ __forceinline__ void codes_of(float w, float s, float rs, uint32_t &q4, uint32_t &r)
+// nested_quantise's codes of two values, given rs = 1 / s rounded: bytes
+// 16 (q4 + 8) + r + 8.  The quotient is the correctly rounded one (Markstein: q +
+// (w - q s) / s in fused operations, s having 11 significant bits) wherever it
+// is not far below the codes' resolution.  It is held within [-8.49, 7.49], which
+// changes no code (beyond, q4 and r are at their ends) and makes q4 = rint(x)
+// need no clamp; rounding to whole numbers is adding 1.5 2^23.
+__device__ __forceinline__ void codes_of(float w0, float w1, float s, float rs, uint32_t &c0, uint32_t &c1)
 {
-    const float q = w * rs, x = __fmaf_rn(__fmaf_rn(-q, s, w), rs, q);
-    const float a = fminf(fmaxf(__fadd_rn(__fadd_rn(x, 12582912.0f), -12582912.0f), -8.0f), 7.0f);
-    const float e = __fmul_rn(__fsub_rn(x, a), 16.0f);
-    const float b = fminf(fmaxf(__fadd_rn(__fadd_rn(e, 12582912.0f), -12582912.0f), -8.0f), 7.0f);
-    q4 = __float_as_uint(__fadd_rn(a, 8388616.0f)) & 15u;        // 2^23 + 8 + a: the low bits are a + 8
-    r = __float_as_uint(__fadd_rn(b, 8388616.0f)) & 15u;
+    const auto both = [](float x) { return f2_pack(x, x); };
+    const unsigned long long w = f2_pack(w0, w1), magic = both(12582912.0f), less = both(-12582912.0f), rr = both(rs);
+    const unsigned long long q = f2_fma(w, rr, both(0.0f));
+    float2 x = f2_unpack(f2_fma(f2_fma(q, both(-s), w), rr, q));
+    x.x = fminf(fmaxf(x.x, -8.49f), 7.49f);
+    x.y = fminf(fmaxf(x.y, -8.49f), 7.49f);
+    const unsigned long long xv = f2_pack(x.x, x.y), a = f2_add(f2_add(xv, magic), less);
+    float2 b = f2_unpack(f2_add(f2_fma(f2_sub(xv, a), both(16.0f), magic), less));
+    const unsigned long long bv = f2_pack(fminf(b.x, 7.0f), fminf(b.y, 7.0f));
+    const float2 c = f2_unpack(f2_fma(a, both(16.0f), f2_add(bv, both(8388744.0f))));    // 2^23 + 136 + 16 q4 + r: exact
+    c0 = __float_as_uint(c.x);
+    c1 = __float_as_uint(c.y);
 }
 
 // One K (v = 0) or V (v = 1) row of head h, quantised in groups of D / NG.
@@ -224,13 +238,16 @@ __device__ __forceinline__ void store_nested(const Pool &p, const Row &w, int h,
     const float s = __half2float(sh);
     if (!(nan == 0.0f) || !(s <= 65504.0f)) set_status(status, NQ_DEV_NONFINITE);
     const float rs = __frcp_rn(s);
-    uint32_t b = 0, r = 0;
+    uint32_t c[E], b, r;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        uint32_t q4, rr;
-        codes_of(x.v[e], s, rs, q4, rr);
-        b |= q4 << (4 * e);
-        r |= rr << (4 * e);
+    for (int e = 0; e < E; e += 2) codes_of(x.v[e], x.v[e + 1], s, rs, c[e], c[e + 1]);
+    if constexpr (E == 4) {
+        const uint32_t lo = __byte_perm(c[0], c[2], 0x0040), hi = __byte_perm(c[1], c[3], 0x0040);   // bytes 0, 1: values 0, 2 and 1, 3
+        b = (lo >> 4 & 0x0F0Fu) | (hi & 0xF0F0u);
+        r = (lo & 0x0F0Fu) | (hi << 4 & 0xF0F0u);
+    } else {
+        b = (c[0] >> 4 & 0x0Fu) | (c[1] & 0xF0u);
+        r = (c[0] & 0x0Fu) | (c[1] << 4 & 0xF0u);
     }
     if (s == 0.0f) b = r = 0x8888u;                              // zeros
     const int blk = w.r >> 4, r16 = w.r & 15;
