@@ -20,7 +20,6 @@ namespace nq {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kBatch = 4;
 
 struct Rope {
     int rot, layout;
@@ -30,36 +29,76 @@ struct Rope {
 
 template <int E> struct Vec { float v[E]; };
 
-template <int E>
-__device__ __forceinline__ Vec<E> load_vec(const float *p)
-{
-    Vec<E> r;
-    if constexpr (E == 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(p);
-        r.v[0] = f.x; r.v[1] = f.y; r.v[2] = f.z; r.v[3] = f.w;
-    } else {
-        const float2 f = *reinterpret_cast<const float2 *>(p);
-        r.v[0] = f.x; r.v[1] = f.y;
-    }
-    return r;
-}
 __device__ __forceinline__ void bf_pair(uint32_t w, float &a, float &b)
 {
     a = __uint_as_float(w << 16);
     b = __uint_as_float(w & 0xFFFF0000u);
 }
+// A lane's E values as loaded; kBatch of them are in flight at once (16 registers).
+template <int E, typename T> struct Raw;
 template <int E>
-__device__ __forceinline__ Vec<E> load_vec(const __nv_bfloat16 *p)
-{
-    Vec<E> r;
-    if constexpr (E == 4) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-        bf_pair(w.x, r.v[0], r.v[1]);
-        bf_pair(w.y, r.v[2], r.v[3]);
-    } else {
-        bf_pair(*reinterpret_cast<const uint32_t *>(p), r.v[0], r.v[1]);
+struct Raw<E, float> {
+    static constexpr int kBatch = 16 / E;
+    float v[E];
+    __device__ __forceinline__ void load(const float *p)
+    {
+        if constexpr (E == 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(p);
+            v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        } else {
+            const float2 f = *reinterpret_cast<const float2 *>(p);
+            v[0] = f.x; v[1] = f.y;
+        }
     }
-    return r;
+    __device__ __forceinline__ Vec<E> values() const
+    {
+        Vec<E> r;
+#pragma unroll
+        for (int e = 0; e < E; ++e) r.v[e] = v[e];
+        return r;
+    }
+};
+template <int E>
+struct Raw<E, __nv_bfloat16> {
+    static constexpr int kBatch = 8;
+    uint32_t v[E / 2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p)
+    {
+        if constexpr (E == 4) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(p);
+            v[0] = w.x; v[1] = w.y;
+        } else {
+            v[0] = *reinterpret_cast<const uint32_t *>(p);
+        }
+    }
+    __device__ __forceinline__ Vec<E> values() const
+    {
+        Vec<E> r;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) bf_pair(v[e / 2], r.v[e], r.v[e + 1]);
+        return r;
+    }
+};
+// f(row, values) for rows n of D values from `in`: full batches, then one by one.
+template <int D, typename T, typename F>
+__device__ __forceinline__ void each_row(const T *in, int n, F f)
+{
+    constexpr int E = D / 32, B = Raw<E, T>::kBatch;
+    int i = 0;
+#pragma unroll 1
+    for (; i + B <= n; i += B) {
+        Raw<E, T> x[B];
+#pragma unroll
+        for (int u = 0; u < B; ++u) x[u].load(in + (i + u) * D);
+#pragma unroll
+        for (int u = 0; u < B; ++u) f(i + u, x[u].values());
+    }
+#pragma unroll 1
+    for (; i < n; ++i) {
+        Raw<E, T> x;
+        x.load(in + i * D);
+        f(i, x.values());
+    }
 }
 __device__ __forceinline__ uint32_t bf_pack(float a, float b)
 {
@@ -156,15 +195,7 @@ rope_kernel(Rope R, const TI *x, long long xs, const int32_t *__restrict__ pos, 
     const TI *in = x + t * xs + lane * E;
     TO *to = out + t * os + lane * E;
     const Turn<E> tn = make_turn<E>(R, pos[t], lane, inverse);
-    for (int h = h0; h < h1; h += kBatch) {
-        Vec<E> v[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-            if (h + u < h1) v[u] = load_vec<E>(in + (h + u) * D);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-            if (h + u < h1) store_vec<E>(to + (h + u) * D, turn<E>(tn, v[u]));
-    }
+    each_row<D>(in + h0 * D, h1 - h0, [&](int i, const Vec<E> &v) { store_vec<E>(to + (h0 + i) * D, turn<E>(tn, v)); });
 }
 
 // ---------------------------------------------------------------- append
@@ -218,12 +249,33 @@ __device__ __forceinline__ void codes_of(float w0, float w1, float s, float rs, 
     c1 = __float_as_uint(c.y);
 }
 
-// One K (v = 0) or V (v = 1) row of head h, quantised in groups of D / NG.
+// Where a lane's part of a K (v = 0) or V (v = 1) row of head 0 lies; the other
+// heads' follow p.rec bytes apart.
 template <int D, int NG>
-__device__ __forceinline__ void store_nested(const Pool &p, const Row &w, int h, int v, const Vec<D / 32> &x, int lane,
-                                             unsigned int *status)
+struct Place {
+    uint8_t *base;
+    int resid, scale;     // from base
+    __device__ __forceinline__ Place(const Pool &p, const Row &w, int v, int lane)
+    {
+        constexpr int E = D / 32, RB = D / 2;
+        const int blk = w.r >> 4, r16 = w.r & 15;
+        if constexpr (NG == 0) {
+            base = w.page + blk * p.base_block + v * 32 * D + 2 * bf_off(D, r16, lane * E);
+            resid = scale = 0;
+        } else {
+            const int at = v * 16 * RB + nib_off(RB, r16, lane * E / 2);
+            base = w.page + blk * p.base_block + at;
+            resid = static_cast<int>(p.resid_off) + blk * (16 * D) - blk * static_cast<int>(p.base_block);
+            scale = 32 * RB + v * 32 * NG + (r16 * NG + lane * NG / 32) * 2 - at;
+        }
+    }
+};
+
+// One row, quantised in groups of D / NG; true where it is not finite.
+template <int D, int NG>
+__device__ __forceinline__ bool store_nested(const Place<D, NG> &at, size_t off, const Vec<D / 32> &x, int lane)
 {
-    constexpr int E = D / 32, RB = D / 2;
+    constexpr int E = D / 32;
     float amax = 0.0f, nan = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -232,48 +284,34 @@ __device__ __forceinline__ void store_nested(const Pool &p, const Row &w, int h,
     }
 #pragma unroll
     for (int o = 16 / NG; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // absmax / 7, correctly rounded as above
+    // absmax / 7, correctly rounded as in codes_of
     const float q7 = amax * 0.142857142857142857f;
     const __half sh = __float2half_rn(__fmaf_rn(__fmaf_rn(-q7, 7.0f, amax), 0.142857142857142857f, q7));
-    const float s = __half2float(sh);
-    if (!(nan == 0.0f) || !(s <= 65504.0f)) set_status(status, NQ_DEV_NONFINITE);
-    const float rs = __frcp_rn(s);
+    const float s = __half2float(sh), rs = __frcp_rn(s);
     uint32_t c[E], b, r;
 #pragma unroll
     for (int e = 0; e < E; e += 2) codes_of(x.v[e], x.v[e + 1], s, rs, c[e], c[e + 1]);
+    uint8_t *to = at.base + off;
     if constexpr (E == 4) {
         const uint32_t lo = __byte_perm(c[0], c[2], 0x0040), hi = __byte_perm(c[1], c[3], 0x0040);   // bytes 0, 1: values 0, 2 and 1, 3
         b = (lo >> 4 & 0x0F0Fu) | (hi & 0xF0F0u);
         r = (lo & 0x0F0Fu) | (hi << 4 & 0xF0F0u);
+        b = s == 0.0f ? 0x8888u : b;                             // zeros
+        r = s == 0.0f ? 0x8888u : r;
+        *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(b);
+        *reinterpret_cast<uint16_t *>(to + at.resid) = static_cast<uint16_t>(r);
     } else {
         b = (c[0] >> 4 & 0x0Fu) | (c[1] & 0xF0u);
         r = (c[0] & 0x0Fu) | (c[1] << 4 & 0xF0u);
+        to[0] = static_cast<uint8_t>(s == 0.0f ? 0x88u : b);
+        to[at.resid] = static_cast<uint8_t>(s == 0.0f ? 0x88u : r);
     }
-    if (s == 0.0f) b = r = 0x8888u;                              // zeros
-    const int blk = w.r >> 4, r16 = w.r & 15;
-    uint8_t *rec = w.page + static_cast<size_t>(h) * p.rec;
-    uint8_t *base = rec + blk * p.base_block;
-    const uint32_t at = v * 16 * RB + nib_off(RB, r16, lane * E / 2);
-    uint8_t *resid = rec + p.resid_off + blk * (16 * D);
-    if constexpr (E == 4) {
-        *reinterpret_cast<uint16_t *>(base + at) = static_cast<uint16_t>(b);
-        *reinterpret_cast<uint16_t *>(resid + at) = static_cast<uint16_t>(r);
-    } else {
-        base[at] = static_cast<uint8_t>(b);
-        resid[at] = static_cast<uint8_t>(r);
-    }
-    if (lane % (32 / NG) == 0)
-        *reinterpret_cast<__half *>(base + 32 * RB + v * 32 * NG + (r16 * NG + lane / (32 / NG)) * 2) = sh;
-}
-template <int D>
-__device__ __forceinline__ void store_bf16(const Pool &p, const Row &w, int h, int v, const Vec<D / 32> &x, int lane)
-{
-    constexpr int E = D / 32;
-    uint8_t *rec = w.page + static_cast<size_t>(h) * p.rec + (w.r >> 4) * p.base_block;
-    store_vec<E>(reinterpret_cast<__nv_bfloat16 *>(rec) + v * 16 * D + bf_off(D, w.r & 15, lane * E), x);
+    if (lane % (32 / NG) == 0) *reinterpret_cast<__half *>(to + at.scale) = sh;
+    return !(nan == 0.0f) || !(s <= 65504.0f);
 }
 
-// NG = 0: BF16.  Rows of a token in the order q heads, k heads, v heads.
+// NG = 0: BF16.  Rows of a token in the order q heads, k heads, v heads; a warp
+// takes a run of them.
 template <int D, int NG, typename TI>
 __global__ void __launch_bounds__(kWarps * 32)
 append_kernel(Pool p, Map m, Rope R, bool rope, const TI *__restrict__ q, const TI *__restrict__ k,
@@ -286,35 +324,33 @@ append_kernel(Pool p, Map m, Rope R, bool rope, const TI *__restrict__ q, const 
     const int lane = threadIdx.x & 31;
     const long long t = wi / chunks;
     if (t >= T) return;
-    const int all = Hq + 2 * p.H, h0 = static_cast<int>(wi % chunks) * per, h1 = min(h0 + per, all);
+    const int H = p.H, h0 = static_cast<int>(wi - t * chunks) * per, h1 = min(h0 + per, Hq + 2 * H);
     const int ps = pos[t];
     const Row w = row_of(p, m, seqs[t], ps, status, lane == 0 && h1 > Hq);
     Turn<E> tn{};
-    if (rope && h0 < Hq + p.H) tn = make_turn<E>(R, ps, lane, false);
-    for (int h = h0; h < h1; h += kBatch) {
-        Vec<E> x[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int a = h + u;
-            if (a >= h1) continue;
-            const TI *src = a < Hq ? q + a * D : a < Hq + p.H ? k + (a - Hq) * D : v + (a - Hq - p.H) * D;
-            x[u] = load_vec<E>(src + t * stride + lane * E);
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int a = h + u;
-            if (a >= h1) continue;
-            if (rope && a < Hq + p.H) x[u] = turn<E>(tn, x[u]);
-            if (a < Hq) {
-                store_vec<E>(q_out + (t * Hq + a) * D + lane * E, x[u]);
-                continue;
-            }
-            if (!w.ok) continue;
-            const int kv = a >= Hq + p.H, head = a - Hq - kv * p.H;
-            if constexpr (NG == 0) store_bf16<D>(p, w, head, kv, x[u], lane);
-            else store_nested<D, NG>(p, w, head, kv, x[u], lane, status);
-        }
+    const bool turned = rope && h0 < Hq + H;
+    if (turned) tn = make_turn<E>(R, ps, lane, false);
+    const long long at = t * stride + lane * E;
+    if (h0 < Hq) {
+        __nv_bfloat16 *to = q_out + (t * Hq + h0) * D + lane * E;
+        each_row<D>(q + at + h0 * D, min(h1, Hq) - h0, [&](int i, const Vec<E> &x) { store_vec<E>(to + i * D, turned ? turn<E>(tn, x) : x); });
     }
+    if (!w.ok) return;
+    bool bad = false;
+#pragma unroll 1
+    for (int kv = 0; kv < 2; ++kv) {
+        const int a = max(h0 - Hq - kv * H, 0), b = min(h1 - Hq - kv * H, H);
+        if (a >= b) continue;
+        const Place<D, NG> place(p, w, kv, lane);
+        const bool tk = turned && kv == 0;
+        each_row<D>((kv ? v : k) + at + a * D, b - a, [&](int i, const Vec<E> &x0) {
+            const Vec<E> x = tk ? turn<E>(tn, x0) : x0;
+            const size_t off = static_cast<size_t>(a + i) * p.rec;
+            if constexpr (NG == 0) store_vec<E>(reinterpret_cast<__nv_bfloat16 *>(place.base + off), x);
+            else bad |= store_nested<D, NG>(place, off, x, lane);
+        });
+    }
+    if (bad) set_status(status, NQ_DEV_NONFINITE);
 }
 
 // ---------------------------------------------------------------- read
