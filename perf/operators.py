@@ -538,7 +538,7 @@ def _own(s):
     s["book"].copy_(s["snap"])
     got = {"book": s["book"]}
     if c["kind"] == "compact":
-        got["used"] = pmap.compact(pool)
+        got["used"] = pmap.compact(pool).view(())
         got["data"] = s["data"].view(torch.int32)
     elif c["kind"] == "beams":
         pmap.fork(s["src"], s["seqs"], s["rows"])
