@@ -659,7 +659,7 @@ attn_kernel(const __grid_constant__ AttnArgs A)
 // CTA (i, v): query vector v of the segment that run i begins and later runs
 // end (if there is one): out = sum_r 2^(m_r - M) o_r / sum_r 2^(m_r - M) l_r
 // over the runs' partial states, eight warps taking every eighth.
-template <int D, int NV>
+template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 join_kernel(const __grid_constant__ AttnArgs A)
 {
@@ -668,7 +668,7 @@ join_kernel(const __grid_constant__ AttnArgs A)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 in = A.info[blockIdx.x];
     if (in.x < 0) return;
-    const int kvh = in.y / A.QT, v = (in.y % A.QT) * NV + blockIdx.y;
+    const int kvh = in.y / A.QT, v = (in.y % A.QT) * A.cols + blockIdx.y;
     if (v >= A.M * A.G) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x, n = in.z - first + 1;
     float m = -INFINITY, l = 0.0f, o[E] = {};
@@ -683,7 +683,7 @@ join_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
             for (int e = 0; e < E; ++e) oo[u][e] = 0.0f;
             if (r < n) {
-                const size_t at = (2 * static_cast<size_t>(first + r) + (r == 0 ? 1 : 0)) * NV + blockIdx.y;
+                const size_t at = (2 * static_cast<size_t>(first + r) + (r == 0 ? 1 : 0)) * A.cols + blockIdx.y;
                 mm[u] = A.part_ml[at * 2];
                 ll[u] = A.part_ml[at * 2 + 1];
                 const float *p = A.part_o + at * D + lane * E;
@@ -759,7 +759,6 @@ cudaError_t launch_d(int nt, const AttnArgs &A, cudaStream_t s, int *grid)
     return launch_x<FMT, 128, 1>(nt, A, s, grid);
 }
 
-template <int D, int NV>
 cudaError_t launch_join(const AttnArgs &A, int grid, cudaStream_t s)
 {
     // a programmatic dependent launch: it overlaps the end of the kernel before it
@@ -767,32 +766,32 @@ cudaError_t launch_join(const AttnArgs &A, int grid, cudaStream_t s)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, A.M * A.G < NV ? A.M * A.G : NV);
+    cfg.gridDim = dim3(grid, A.M * A.G < A.cols ? A.M * A.G : A.cols);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, NV>, A);
+    return cudaLaunchKernelEx(&cfg, A.p.D == 128 ? join_kernel<128> : join_kernel<64>, A);
 }
-template <int D>
-cudaError_t join(int cols, const AttnArgs &A, int grid, cudaStream_t s)
+
+// Columns (query vectors) per tile.  Up to 16 a warp holds them all and decodes
+// for itself.  More share a CTA's decoded steps: 128 rows of the tensor cores
+// where a row of the cache has one scale, else 8 columns per warp.
+bool tensor_cores(int vectors, int fmt, int ng) { return vectors > 16 && fmt != kBf16 && ng == 1; }
+int cols_of(int vectors, bool tc)
 {
-    return cols == 8 ? launch_join<D, 8>(A, grid, s) : cols == 16 ? launch_join<D, 16>(A, grid, s)
-         : cols == 32 ? launch_join<D, 32>(A, grid, s) : launch_join<D, 64>(A, grid, s);
+    if (tc) return vectors < 128 ? (vectors + 7) / 8 * 8 : 128;
+    return vectors <= 8 ? 8 : vectors <= 16 ? 16 : vectors <= 32 ? 32 : 64;
 }
 
-// Query vectors per tile: the fewest columns that hold them.  Up to 16 a warp
-// holds them all and decodes for itself; more share a CTA's decoded steps.
-int cols_of(int vectors) { return vectors <= 8 ? 8 : vectors <= 16 ? 16 : vectors <= 32 ? 32 : 64; }
-constexpr int kMaxCtas = 4;
-
-// Workspace: info, then partial states of two segments per CTA.
+// Workspace: info, then partial states of two segments per CTA; enough for any
+// of the kernels (4 CTAs per SM and 32 columns, 2 and 64, 1 and 128, ..).
 struct Ws {
     size_t ml, o, total;
 };
 Ws ws_of(int vectors, int D)
 {
-    const size_t ctas = static_cast<size_t>(kMaxCtas) * sm_count(), cols = 2 * ctas * cols_of(vectors);
+    const size_t ctas = 4 * static_cast<size_t>(sm_count()), cols = 2 * static_cast<size_t>(sm_count()) * (vectors <= 8 ? 32 : vectors <= 16 ? 48 : 128);
     Ws w;
     w.ml = ctas * sizeof(int4);
     w.o = w.ml + cols * 8;
@@ -840,7 +839,9 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
     A.Hq = heads_q;
     A.G = G;
     A.g_mul = static_cast<unsigned>((0x100000000ull + G - 1) / G);
-    const int cols = nq::cols_of(M * G);
+    const int fmt = p.NG == 0 ? nq::kBf16 : planes == 1 ? nq::kKv4 : nq::kKv8;
+    const bool tc = nq::tensor_cores(M * G, fmt, p.NG);
+    const int cols = A.cols = nq::cols_of(M * G, tc);
     A.QT = (M * G + cols - 1) / cols;
     // the kernel numbers the steps of all segments in 32 bits
     if (static_cast<double>(batch) * p.H * A.QT * (static_cast<double>(A.m.W) * A.m.P / 16 + 2) > 2.0e9) return NQ_ERR_SHAPE;
@@ -855,13 +856,13 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
     A.info = reinterpret_cast<int4 *>(wb);
     A.part_ml = reinterpret_cast<float *>(wb + w.ml);
     A.part_o = reinterpret_cast<float *>(wb + w.o);
-    const int fmt = p.NG == 0 ? nq::kBf16 : planes == 1 ? nq::kKv4 : nq::kKv8;
     int grid = 0;
     cudaError_t e;
-    if (cols > 16) e = nq::attn_wide(fmt, A, cols, stream, &grid);
+    if (tc) e = nq::attn_tc(fmt, A, stream, &grid);
+    else if (cols > 16) e = nq::attn_wide(fmt, A, stream, &grid);
     else if (fmt == nq::kBf16) e = nq::launch_d<nq::kBf16>(cols / 8, A, stream, &grid);
     else if (fmt == nq::kKv4) e = nq::launch_d<nq::kKv4>(cols / 8, A, stream, &grid);
     else e = nq::launch_d<nq::kKv8>(cols / 8, A, stream, &grid);
     if (e != cudaSuccess) return NQ_ERR_CUDA;
-    return nq::cuda_status(p.D == 128 ? nq::join<128>(cols, A, grid, stream) : nq::join<64>(cols, A, grid, stream));
+    return nq::cuda_status(nq::launch_join(A, grid, stream));
 }

@@ -19,7 +19,7 @@ struct AttnArgs {
     Map m;
     const __nv_bfloat16 *q;
     long long q_stride;
-    int B, M, Hq, G, QT;                // G query heads per kv head, QT tiles per (sequence, kv head)
+    int B, M, Hq, G, QT, cols;          // G query heads per kv head, QT tiles of cols vectors per (sequence, kv head)
     unsigned g_mul;                     // ceil(2^32 / G)
     const int32_t *seqs, *len;
     float scale, softcap;
@@ -34,9 +34,9 @@ struct AttnArgs {
 // Query row of vector v = row * G + head of the group (v, G <= 2^16).
 __device__ __forceinline__ int row_of_vector(const AttnArgs &A, int v) { return A.G == 1 ? v : __umulhi(v, A.g_mul); }
 
-// More than 16 query vectors per kv head (nq_page_attn_wide.cu): launches tiles
-// of `cols` columns (32 or 64), *grid CTAs.
-cudaError_t attn_wide(int fmt, const AttnArgs &A, int cols, cudaStream_t s, int *grid);
+// More than 16 query vectors per kv head: tiles of A.cols columns, *grid CTAs.
+cudaError_t attn_wide(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);   // nq_page_attn_wide.cu, 32 or 64
+cudaError_t attn_tc(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);     // nq_page_attn_tc.cu, up to 128
 // Bytes of a block of 16 rows: base (or bf16), and refinement where it is read.
 __host__ __device__ constexpr int block_base(int fmt, int D, int NG) { return fmt == kBf16 ? 64 * D : 16 * D + 64 * NG; }
 __host__ __device__ constexpr int block_resid(int fmt, int D) { return fmt == kKv8 ? 16 * D : 0; }
@@ -334,21 +334,22 @@ struct Feed {
     {
         if (left == 0) return;
         if ((threadIdx.x & 31) == 0) {
-            const int n = BLKS == 1 || row + 16 < w.s.hi ? BLKS : 1;
+            const int n = min(BLKS, (w.s.hi - row + 15) >> 4), page_blocks = 1 << (lp - 4);
             const uint32_t b = bar + 8 * st, dst = ring + st * STAGE;
             mbar_expect_tx(b, n * (BASE + RESID));
+            int next = 0;
 #pragma unroll
             for (int k = 0; k < BLKS; ++k) {
+                if (k != next || k >= n) continue;               // copied with the block before
                 if (id[k] < 0 || id[k] >= A.p.N) {
                     set_status(A.status, NQ_DEV_BAD_PAGE);
                     id[k] = 0;
                 }
-                const bool both = BLKS == 2 && k == 0 && n == 2 && lp > 4;       // two blocks that lie side by side
-                const int blk = ((row + 16 * k) & (A.m.P - 1)) >> 4, x = both ? 2 : 1;
+                const int blk = ((row + 16 * k) & (A.m.P - 1)) >> 4, x = min(n - k, page_blocks - blk);   // side by side in the page
                 const uint8_t *src = rec + static_cast<size_t>(id[k]) * A.p.H * A.p.rec;
                 bulk_g2s(dst + k * BASE, src + blk * BASE, x * BASE, b);
                 if constexpr (FMT == kKv8) bulk_g2s(dst + BLKS * BASE + k * RESID, src + A.p.resid_off + blk * RESID, x * RESID, b);
-                if (both || n == 1) break;
+                next = k + x;
             }
         }
         row += STRIDE * SR;

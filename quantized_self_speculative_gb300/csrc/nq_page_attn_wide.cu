@@ -485,9 +485,9 @@ cudaError_t launch_d(const AttnArgs &A, int warps, cudaStream_t s, int *grid)
 
 }  // namespace
 
-cudaError_t attn_wide(int fmt, const AttnArgs &A, int cols, cudaStream_t s, int *grid)
+cudaError_t attn_wide(int fmt, const AttnArgs &A, cudaStream_t s, int *grid)
 {
-    const int warps = cols / 8;
+    const int warps = A.cols / 8;
     return fmt == kBf16 ? launch_d<kBf16>(A, warps, s, grid) : fmt == kKv4 ? launch_d<kKv4>(A, warps, s, grid) : launch_d<kKv8>(A, warps, s, grid);
 }
 
