@@ -74,6 +74,20 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 {
     return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort_flag, status);
 }
+// The same for hand-overs inside a step, where the sleep's wake-up would be most
+// of the wait: try_wait without a time hint for some microseconds, then as above.
+__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                               unsigned int *status)
+{
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i) {
+        uint32_t ok;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if (ok) return true;
+    }
+    return mbar_wait_slow(bar, parity, abort_flag, status);
+}
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"

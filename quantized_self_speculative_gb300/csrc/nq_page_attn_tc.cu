@@ -13,7 +13,7 @@
 //
 // Warp roles, handing on through mbarriers (all waits bounded):
 //   0-3   softmax: lane quarter w of tensor memory; also Q in, O out
-//   4-11  decode: stage -> K, V^T, scales (two buffers)
+//   4-11  decode: stage -> K, V^T, scales (four buffers: up to three steps ahead)
 //   12    issues the MMAs: S of the next step before P V of this one
 //   13    feeds the ring of raw blocks
 // O is only rescaled when a row's maximum has grown by 2^kSlack, which waits for
@@ -32,6 +32,7 @@ constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp + 1;
 constexpr int kThreads = (kFeedWarp + 1) * 32;
 constexpr int kMinRun = 2;              // steps per CTA
 constexpr int kKeys = 64;               // cache rows per step
+constexpr int kBufs = 4;                // decoded steps
 constexpr int kTmem = 512;              // columns: Q at 0 (D / 2), S at 64 (two of 64), P at 192 (two of 32), O at 256 (D)
 constexpr uint32_t kColS = 64, kColP = 192, kColO = 256;
 
@@ -43,11 +44,11 @@ struct Tc {
     static constexpr int BUF = K_BYTES + V_BYTES;                // one step, both operands in 1024-byte groups
     static constexpr int SCALES = 3 * kKeys * 4;                 // K's, V's, log2 of V's
     static constexpr int STAGES = 4;
-    static constexpr int SMEM = 2 * BUF + 2 * SCALES + STAGES * STAGE;
+    static constexpr int SMEM = kBufs * (BUF + SCALES) + STAGES * STAGE;
 };
 
 // Barriers by number.
-constexpr int kRawFull = 0, kRawEmpty = 4, kKvFull = 8, kPvDone = 10, kSFull = 12, kPFull = 14, kQFull = 16, kDrain = 17, kBars = 18;
+constexpr int kRawFull = 0, kRawEmpty = 4, kKvFull = 8, kKvEmpty = 12, kPvDone = 16, kSFull = 18, kPFull = 20, kQFull = 22, kDrain = 23, kBars = 24;
 
 template <int FMT, int D, bool X>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -55,7 +56,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
 {
     using Q = Tc<FMT, D>;
     constexpr int SR = kKeys, BLKS = Q::BLKS, RB = D / 2;
-    static_assert(Q::STAGES == 4, "barrier numbers");
+    static_assert(Q::STAGES == 4 && kBufs == 4, "barrier numbers");
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) unsigned long long bars[kBars];
     __shared__ int abort_flag, keep_tmem;
@@ -70,9 +71,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(kRawFull + i), 1);
             mbar_init(bar(kRawEmpty + i), kDecodeWarps);
+            mbar_init(bar(kKvFull + i), kDecodeWarps);
+            mbar_init(bar(kKvEmpty + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kKvFull + i), kDecodeWarps);
             mbar_init(bar(kPvDone + i), 1);
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPFull + i), kSoftWarps);
@@ -94,8 +96,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    unsigned char *scales = sm + 2 * Q::BUF, *ring = scales + 2 * Q::SCALES;
-    auto wait = [&](int i, int phase) { return mbar_wait(bar(i), static_cast<uint32_t>(phase) & 1u, &abort_flag, A.status); };
+    unsigned char *scales = sm + kBufs * Q::BUF, *ring = scales + kBufs * Q::SCALES;
+    auto wait = [&](int i, int phase) { return mbar_wait_fast(bar(i), static_cast<uint32_t>(phase) & 1u, &abort_flag, A.status); };
     const int steps = run.f1 - run.f0;
     Walk<SR> use;
     use.open(A, run.b, run.base, run.f0, run.f1);
@@ -117,8 +119,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
         // ================================================= decode
         const int dw = warp - kSoftWarps, g = lane >> 2, t = lane & 3;
         for (int i = 0; i < steps; ++i) {
-            const int st = i % Q::STAGES, b = i & 1;
-            if (!__all_sync(0xffffffffu, wait(kRawFull + st, i / Q::STAGES & 1) && wait(kPvDone + b, (i >> 1 & 1) ^ 1))) break;
+            const int st = i % Q::STAGES, b = i % kBufs;
+            if (!__all_sync(0xffffffffu, wait(kRawFull + st, i / Q::STAGES & 1) && wait(kKvEmpty + b, (i / kBufs & 1) ^ 1))) break;
             const unsigned char *sp = ring + st * Q::STAGE;
             unsigned char *kt = sm + b * Q::BUF, *vt = kt + Q::K_BYTES;
             // ---- K: thread = (row, 16-byte chunk of nibbles): four words of eight values, in
@@ -146,8 +148,12 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                 if (e < kKeys) {
                     const __half *sc = reinterpret_cast<const __half *>(sp + (e >> 4) * Q::BASE + 32 * RB);
                     float *f = reinterpret_cast<float *>(scales + b * Q::SCALES);
-                    const float sv = __half2float(sc[16 + (e & 15)]);
-                    f[e] = __half2float(sc[e & 15]);
+                    // a scale that is not finite counts as 0: rows past the end may hold anything, and
+                    // the value of a row that was not finite is unspecified
+                    float sk = __half2float(sc[e & 15]), sv = __half2float(sc[16 + (e & 15)]);
+                    sk = sk <= 65504.0f ? sk : 0.0f;
+                    sv = sv <= 65504.0f ? sv : 0.0f;
+                    f[e] = sk;
                     f[kKeys + e] = sv;
                     f[2 * kKeys + e] = lg2(fmaxf(sv, 3.7252902984619140625e-09f));   // a scale of 0 has codes of 0
                 }
@@ -205,12 +211,12 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
         bool ok = true;
         int issued_s = 0, seg_no = 0;         // S products issued; segments begun
         auto scores = [&](int i, bool first) {                   // S of step i
-            bool w = wait(kKvFull + (i & 1), i >> 1 & 1);
+            bool w = wait(kKvFull + i % kBufs, i / kBufs & 1);
             if (first) w = w && wait(kQFull, seg_no & 1);
             if (!__all_sync(0xffffffffu, w)) return false;
             if (first) ++seg_no;
             tc_fence_after();
-            const uint32_t kt = smem_u32(sm + (i & 1) * Q::BUF);
+            const uint32_t kt = smem_u32(sm + i % kBufs * Q::BUF);
             uint32_t leader;
             if (elect_one(leader)) {
 #pragma unroll
@@ -237,13 +243,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
             ok = __all_sync(0xffffffffu, wait(kPFull + (i & 1), i >> 1 & 1));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t vt = smem_u32(sm + (i & 1) * Q::BUF + Q::K_BYTES);
+            const uint32_t vt = smem_u32(sm + i % kBufs * Q::BUF + Q::K_BYTES);
             uint32_t leader;
             if (elect_one(leader)) {
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
                     tc_mma(tmem + kColO, tmem + kColP + 32 * (i & 1) + 8 * k, sw128_desc(vt + k * 32), idesc_o, !first || k != 0);
                 tc_commit(bar(kPvDone + (i & 1)));
+                tc_commit(bar(kKvEmpty + i % kBufs));
             }
             __syncwarp();
             issued_by |= 1u << leader;
@@ -335,30 +342,40 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld16(tq + kColS + 64 * b + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(s + 16 * c));
                 tc_wait_ld();
-                const float *f = reinterpret_cast<const float *>(scales + b * Q::SCALES);
-                float top = -INFINITY;
+                const float *f = reinterpret_cast<const float *>(scales + i % kBufs * Q::SCALES);
+                // scores in base 2 (X), or what cq makes scores of
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
-                    const float4 k4 = *reinterpret_cast<const float4 *>(f + j), l4 = *reinterpret_cast<const float4 *>(f + 2 * kKeys + j);
-                    const float sk[4] = {k4.x, k4.y, k4.z, k4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+                    const float4 k4 = *reinterpret_cast<const float4 *>(f + j);
+                    const float sk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         float x = __uint_as_float(s[j + u]) * sk[u];
                         if constexpr (X) {
                             x *= cq;
                             if (A.softcap > 0.0f) x = capped(x, cap2, inv2);
-                            if (A.slopes) x = fmaf(slope2, static_cast<float>(row0 + j + u - own), x);
-                        }
-                        float y = X ? x + lv[u] : fmaf(x, cq, lv[u]);
-                        if (masked) {     // before the window, or (negative) after the query's own row
-                            const bool hidden = static_cast<unsigned>(own - (row0 + j + u)) >= window;
-                            x = hidden ? -INFINITY : x;
-                            y = hidden ? -INFINITY : y;
+                            x = fmaf(slope2, static_cast<float>(row0 + j + u - own), x);
                         }
                         s[j + u] = __float_as_uint(x);
-                        top = fmaxf(top, y);
                     }
                 }
+                if (masked) {                 // before the window, or (negative) after the query's own row
+                    const unsigned d = own - row0;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) s[j] = d - j >= window ? 0xFF800000u : s[j];
+                }
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};    // with the log2 of V's scales
+#pragma unroll
+                for (int j = 0; j < 64; j += 4) {
+                    const float4 l4 = *reinterpret_cast<const float4 *>(f + 2 * kKeys + j);
+                    const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float x = __uint_as_float(s[j + u]);
+                        tops[u] = fmaxf(tops[u], X ? x + lv[u] : fmaf(x, cq, lv[u]));
+                    }
+                }
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 if (__any_sync(0xffffffffu, top > mref + kSlack)) {
                     const float mn = top > mref + kSlack ? top : mref, alpha = ex2(mref == -INFINITY ? -INFINITY : mref - mn);
                     mref = mn;
@@ -379,6 +396,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                         tc_wait_st();
                     }
                 }
+                float sums[4] = {lsum, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t pr[16];
@@ -386,19 +404,19 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                     for (int j = 0; j < 32; j += 4) {
                         const float4 v4 = *reinterpret_cast<const float4 *>(f + kKeys + 32 * c + j);
                         const float sv[4] = {v4.x, v4.y, v4.z, v4.w};
-                        float p[4];
+                        float e[4];
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
-                            const float x = __uint_as_float(s[32 * c + j + u]), e = ex2(X ? x - mz : fmaf(x, cq, -mz));
-                            lsum += e;
-                            p[u] = e * sv[u];
-                            if (masked) p[u] = x == -INFINITY ? 0.0f : p[u];     // a hidden row's scale may be anything
+                            const float x = __uint_as_float(s[32 * c + j + u]);
+                            e[u] = ex2(X ? x - mz : fmaf(x, cq, -mz));
+                            sums[u] += e[u];
                         }
-                        pr[j / 2] = pack_h(p[0], p[1]);
-                        pr[j / 2 + 1] = pack_h(p[2], p[3]);
+                        pr[j / 2] = pack_h(e[0] * sv[0], e[1] * sv[1]);
+                        pr[j / 2 + 1] = pack_h(e[2] * sv[2], e[3] * sv[3]);
                     }
                     tc_st16(tq + kColP + 32 * b + 16 * c, pr);
                 }
+                lsum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
                 tc_wait_st();
             }
             if (gave_up) break;
