@@ -290,12 +290,13 @@ __device__ __forceinline__ Run find_run(const AttnArgs &A, int segs, int min_run
 }
 
 // Fills a ring with the steps f, f + STRIDE, .. of a run: the whole warp walks,
-// lane 0 copies.  The page ids of a step are loaded one step ahead.
+// lane k copies block k of the step (and those that follow it in its page).  The
+// page ids of a step are loaded one step ahead.
 template <int FMT, int D, int NG, int BLKS, int STRIDE>
 struct Feed {
     static constexpr int SR = 16 * BLKS, BASE = block_base(FMT, D, NG), RESID = block_resid(FMT, D), STAGE = BLKS * (BASE + RESID);
     Walk<SR> w;
-    int row, left, id[BLKS], lp;              // row of the next step; how many are left in this segment (0: none at all)
+    int row, left, id, lp;                    // row of the next step; how many are left in this segment (0: none at all); lane's page
     const int32_t *tab;
     const uint8_t *rec;
     uint32_t ring, bar;
@@ -317,9 +318,8 @@ struct Feed {
     }
     __device__ __forceinline__ void look()
     {
-        if (left == 0) return;
-#pragma unroll
-        for (int k = 0; k < BLKS; ++k) id[k] = row + 16 * k < w.s.hi ? tab[(row + 16 * k) >> lp] : 0;
+        const int k = threadIdx.x & 31, r = row + 16 * k;
+        if (left > 0 && k < BLKS && r < w.s.hi) id = tab[r >> lp];
     }
     __device__ __forceinline__ void start(const AttnArgs &A, const Walk<SR> &at, int segs, int f, uint32_t ring_, uint32_t bar_)
     {
@@ -327,31 +327,28 @@ struct Feed {
         ring = ring_;
         bar = bar_;
         lp = 31 - __clz(A.m.P);
+        id = 0;
         aim(A, segs, f);
         look();
     }
     __device__ __forceinline__ void issue(const AttnArgs &A, int segs, int st)   // the step into stage st, then on to the next
     {
         if (left == 0) return;
-        if ((threadIdx.x & 31) == 0) {
-            const int n = min(BLKS, (w.s.hi - row + 15) >> 4), page_blocks = 1 << (lp - 4);
-            const uint32_t b = bar + 8 * st, dst = ring + st * STAGE;
-            mbar_expect_tx(b, n * (BASE + RESID));
-            int next = 0;
-#pragma unroll
-            for (int k = 0; k < BLKS; ++k) {
-                if (k != next || k >= n) continue;               // copied with the block before
-                if (id[k] < 0 || id[k] >= A.p.N) {
-                    set_status(A.status, NQ_DEV_BAD_PAGE);
-                    id[k] = 0;
-                }
-                const int blk = ((row + 16 * k) & (A.m.P - 1)) >> 4, x = min(n - k, page_blocks - blk);   // side by side in the page
-                const uint8_t *src = rec + static_cast<size_t>(id[k]) * A.p.H * A.p.rec;
-                bulk_g2s(dst + k * BASE, src + blk * BASE, x * BASE, b);
-                if constexpr (FMT == kKv8) bulk_g2s(dst + BLKS * BASE + k * RESID, src + A.p.resid_off + blk * RESID, x * RESID, b);
-                next = k + x;
+        const int k = threadIdx.x & 31, n = min(BLKS, (w.s.hi - row + 15) >> 4), blk = ((row + 16 * k) & (A.m.P - 1)) >> 4;
+        const uint32_t b = bar + 8 * st, dst = ring + st * STAGE;
+        if (k == 0) mbar_expect_tx(b, n * (BASE + RESID));
+        __syncwarp();
+        if (k < n && (k == 0 || blk == 0)) {
+            if (id < 0 || id >= A.p.N) {
+                set_status(A.status, NQ_DEV_BAD_PAGE);
+                id = 0;
             }
+            const int x = min(n - k, (1 << (lp - 4)) - blk);                     // blocks side by side in the page
+            const uint8_t *src = rec + static_cast<size_t>(id) * A.p.H * A.p.rec;
+            bulk_g2s(dst + k * BASE, src + blk * BASE, x * BASE, b);
+            if constexpr (FMT == kKv8) bulk_g2s(dst + BLKS * BASE + k * RESID, src + A.p.resid_off + blk * RESID, x * RESID, b);
         }
+        __syncwarp();
         row += STRIDE * SR;
         if (--left == 0) aim(A, segs, w.base + (row - w.s.lo) / SR);
         look();

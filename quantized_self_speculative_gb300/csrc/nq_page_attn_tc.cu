@@ -343,21 +343,26 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                 for (int c = 0; c < 4; ++c) tc_ld16(tq + kColS + 64 * b + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(s + 16 * c));
                 tc_wait_ld();
                 const float *f = reinterpret_cast<const float *>(scales + i % kBufs * Q::SCALES);
-                // scores in base 2 (X), or what cq makes scores of
+                // scores in base 2 (X), or what cq makes scores of; two keys at a time in packed fp32
+                const unsigned long long zero2 = f2_pack(0.0f, 0.0f), cq2 = f2_pack(cq, cq);
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 k4 = *reinterpret_cast<const float4 *>(f + j);
-                    const float sk[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        float x = __uint_as_float(s[j + u]) * sk[u];
-                        if constexpr (X) {
-                            x *= cq;
-                            if (A.softcap > 0.0f) x = capped(x, cap2, inv2);
-                            x = fmaf(slope2, static_cast<float>(row0 + j + u - own), x);
-                        }
-                        s[j + u] = __float_as_uint(x);
+                    float2 x[2] = {f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2_pack(k4.x, k4.y), zero2)),
+                                   f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), f2_pack(k4.z, k4.w), zero2))};
+                    if constexpr (X) {
+                        auto option = [&](float y, int key) {
+                            y *= cq;
+                            if (A.softcap > 0.0f) y = capped(y, cap2, inv2);
+                            return fmaf(slope2, static_cast<float>(row0 + key - own), y);
+                        };
+                        x[0] = make_float2(option(x[0].x, j), option(x[0].y, j + 1));
+                        x[1] = make_float2(option(x[1].x, j + 2), option(x[1].y, j + 3));
                     }
+                    s[j] = __float_as_uint(x[0].x);
+                    s[j + 1] = __float_as_uint(x[0].y);
+                    s[j + 2] = __float_as_uint(x[1].x);
+                    s[j + 3] = __float_as_uint(x[1].y);
                 }
                 if (masked) {                 // before the window, or (negative) after the query's own row
                     const unsigned d = own - row0;
@@ -368,12 +373,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 l4 = *reinterpret_cast<const float4 *>(f + 2 * kKeys + j);
-                    const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float x = __uint_as_float(s[j + u]);
-                        tops[u] = fmaxf(tops[u], X ? x + lv[u] : fmaf(x, cq, lv[u]));
-                    }
+                    const unsigned long long x0 = f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])),
+                                             x1 = f2_pack(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+                    const float2 y0 = f2_unpack(X ? f2_add(x0, f2_pack(l4.x, l4.y)) : f2_fma(x0, cq2, f2_pack(l4.x, l4.y))),
+                                 y1 = f2_unpack(X ? f2_add(x1, f2_pack(l4.z, l4.w)) : f2_fma(x1, cq2, f2_pack(l4.z, l4.w)));
+                    tops[0] = fmaxf(tops[0], y0.x);
+                    tops[1] = fmaxf(tops[1], y0.y);
+                    tops[2] = fmaxf(tops[2], y1.x);
+                    tops[3] = fmaxf(tops[3], y1.y);
                 }
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 if (__any_sync(0xffffffffu, top > mref + kSlack)) {
@@ -396,27 +403,30 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                         tc_wait_st();
                     }
                 }
-                float sums[4] = {lsum, 0.0f, 0.0f, 0.0f};
+                unsigned long long sum0 = f2_pack(lsum, 0.0f), sum1 = zero2;
+                const unsigned long long less = f2_pack(-mz, -mz);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t pr[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 v4 = *reinterpret_cast<const float4 *>(f + kKeys + 32 * c + j);
-                        const float sv[4] = {v4.x, v4.y, v4.z, v4.w};
-                        float e[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float x = __uint_as_float(s[32 * c + j + u]);
-                            e[u] = ex2(X ? x - mz : fmaf(x, cq, -mz));
-                            sums[u] += e[u];
-                        }
-                        pr[j / 2] = pack_h(e[0] * sv[0], e[1] * sv[1]);
-                        pr[j / 2 + 1] = pack_h(e[2] * sv[2], e[3] * sv[3]);
+                        const int k = 32 * c + j;
+                        const unsigned long long x0 = f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])),
+                                                 x1 = f2_pack(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+                        const float2 a0 = f2_unpack(X ? f2_add(x0, less) : f2_fma(x0, cq2, less)),
+                                     a1 = f2_unpack(X ? f2_add(x1, less) : f2_fma(x1, cq2, less));
+                        const unsigned long long e0 = f2_pack(ex2(a0.x), ex2(a0.y)), e1 = f2_pack(ex2(a1.x), ex2(a1.y));
+                        sum0 = f2_add(sum0, e0);
+                        sum1 = f2_add(sum1, e1);
+                        const float2 p0 = f2_unpack(f2_fma(e0, f2_pack(v4.x, v4.y), zero2)), p1 = f2_unpack(f2_fma(e1, f2_pack(v4.z, v4.w), zero2));
+                        pr[j / 2] = pack_h(p0.x, p0.y);
+                        pr[j / 2 + 1] = pack_h(p1.x, p1.y);
                     }
                     tc_st16(tq + kColP + 32 * b + 16 * c, pr);
                 }
-                lsum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+                const float2 sum = f2_unpack(f2_add(sum0, sum1));
+                lsum = sum.x + sum.y;
                 tc_wait_st();
             }
             if (gave_up) break;
