@@ -775,9 +775,11 @@ cudaError_t launch_join(const AttnArgs &A, int grid, cudaStream_t s)
 }
 
 // Columns (query vectors) per tile.  Up to 16 a warp holds them all and decodes
-// for itself.  More share a CTA's decoded steps: 128 rows of the tensor cores
-// where a row of the cache has one scale, else 8 columns per warp.
-bool tensor_cores(int vectors, int fmt, int ng) { return vectors > 16 && fmt != kBf16 && ng == 1; }
+// for itself (16 vectors, 16 ragged sequences of the 8-bit view: 38 us against 64
+// on the tensor cores).  More share a CTA's decoded steps: the tensor cores from
+// 25 on where a row of the cache has one scale (36 vectors 66 us against 77, 72
+// vectors 79 against 176), else 8 columns per warp (20 vectors 58 us against 65).
+bool tensor_cores(int vectors, int fmt, int ng) { return vectors > 24 && fmt != kBf16 && ng == 1; }
 int cols_of(int vectors, bool tc)
 {
     if (tc) return vectors < 128 ? (vectors + 7) / 8 * 8 : 128;

@@ -1,5 +1,5 @@
-// nq_page_attn_tc.cu -- attention over nested pages for more than 16 query
-// vectors per kv head (a verify pass with grouped queries), on the 5th-generation
+// nq_page_attn_tc.cu -- attention over nested pages for many query vectors per
+// kv head (from 25 on: a verify pass with grouped queries), on the 5th-generation
 // tensor cores.
 //
 // With many query vectors the products and the decoding bound the time, not
