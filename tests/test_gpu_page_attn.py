@@ -13,14 +13,14 @@ def i32(v):
     return torch.tensor(v, dtype=torch.int32, device="cuda")
 
 
-def cache(nq, lens, H, D, G, P, fmt, seed, layers=1, amp=1.0, extra=2):
+def cache(nq, lens, H, D, G, P, fmt, seed, layers=1, amp=1.0, extra=2, fill=-1):
     """Sequences of lens rows at shuffled pages.  Everything past their rows --
     the rest of their last pages, other pages, table entries -- is garbage."""
     g = torch.Generator().manual_seed(seed)
     need = [-(-n // P) for n in lens]
     W, N = max(need) + extra, sum(need) + 3
     pool = nq.PagePool(layers, N, P, H, D, fmt, group=G)
-    pool.data.fill_(255)                         # NaN as bf16, NaN scales
+    pool.data.view(torch.int16).fill_(fill)      # -1: NaN as bf16, NaN scales
     ids = torch.randperm(N, generator=g).int()
     table = torch.full((len(lens), W), -7, dtype=torch.int32)
     at = 0
@@ -198,3 +198,71 @@ def test_reports(nq):
             bad()
     with pytest.raises(nq.NQError):
         pool.attention(0, m, q, i32([1, 1]), 3, 0.1)
+
+
+# more query vectors per kv head than one warp holds: 8 columns per warp, or rows of the tensor cores
+MANY = [
+    (1, 8, 64, 64, 16, 4, [0, 1, 63, 64, 65, 200, 3]),       # 32 vectors of small heads, lengths about a step
+    (2, 8, 128, 128, 16, 5, [1, 4, 700, 129, 64]),           # 40
+    (2, 8, 128, 64, 32, 5, [1, 4, 700, 129]),                # 40, two groups per row
+    (1, 20, 128, 128, 64, 9, [333, 100, 9]),                 # 180: two tiles of the tensor cores, three of 64
+    (2, 7, 128, 128, 128, 3, [80, 2000]),                    # 21
+    (1, 13, 64, 64, 256, 2, [515, 31]),                      # 26
+    (1, 128, 128, 128, 16, 1, [300]),                        # 128: a full tile
+]
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("H,g,D,G,P,M,lens", MANY)
+def test_many_query_vectors(nq, fmt, planes, H, g, D, G, P, M, lens):
+    pool, m = cache(nq, lens, H, D, G, P, getattr(nq, "KV_BF16" if fmt == "bf16" else "KV_NESTED44"), 11 * H + M, layers=2)
+    check(nq, pool, m, lens, query(M + D, len(lens), M, H * g, D), planes, D ** -0.5)
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("cap,window,slopes", [(20.0, 0, False), (0.0, 1, False), (0.0, 90, False), (0.0, 0, True), (50.0, 333, True)])
+@pytest.mark.parametrize("D,G,g", [(128, 128, 8), (64, 64, 4), (128, 64, 4)])
+def test_many_query_vectors_cap_window_bias(nq, fmt, planes, cap, window, slopes, D, G, g):
+    lens, H, M = [1, 47, 900, 0, 130], 2, 7
+    pool, m = cache(nq, lens, H, D, G, 32, getattr(nq, "KV_BF16" if fmt == "bf16" else "KV_NESTED44"), 150)
+    s = torch.tensor([2.0 ** -(i % 7 + 1) for i in range(H * g)], device="cuda") if slopes else None
+    check(nq, pool, m, lens, 4 * query(151, len(lens), M, H * g, D), planes, 0.1, softcap=cap, window=window, slopes=s)
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+def test_many_query_vectors_long_and_many(nq, fmt, planes):
+    """Segments cut over many CTAs, many short ones, peaked and tiny values; the same bits again."""
+    kind = getattr(nq, "KV_BF16" if fmt == "bf16" else "KV_NESTED44")
+    pool, m = cache(nq, [9000, 5, 0, 4097], 1, 128, 128, 64, kind, 170)
+    q = query(171, 4, 5, 8, 128)
+    want = check(nq, pool, m, [9000, 5, 0, 4097], q, planes, 0.09)
+    for _ in range(30):
+        assert torch.equal(pool.attention(0, m, q, i32([9000, 5, 0, 4097]), planes, 0.09), want)
+    lens = [(53 * i) % 150 for i in range(90)]
+    pool, m = cache(nq, lens, 4, 64, 64, 16, kind, 172)
+    check(nq, pool, m, lens, query(173, 90, 4, 32, 64), planes, 0.125)
+    pool, m = cache(nq, [900, 77], 1, 128, 128, 16, kind, 174, amp=1e-4)
+    check(nq, pool, m, [900, 77], 30 * query(175, 2, 4, 8, 128), planes, 0.09)
+
+
+def test_many_query_vectors_inner_values(nq):
+    """bf16: a non-finite value row is seen by the queries at and after it, by no earlier one."""
+    lens, M = [50], 4
+    pool, m = cache(nq, lens, 1, 64, 64, 16, nq.KV_BF16, 190)
+    q = query(191, 1, M, 8, 64)
+    want = pool.attention(0, m, q, i32(lens), 2, 0.1)
+    k, v = pool.read(0, m, i32([0]), i32([48]))
+    v[:] = float("inf")
+    pool.append(0, m, k, v, i32([0]), i32([48]))
+    got = pool.attention(0, m, q, i32(lens), 2, 0.1)
+    assert torch.equal(got[:, :2], want[:, :2]) and torch.isinf(got[:, 2:]).all()
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("fill", [-1, -1024, 0x7C00, -128, 0x7F80, 0x7BFF])
+@pytest.mark.parametrize("g,M", [(1, 1), (4, 3), (4, 5), (8, 5)])
+def test_rows_past_the_end_hold_anything(nq, fmt, planes, fill, g, M):
+    """NaN, both infinities (of fp16, of bf16) and the largest scale in every row that no sequence has."""
+    lens = [1, 18, 250, 65, 0, 33]
+    pool, m = cache(nq, lens, 2, 64, 64, 32, getattr(nq, "KV_BF16" if fmt == "bf16" else "KV_NESTED44"), 200, fill=fill)
+    check(nq, pool, m, lens, query(201 + M, len(lens), M, 2 * g, 64), planes, 0.125)
