@@ -10,11 +10,12 @@ namespace nq {
 enum { kBf16 = 0, kKv4 = 1, kKv8 = 2 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-// m is only raised when the maximum has grown by 2^kSlack, so that the
-// accumulators are rarely rescaled.  P <= 2^12 is inside fp16's range (below
-// 2^16), and what falls below its normal range is under 2^-14 of the first
-// maximum.  At 6 some row of 32 outgrew it at nearly every step of 64 keys.
-constexpr float kSlack = 12.0f;
+// m is only raised when the maximum has grown by more than 2^slack, so that the
+// accumulators are rarely rescaled.  With fp16 probabilities P <= 2^12 is inside
+// their range (below 2^16), and what falls below its normal part is under 2^-14 of
+// the first maximum; at 6 some row of 32 outgrew it at nearly every step of 64 keys.
+// bf16 rounds P to 2^-8: there the largest P stays 1, which is exact.
+template <int FMT> __host__ __device__ constexpr float slack() { return FMT == kBf16 ? 0.0f : 12.0f; }
 
 struct AttnArgs {
     Pool p;

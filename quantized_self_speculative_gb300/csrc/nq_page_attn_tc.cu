@@ -16,7 +16,7 @@
 //   4-11  decode: stage -> K, V^T, scales (four buffers: up to three steps ahead)
 //   12    issues the MMAs: S of the next step before P V of this one
 //   13    feeds the ring of raw blocks
-// O is only rescaled when a row's maximum has grown by 2^kSlack, which waits for
+// O is only rescaled when a row's maximum has grown by 2^12, which waits for
 // the product before.  One CTA per SM (512 columns of tensor memory), the same
 // runs, partial states and join as the other kernels.
 #include <atomic>
@@ -383,8 +383,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                     tops[3] = fmaxf(tops[3], y1.y);
                 }
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                if (__any_sync(0xffffffffu, top > mref + kSlack)) {
-                    const float mn = top > mref + kSlack ? top : mref, alpha = ex2(mref == -INFINITY ? -INFINITY : mref - mn);
+                if (__any_sync(0xffffffffu, top > mref + slack<FMT>())) {
+                    const float mn = top > mref + slack<FMT>() ? top : mref, alpha = ex2(mref == -INFINITY ? -INFINITY : mref - mn);
                     mref = mn;
                     mz = mn == -INFINITY ? 0.0f : mn;
                     lsum *= alpha;
