@@ -493,6 +493,36 @@ class KVCache:
                     v_base=p(self.v_base), v_resid=p(self.v_resid), v_scales=sc(self.v_scales))
 
 
+# ---------------------------------------------------------------- memory of the calls below
+def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new tensor that the stream may write at once: its memory comes from that
+    stream's share of the allocator, whose earlier users the stream waits for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class _Scratch:
+    """Workspaces of the calls on one object, kept from call to call (a fork and a
+    reservation take 37 us instead of 43, the host's share being all of it): one
+    per stream, whose calls follow each other, and per host thread, as two threads'
+    launches may interleave.  A captured call takes memory of its graph, a call
+    with a stream argument memory of that stream."""
+
+    def __init__(self, device):
+        self.device, self.kept = device, {}
+
+    def get(self, need: int, stream: Optional[torch.cuda.Stream], handle: int) -> torch.Tensor:
+        if stream is not None or torch.cuda.is_current_stream_capturing():
+            return _empty(need, torch.uint8, self.device, stream)
+        key = handle, threading.get_ident()
+        ws = self.kept.get(key)
+        if ws is None or ws.numel() < need:
+            ws = self.kept[key] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return ws
+
+
 # ---------------------------------------------------------------- rotary positions
 _DT = {torch.float32: 0, torch.bfloat16: 1}
 
@@ -538,7 +568,7 @@ def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Ten
         raise ValueError("x must be fp32 or bf16 [T][heads][head_dim]")
     T, H, D = x.shape
     if out is None:
-        out = torch.empty((T, H, D), dtype=out_dtype or x.dtype, device=x.device)
+        out = _empty((T, H, D), out_dtype or x.dtype, x.device, stream)
     elif out.dtype not in _DT or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be fp32 or bf16, of out_dtype")
     if pos.shape != (T,):
@@ -561,7 +591,7 @@ class PageMap:
     def __init__(self, max_seqs: int, max_pages: int, n_pages: int, page_size: int, table=None, held=None, ref=None,
                  device=None, stream=None):
         dev = table.device if table is not None else device or torch.device("cuda")
-        mk = lambda *s: torch.empty(s, dtype=torch.int32, device=dev)  # noqa: E731
+        mk = lambda *s: _empty(s, torch.int32, dev, stream)  # noqa: E731
         fresh = table is None
         if fresh and (held is not None or ref is not None):
             raise ValueError("held and ref come with a table")
@@ -578,14 +608,19 @@ class PageMap:
         self.struct = nq_page_map(max_seqs, max_pages, n_pages, page_size, p(table, "table"), p(held, "held"), p(ref, "ref"))
         self.ptr = C.byref(self.struct)
         self._ws_bytes = {}              # workspace size by the number of sequences
+        self._scratch = _Scratch(dev)
         if fresh:
             _check(lib().nq_page_map_init(self.ptr, _stream(stream)), "nq_page_map_init")
 
-    def workspace(self, n: int) -> torch.Tensor:
+    def _work(self, n: int, ws: Optional[torch.Tensor], stream, handle: int) -> torch.Tensor:
+        """The given workspace, or one for n sequences."""
+        if ws is not None:
+            _dev(ws, torch.uint8, "ws")
+            return ws
         need = self._ws_bytes.get(n)
         if need is None:
             need = self._ws_bytes[n] = max(lib().nq_page_workspace_bytes(self.ptr, n), 16)
-        return torch.empty(need, dtype=torch.uint8, device=self.table.device)
+        return self._scratch.get(need, stream, handle)
 
     @staticmethod
     def _list(t: torch.Tensor, n: int, what: str) -> int:
@@ -597,21 +632,21 @@ class PageMap:
         """Pages for rows first[i] .. last[i]-1 of slots seqs[i], shared ones
         copied first; returns int32 [n], 1 where served."""
         n = seqs.shape[0]
-        granted = granted if granted is not None else torch.empty(n, dtype=torch.int32, device=seqs.device)
-        ws = ws if ws is not None else self.workspace(n)
+        on = _stream(stream)
+        granted = granted if granted is not None else _empty(n, torch.int32, seqs.device, stream)
+        ws = self._work(n, ws, stream, on)
         _check(lib().nq_page_reserve(self.ptr, None if pool is None else pool.ptr, self._list(seqs, n, "seqs"),
                                      self._list(first, n, "first"), self._list(last, n, "last"), n,
-                                     self._list(granted, n, "granted"), _dev(ws, torch.uint8, "ws"), ws.numel(),
-                                     _stream(stream)), "nq_page_reserve")
+                                     self._list(granted, n, "granted"), ws.data_ptr(), ws.numel(), on),
+               "nq_page_reserve")
         return granted
 
     def fork(self, src, dst, rows, ws=None, stream=None) -> None:
         """Slot dst[i] shares slot src[i]'s first rows[i] rows (all pairs at once)."""
-        n = src.shape[0]
-        ws = ws if ws is not None else self.workspace(n)
+        n, on = src.shape[0], _stream(stream)
+        ws = self._work(n, ws, stream, on)
         _check(lib().nq_page_fork(self.ptr, self._list(src, n, "src"), self._list(dst, n, "dst"),
-                                  self._list(rows, n, "rows"), n, _dev(ws, torch.uint8, "ws"), ws.numel(),
-                                  _stream(stream)), "nq_page_fork")
+                                  self._list(rows, n, "rows"), n, ws.data_ptr(), ws.numel(), on), "nq_page_fork")
 
     def truncate(self, seqs, rows, stream=None) -> None:
         """Slot seqs[i] keeps the pages of its first rows[i] rows."""
@@ -621,10 +656,11 @@ class PageMap:
 
     def compact(self, pool: "PagePool", used=None, ws=None, stream=None) -> torch.Tensor:
         """Move the pages in use to the lowest ids; returns how many (int32 [1])."""
-        used = used if used is not None else torch.empty(1, dtype=torch.int32, device=self.table.device)
-        ws = ws if ws is not None else self.workspace(1)
-        _check(lib().nq_page_compact(self.ptr, pool.ptr, self._list(used, 1, "used"), _dev(ws, torch.uint8, "ws"),
-                                     ws.numel(), _stream(stream)), "nq_page_compact")
+        on = _stream(stream)
+        used = used if used is not None else _empty(1, torch.int32, self.table.device, stream)
+        ws = self._work(1, ws, stream, on)
+        _check(lib().nq_page_compact(self.ptr, pool.ptr, self._list(used, 1, "used"), ws.data_ptr(), ws.numel(), on),
+               "nq_page_compact")
         return used
 
 
@@ -647,6 +683,7 @@ class PagePool:
                                    _dev(data, torch.uint8, "data"))
         self.ptr = C.byref(self.struct)
         self._attn_bytes = {}            # workspace size by (M, heads_q)
+        self._scratch = _Scratch(data.device)
 
     def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Copy pages src[i] to dst[i] in every layer."""
@@ -670,7 +707,7 @@ class PagePool:
         if T == 1:
             stride = max(H, Hq) * D
         if q is not None and q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            q_out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
         if T == 0:
             return q_out
         _check(lib().nq_page_append(self.ptr, layer, pmap.ptr, None if rope is None else rope.ref,
@@ -692,7 +729,7 @@ class PagePool:
         """The stored K and V rows pos[t] of slots seqs[t] as bf16 [T][heads_kv][head_dim]."""
         T = seqs.shape[0]
         shape = (T, self.heads_kv, self.head_dim)
-        mk = lambda t: t if t is not None else torch.empty(shape, dtype=torch.bfloat16, device=seqs.device)  # noqa: E731
+        mk = lambda t: t if t is not None else _empty(shape, torch.bfloat16, seqs.device, stream)  # noqa: E731
         k_out, v_out = mk(k_out), mk(v_out)
         if T:
             _check(lib().nq_page_read(self.ptr, layer, pmap.ptr, PageMap._list(seqs, T, "seqs"),
@@ -711,20 +748,23 @@ class PagePool:
             raise ValueError("q must have the pool's head_dim")
         if slopes is not None and slopes.shape != (Hq,):
             raise ValueError("slopes must be fp32 [heads_q]")
+        on = _stream(stream)
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty((B, M, Hq, D), q.dtype, q.device, stream)
         if ws is None:
             need = self._attn_bytes.get((M, Hq))
             if need is None:
                 need = self._attn_bytes[M, Hq] = max(lib().nq_page_attn_workspace_bytes(M, Hq, self.heads_kv, D), 16)
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = self._scratch.get(need, stream, on)
+        else:
+            _dev(ws, torch.uint8, "ws")
         o = nq_attn_opts(float(scale), float(softcap), int(window), 0,
                          None if slopes is None else _dev(slopes, torch.float32, "slopes"))
         _check(lib().nq_page_attn(self.ptr, layer, pmap.ptr, _dev(q, torch.bfloat16, "q"), Hq * D, B, M, Hq,
                                   None if seqs is None else PageMap._list(seqs, B, "seqs"),
                                   PageMap._list(lens, B, "lens"), int(planes), C.byref(o),
-                                  self._rows(out, (B, M, Hq, D), "out"), _dev(ws, torch.uint8, "ws"), ws.numel(),
-                                  _stream(stream)), "nq_page_attn")
+                                  self._rows(out, (B, M, Hq, D), "out"), ws.data_ptr(), ws.numel(), on),
+               "nq_page_attn")
         return out
 
 
