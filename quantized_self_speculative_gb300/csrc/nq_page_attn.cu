@@ -37,8 +37,8 @@
 // rows, 8 kv heads of 128: 252 us, 6.8 TB/s, the measured copy rate.  131072 rows
 // x 32 kv heads of 128: 8-bit view 171 us, 6.4 TB/s (94%); 4-bit view 119 us, 4.7
 // TB/s (69%), bound by instruction issue: 293 warp instructions per block of 16
-// rows (placing codes, scales, softmax), issue slots 54% busy with the 12 warps
-// that registers allow, the MMA pipe 23%.  32768 rows of the 4-bit view: 38 us,
+// rows (placing codes, scales, softmax) would need 3.0 per cycle and SM to keep up
+// with HBM; the 12 warps that registers allow reach 2.1 (MMA pipe 23% busy).  32768 rows of the 4-bit view: 38 us,
 // some 10 of them launch, first fills, merge and join.
 #include <atomic>
 
