@@ -632,21 +632,22 @@ class PageMap:
         """Pages for rows first[i] .. last[i]-1 of slots seqs[i], shared ones
         copied first; returns int32 [n], 1 where served."""
         n = seqs.shape[0]
+        lists = self._list(seqs, n, "seqs"), self._list(first, n, "first"), self._list(last, n, "last")
         on = _stream(stream)
         granted = granted if granted is not None else _empty(n, torch.int32, seqs.device, stream)
         ws = self._work(n, ws, stream, on)
-        _check(lib().nq_page_reserve(self.ptr, None if pool is None else pool.ptr, self._list(seqs, n, "seqs"),
-                                     self._list(first, n, "first"), self._list(last, n, "last"), n,
+        _check(lib().nq_page_reserve(self.ptr, None if pool is None else pool.ptr, *lists, n,
                                      self._list(granted, n, "granted"), ws.data_ptr(), ws.numel(), on),
                "nq_page_reserve")
         return granted
 
     def fork(self, src, dst, rows, ws=None, stream=None) -> None:
         """Slot dst[i] shares slot src[i]'s first rows[i] rows (all pairs at once)."""
-        n, on = src.shape[0], _stream(stream)
+        n = src.shape[0]
+        lists = self._list(src, n, "src"), self._list(dst, n, "dst"), self._list(rows, n, "rows")
+        on = _stream(stream)
         ws = self._work(n, ws, stream, on)
-        _check(lib().nq_page_fork(self.ptr, self._list(src, n, "src"), self._list(dst, n, "dst"),
-                                  self._list(rows, n, "rows"), n, ws.data_ptr(), ws.numel(), on), "nq_page_fork")
+        _check(lib().nq_page_fork(self.ptr, *lists, n, ws.data_ptr(), ws.numel(), on), "nq_page_fork")
 
     def truncate(self, seqs, rows, stream=None) -> None:
         """Slot seqs[i] keeps the pages of its first rows[i] rows."""
@@ -748,9 +749,11 @@ class PagePool:
             raise ValueError("q must have the pool's head_dim")
         if slopes is not None and slopes.shape != (Hq,):
             raise ValueError("slopes must be fp32 [heads_q]")
+        given = (_dev(q, torch.bfloat16, "q"), Hq * D, B, M, Hq, None if seqs is None else PageMap._list(seqs, B, "seqs"),
+                 PageMap._list(lens, B, "lens"), int(planes))
         on = _stream(stream)
         if out is None:
-            out = _empty((B, M, Hq, D), q.dtype, q.device, stream)
+            out = torch.empty_like(q) if stream is None else _empty(q.shape, q.dtype, q.device, stream)
         if ws is None:
             need = self._attn_bytes.get((M, Hq))
             if need is None:
@@ -760,11 +763,8 @@ class PagePool:
             _dev(ws, torch.uint8, "ws")
         o = nq_attn_opts(float(scale), float(softcap), int(window), 0,
                          None if slopes is None else _dev(slopes, torch.float32, "slopes"))
-        _check(lib().nq_page_attn(self.ptr, layer, pmap.ptr, _dev(q, torch.bfloat16, "q"), Hq * D, B, M, Hq,
-                                  None if seqs is None else PageMap._list(seqs, B, "seqs"),
-                                  PageMap._list(lens, B, "lens"), int(planes), C.byref(o),
-                                  self._rows(out, (B, M, Hq, D), "out"), ws.data_ptr(), ws.numel(), on),
-               "nq_page_attn")
+        _check(lib().nq_page_attn(self.ptr, layer, pmap.ptr, *given, C.byref(o), self._rows(out, (B, M, Hq, D), "out"),
+                                  ws.data_ptr(), ws.numel(), on), "nq_page_attn")
         return out
 
 
