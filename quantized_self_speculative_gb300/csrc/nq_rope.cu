@@ -127,6 +127,17 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const Vec<E> &x)
     else *reinterpret_cast<uint32_t *>(p) = bf_pack(x.v[0], x.v[1]);
 }
 
+// sin and cos of a / 2^32 turns: the nearest quarter turn exactly, the rest, at
+// most an eighth, in fp32 (off by 2^-28 turns at most).
+__device__ __forceinline__ void turn_of(uint32_t a, float &sn, float &cs)
+{
+    const uint32_t k = (a + 0x20000000u) >> 30;
+    float s, c;
+    sincospif(__int2float_rn(static_cast<int>(a - (k << 30))) * 4.656612873077393e-10f, &s, &c);
+    sn = __uint_as_float(__float_as_uint(k & 1 ? c : s) ^ (k & 2) << 30);
+    cs = __uint_as_float(__float_as_uint(k & 1 ? s : c) ^ ((k + 1) & 2) << 30);
+}
+
 // This lane's part of a token's rotation: y[e] = c[e] x[e] + s[e] partner[e].
 template <int E>
 struct Turn {
@@ -152,8 +163,7 @@ __device__ __forceinline__ Turn<E> make_turn(const Rope &R, int pos, int lane, b
     for (int k = 0; k < A; ++k) {
         const int i = A * lane + k;
         const unsigned long long x = static_cast<unsigned long long>(static_cast<long long>(pos)) * (i < hr ? R.rates[i] : 0ull);
-        // half turns in [-1, 1)
-        sincospif(__int2float_rn(static_cast<int>(x >> 32)) * 4.656612873077393e-10f, &sn[k], &cs[k]);
+        turn_of(static_cast<uint32_t>(x >> 32), sn[k], cs[k]);
         cs[k] *= R.mscale;
         sn[k] *= inverse ? -R.mscale : R.mscale;
     }
