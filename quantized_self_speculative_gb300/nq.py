@@ -70,6 +70,8 @@ class nq_attn_opts(C.Structure):
 def lib():
     """Load libnq.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
