@@ -406,7 +406,7 @@ typedef struct {
     int32_t rot_dim;
     int32_t layout;   /* nq_rope_layout */
     float mscale;
-    int32_t pad;
+    float mscale_lo;  /* what the exact factor has beyond its fp32 value: added to it, 0 for none */
     const uint64_t *rates;
 } nq_rope_plan;
 

@@ -4,9 +4,8 @@
 //
 // A pair turns by a = pos * w.  The rate w / (2 pi) is a 64-bit fraction of a
 // turn, so frac(pos * rate) is one integer product: no precision is lost at
-// far positions, and no table of angles is read.  sin and cos are taken of the
-// fraction's top 32 bits, once per token and lane, and used for every head
-// that the warp handles.
+// far positions, and no table of angles is read.  sin and cos of that fraction
+// are taken once per token and lane and used for every head that the warp handles.
 //
 // One warp takes one token and a run of heads, kBatch rows at a time: all their
 // loads are issued before the first row is turned.  Lane l holds elements
@@ -31,7 +30,7 @@ constexpr int kWarps = 4;               // short CTAs end together: append of 81
 
 struct Rope {
     int rot, layout;
-    float mscale;
+    float mscale, mscale_lo;
     const unsigned long long *rates;
 };
 
@@ -127,13 +126,38 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const Vec<E> &x)
     else *reinterpret_cast<uint32_t *>(p) = bf_pack(x.v[0], x.v[1]);
 }
 
-// sin and cos of a / 2^32 turns: the nearest quarter turn exactly, the rest, at
-// most an eighth, in fp32 (off by 2^-28 turns at most).
-__device__ __forceinline__ void turn_of(uint32_t a, float &sn, float &cs)
+// v (m + lo) rounded once (the product's low part is off by far less than a step).
+__device__ __forceinline__ float scaled(uint32_t v, float m, float lo)
 {
-    const uint32_t k = (a + 0x20000000u) >> 30;
-    float s, c;
-    sincospif(__int2float_rn(static_cast<int>(a - (k << 30))) * 4.656612873077393e-10f, &s, &c);
+    const float hi = __uint2float_rz(v), rest = __uint2float_rn(v - __float2uint_rz(hi));      // both exact
+    return __fmaf_rn(hi, m, __fmaf_rn(hi, lo, rest * m));
+}
+// sin and cos of x / 2^64 turns times m + lo, rounded to fp32 nearly always correctly (999 of
+// 1000, else by one step): so keys come out bit for bit as from angles in 64 bits
+// and hardly a code next to a border falls to its other side.  The nearest quarter
+// turn is exact; the rest, t eighths of a turn (at most 1), goes through the Taylor
+// series of sin and cos of (pi / 4) t in 32-bit fixed point, each coefficient
+// (pi / 4)^n / n! 2^32, the sine from a t that is shifted to its first bit.
+__device__ __forceinline__ void turn_of(unsigned long long x, float scale, float scale_lo, float &sn, float &cs)
+{
+    const uint32_t k = static_cast<uint32_t>((x + (1ull << 61)) >> 62);
+    const long long r = static_cast<long long>(x - (static_cast<unsigned long long>(k) << 62));
+    const unsigned long long m = r < 0 ? 0ull - static_cast<unsigned long long>(r) : static_cast<unsigned long long>(r);
+    const uint32_t t = static_cast<uint32_t>((m - (m >> 61)) >> 29), z = __umulhi(t, t);
+    uint32_t p = 1346u - __umulhi(8u, z);
+    p = 157094u - __umulhi(p, z);
+    p = 10696163u - __umulhi(p, z);
+    p = 346799334u - __umulhi(p, z);
+    p = 3373259426u - __umulhi(p, z);
+    const int n = __clzll(static_cast<long long>(m | 1ull));
+    const uint32_t first = static_cast<uint32_t>((m << n) >> 32);
+    float s = scaled(__umulhi(first, p), scale, scale_lo) * __uint_as_float(static_cast<uint32_t>(98 - n) << 23);      // 2^(-29 - n)
+    if (r < 0) s = -s;
+    uint32_t q = 15423u - __umulhi(106u, z);
+    q = 1400124u - __umulhi(q, z);
+    q = 68093890u - __umulhi(q, z);
+    q = 1324675879u - __umulhi(q, z);
+    const float c = scaled(~__umulhi(z, q), scale, scale_lo) * 2.3283064365386963e-10f;
     sn = __uint_as_float(__float_as_uint(k & 1 ? c : s) ^ (k & 2) << 30);
     cs = __uint_as_float(__float_as_uint(k & 1 ? s : c) ^ ((k + 1) & 2) << 30);
 }
@@ -163,9 +187,8 @@ __device__ __forceinline__ Turn<E> make_turn(const Rope &R, int pos, int lane, b
     for (int k = 0; k < A; ++k) {
         const int i = A * lane + k;
         const unsigned long long x = static_cast<unsigned long long>(static_cast<long long>(pos)) * (i < hr ? R.rates[i] : 0ull);
-        turn_of(static_cast<uint32_t>(x >> 32), sn[k], cs[k]);
-        cs[k] *= R.mscale;
-        sn[k] *= inverse ? -R.mscale : R.mscale;
+        turn_of(x, R.mscale, R.mscale_lo, sn[k], cs[k]);
+        if (inverse) sn[k] = -sn[k];
     }
     const int i0 = t.any && !first ? e0 - hr : e0;
 #pragma unroll
@@ -190,8 +213,10 @@ __device__ __forceinline__ Vec<E> turn(const Turn<E> &t, const Vec<E> &x)
     }
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
-        const float2 z = f2_unpack(f2_fma(f2_pack(t.c[e], t.c[e + 1]), f2_pack(x.v[e], x.v[e + 1]),
-                                          f2_fma(f2_pack(t.s[e], t.s[e + 1]), f2_pack(q.v[e], q.v[e + 1]), f2_pack(0.0f, 0.0f))));
+        // both products rounded, as the formula reads: the codes of a key do not depend on how it is evaluated
+        const unsigned long long zero = f2_pack(0.0f, 0.0f);
+        const float2 z = f2_unpack(f2_add(f2_fma(f2_pack(t.c[e], t.c[e + 1]), f2_pack(x.v[e], x.v[e + 1]), zero),
+                                          f2_fma(f2_pack(t.s[e], t.s[e + 1]), f2_pack(q.v[e], q.v[e + 1]), zero)));
         y.v[e] = t.any ? z.x : x.v[e];         // also where the partner, unused, is not finite
         y.v[e + 1] = t.any ? z.y : x.v[e + 1];
     }
@@ -462,7 +487,7 @@ nq_status rope_of(const nq_rope_plan *r, int head_dim, Rope &out)
     if (!r || !r->rates || !(r->layout == NQ_ROPE_HALF || r->layout == NQ_ROPE_INTERLEAVED)) return NQ_ERR_ARG;
     if (r->rot_dim < 8 || r->rot_dim % 8 != 0 || r->rot_dim > head_dim) return NQ_ERR_SHAPE;
     if (!aligned16(r->rates)) return NQ_ERR_ALIGN;
-    out = Rope{r->rot_dim, r->layout, r->mscale, reinterpret_cast<const unsigned long long *>(r->rates)};
+    out = Rope{r->rot_dim, r->layout, r->mscale, r->mscale_lo, reinterpret_cast<const unsigned long long *>(r->rates)};
     return NQ_OK;
 }
 // Heads per warp: up to 48 for prompts, where the sines of a token serve them all,

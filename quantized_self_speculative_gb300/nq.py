@@ -8,6 +8,7 @@ there is no fallback: a missing library raises immediately.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 import threading
 from dataclasses import dataclass
@@ -48,7 +49,7 @@ class nq_kv_cache(C.Structure):
 
 
 class nq_rope_plan(C.Structure):
-    _fields_ = [("rot_dim", C.c_int32), ("layout", C.c_int32), ("mscale", C.c_float), ("pad", C.c_int32),
+    _fields_ = [("rot_dim", C.c_int32), ("layout", C.c_int32), ("mscale", C.c_float), ("mscale_lo", C.c_float),
                 ("rates", C.c_void_p)]
 
 
@@ -556,8 +557,9 @@ class Rope:
         _check(lib().nq_rope_rates(rot_dim, float(theta), kinds.index(scaling), float(factor), int(old_len),
                                    rates.data_ptr(), C.byref(ms)), "nq_rope_rates")
         self.rot_dim, self.mscale = rot_dim, ms.value
+        lo = 0.1 * math.log(factor) + 1.0 - ms.value if scaling == "parts" else 0.0
         self.rates = rates.to(device or torch.device("cuda"))
-        self.struct = nq_rope_plan(rot_dim, layouts.index(layout), ms.value, 0, self.rates.data_ptr())
+        self.struct = nq_rope_plan(rot_dim, layouts.index(layout), ms.value, lo, self.rates.data_ptr())
         self.ref = C.byref(self.struct)
 
 
