@@ -13,8 +13,8 @@
 // lane and a half pair is one shuffle away.
 //
 // Measured (GB300, 2070 MHz).  Rotation, 16384 tokens x 32 heads x 128, bf16 to
-// bf16: 43 us, 6.3 TB/s, HBM bound (92% of the copy rate).  Append, 8191 tokens,
-// 32 + 32 + 32 heads x 128, fp32 to nested groups of 64: 106 us, 5.1 TB/s, bound
+// bf16: 43.5 us, 6.2 TB/s, HBM bound (91% of the copy rate).  Append, 8191 tokens,
+// 32 + 32 + 32 heads x 128, fp32 to nested groups of 64: 110 us, 4.9 TB/s, bound
 // by instruction issue (some 110 warp instructions per row: maximum over the
 // group, two correctly rounded quotients, the codes).  Read of the same rows:
 // 44 us, 4.6 TB/s, bound by latency: 64-byte pieces of four heads at a time.
@@ -132,11 +132,12 @@ __device__ __forceinline__ float scaled(uint32_t v, float m, float lo)
     const float hi = __uint2float_rz(v), rest = __uint2float_rn(v - __float2uint_rz(hi));      // both exact
     return __fmaf_rn(hi, m, __fmaf_rn(hi, lo, rest * m));
 }
-// sin and cos of x / 2^64 turns times m + lo, rounded to fp32 nearly always correctly (999 of
-// 1000, else by one step): so keys come out bit for bit as from angles in 64 bits
-// and hardly a code next to a border falls to its other side.  The nearest quarter
-// turn is exact; the rest, t eighths of a turn (at most 1), goes through the Taylor
-// series of sin and cos of (pi / 4) t in 32-bit fixed point, each coefficient
+// sin and cos of x / 2^64 turns times m + lo, rounded to fp32 correctly in 997 of
+// 1000 cases, else a step off: keys come out as from angles in 64 bits, and hardly a
+// code next to a border falls to its other side.  (sincospif of a rounded angle is
+// 4 us faster in an append of 110 us, and a step off half the time.)  The nearest
+// quarter turn is exact; the rest, t eighths of a turn (at most 1), goes through the
+// Taylor series of sin and cos of (pi / 4) t in 32-bit fixed point, each coefficient
 // (pi / 4)^n / n! 2^32, the sine from a t that is shifted to its first bit.
 __device__ __forceinline__ void turn_of(unsigned long long x, float scale, float scale_lo, float &sn, float &cs)
 {
@@ -492,7 +493,7 @@ nq_status rope_of(const nq_rope_plan *r, int head_dim, Rope &out)
 }
 // Heads per warp: up to 48 for prompts, where the sines of a token serve them all,
 // and down to one, so that a small call spreads over the machine (16 warps per SM).
-// Append of 8191 tokens, 96 heads: 106 us with two runs, 116 with three (of q, k
+// Append of 8191 tokens, 96 heads (before the fixed-point sines, 4 us): 106 us with two runs, 116 with three (of q, k
 // and v rows, which cost unlike), 128 with twelve of 8.  Of 144 tokens, 48 heads:
 // 6.7 us; 12.1 in runs of 32, 8.2 with twice the warps.  Rotating 16384 tokens of
 // 32 heads: 43 us whole, 46 in runs of 8.
