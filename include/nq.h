@@ -612,6 +612,18 @@ NQ_API nq_status spec_accept_greedy_noalloc(const int32_t *draft, const float *t
  */
 NQ_API nq_status nq_selftest_bounded_wait(uint32_t limit_us, cudaStream_t stream);
 
+/*
+ * The same for nq_page_attn: its arguments, but what feeds each ring of cache
+ * blocks stops after `steps` (>= 0) steps, and waits are limited to limit_us
+ * (1 .. 1,000,000).  Where more steps than that are needed the waits give up
+ * and set NQ_DEV_TIMEOUT; out is then unspecified, and nothing outside out and
+ * the workspace is written.
+ */
+NQ_API nq_status nq_selftest_page_attn(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,
+                                       int64_t q_stride, int batch, int M, int heads_q, const int32_t *seqs,
+                                       const int32_t *len, int planes, const nq_attn_opts *opts, uint16_t *out, void *ws,
+                                       size_t ws_bytes, int steps, uint32_t limit_us, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 NQ_API const char *nq_status_string(int status);
 

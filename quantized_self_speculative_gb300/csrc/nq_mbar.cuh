@@ -64,20 +64,15 @@ static __device__ __noinline__ bool mbar_wait_until(uint32_t bar, uint32_t parit
         }
     }
 }
-__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                               unsigned int *status)
-{
-    return mbar_wait_until(bar, parity, abort_flag, status, kWaitNs);
-}
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                          unsigned int *status)
+                                          unsigned int *status, unsigned long long limit_ns = kWaitNs)
 {
-    return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort_flag, status);
+    return mbar_test(bar, parity) || mbar_wait_until(bar, parity, abort_flag, status, limit_ns);
 }
 // The same for hand-overs inside a step, where the sleep's wake-up would be most
 // of the wait: try_wait without a time hint for some microseconds, then as above.
 __device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                               unsigned int *status)
+                                               unsigned int *status, unsigned long long limit_ns = kWaitNs)
 {
 #pragma unroll 1
     for (int i = 0; i < 256; ++i) {
@@ -86,7 +81,36 @@ __device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, vo
                      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
         if (ok) return true;
     }
-    return mbar_wait_slow(bar, parity, abort_flag, status);
+    return mbar_wait_until(bar, parity, abort_flag, status, limit_ns);
+}
+// A warp's wait for stage st of a ring of bulk copies of which it has the n from st on
+// in flight: true on every lane once the stage is there.  Where that wait gives up, or
+// one of the CTA has, false once the n copies have landed (or waits for them have run
+// out too).
+__device__ __forceinline__ bool ring_wait(uint32_t bar, int st, uint32_t parity, int n, int stages, volatile int *abort_flag,
+                                          unsigned int *status, unsigned long long limit_ns)
+{
+    if (__all_sync(0xffffffffu, mbar_test(bar + 8 * st, parity))) return true;
+    unsigned long long t0 = global_ns();
+    bool ok = true;
+#pragma unroll 1
+    for (bool mine = *abort_flag == 0; mine && !mbar_try(bar + 8 * st, parity);)
+        if (*abort_flag || global_ns() - t0 > limit_ns) mine = ok = false;
+    ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+    if (ok) return true;
+    *abort_flag = 1;
+    set_status(status, NQ_DEV_TIMEOUT);
+#pragma unroll 1
+    for (t0 = global_ns(); n > 0 && global_ns() - t0 <= limit_ns;)
+        if (mbar_try(bar + 8 * st, parity)) {
+            --n;
+            if (++st == stages) {
+                st = 0;
+                parity ^= 1u;
+            }
+        }
+    __syncwarp();
+    return false;
 }
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {

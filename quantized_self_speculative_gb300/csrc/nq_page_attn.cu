@@ -93,13 +93,11 @@ attn_kernel(const __grid_constant__ AttnArgs A)
     if (threadIdx.x < kWarps * Q::STAGES) mbar_init(smem_u32(bars + threadIdx.x), 1);
     if (threadIdx.x == 0) {
         abort_flag = 0;
+        A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);             // until the CTA has left a part for the join
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const Run run = find_run<SR, kThreads, D>(A, segs, kMinRun);
-    if (run.f0 >= run.f1) {
-        if (threadIdx.x == 0) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        return;
-    }
+    if (run.f0 >= run.f1) return;
 
     unsigned char *ring = sm + warp * (Q::STAGES * Q::STAGE);
     const uint32_t bar_s = smem_u32(bars + warp * Q::STAGES);
@@ -232,7 +230,7 @@ attn_kernel(const __grid_constant__ AttnArgs A)
 
         // ================================================= the warp's next step of it
         if (fu < use.end) {
-            mbar_wait(bar_s + 8 * stage, phase, &abort_flag, A.status);
+            feed.wait(A, bar_s, stage, phase, Q::STAGES, filled, &abort_flag);
             const int row0 = use.s.lo + (fu - use.base) * SR;
             const unsigned char *sp = ring + stage * Q::STAGE;
             const bool masked = row0 < all_lo || row0 + SR > all_hi;
@@ -606,7 +604,7 @@ attn_kernel(const __grid_constant__ AttnArgs A)
         }
         if (warp == 0) {
             const bool starts = use.base >= run.f0, ends = use.base + use.s.steps <= run.f1, whole = starts && ends;
-            if (!ends && starts && lane == 0)
+            if (!ends && starts && lane == 0 && *const_cast<volatile int *>(&abort_flag) == 0)
                 A.info[blockIdx.x] = make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / run.per, 0);
             const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0);
             constexpr float unit = FMT == kKv8 ? 0.0625f : 1.0f;                 // KV8's codes are 16 times the value
@@ -654,11 +652,7 @@ attn_kernel(const __grid_constant__ AttnArgs A)
                     }
                 }
         }
-        if (use.end >= use.stop) {
-            // the run ends with its last segment, or inside one that an earlier run began
-            if (threadIdx.x == 0 && (use.base + use.s.steps <= run.f1 || use.base < run.f0)) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
-            break;
-        }
+        if (use.end >= use.stop) break;
         use.next(A, segs);
         fresh = true;
     }
@@ -820,10 +814,11 @@ extern "C" size_t nq_page_attn_workspace_bytes(int M, int heads_q, int heads_kv,
     return nq::ws_of(M * (heads_q / heads_kv), head_dim).total;
 }
 
-extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,
-                                  int64_t q_stride, int batch, int M, int heads_q, const int32_t *seqs,
-                                  const int32_t *len, int planes, const nq_attn_opts *opts, uint16_t *out, void *ws,
-                                  size_t ws_bytes, cudaStream_t stream)
+// starve and wait_ns as in AttnArgs
+static nq_status page_attn(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q, int64_t q_stride,
+                           int batch, int M, int heads_q, const int32_t *seqs, const int32_t *len, int planes,
+                           const nq_attn_opts *opts, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream, int starve,
+                           unsigned long long wait_ns)
 {
     nq::AttnArgs A{};
     const nq_status st = nq::pool_map_of(pool, map, A.p, A.m, false);
@@ -863,6 +858,8 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
     A.window = opts->window;
     A.slopes = opts->slopes;
     A.out = reinterpret_cast<__nv_bfloat16 *>(out);
+    A.wait_ns = wait_ns;
+    A.starve = starve;
     uint8_t *wb = static_cast<uint8_t *>(ws);
     A.info = reinterpret_cast<int4 *>(wb);
     A.part_ml = reinterpret_cast<float *>(wb + w.ml);
@@ -876,4 +873,23 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
     else e = nq::launch_d<nq::kKv8>(cols / 8, A, stream, &grid);
     if (e != cudaSuccess) return NQ_ERR_CUDA;
     return nq::cuda_status(nq::launch_join(A, grid, stream));
+}
+
+extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,
+                                  int64_t q_stride, int batch, int M, int heads_q, const int32_t *seqs,
+                                  const int32_t *len, int planes, const nq_attn_opts *opts, uint16_t *out, void *ws,
+                                  size_t ws_bytes, cudaStream_t stream)
+{
+    return page_attn(pool, layer, map, q, q_stride, batch, M, heads_q, seqs, len, planes, opts, out, ws, ws_bytes, stream, -1,
+                     nq::kWaitNs);
+}
+
+extern "C" nq_status nq_selftest_page_attn(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,
+                                           int64_t q_stride, int batch, int M, int heads_q, const int32_t *seqs,
+                                           const int32_t *len, int planes, const nq_attn_opts *opts, uint16_t *out, void *ws,
+                                           size_t ws_bytes, int steps, uint32_t limit_us, cudaStream_t stream)
+{
+    if (steps < 0 || limit_us < 1 || limit_us > 1000000u) return NQ_ERR_ARG;
+    return page_attn(pool, layer, map, q, q_stride, batch, M, heads_q, seqs, len, planes, opts, out, ws, ws_bytes, stream, steps,
+                     limit_us * 1000ull);
 }

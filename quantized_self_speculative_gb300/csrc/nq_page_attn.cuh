@@ -29,9 +29,11 @@ struct AttnArgs {
     int window;
     const float *slopes;
     __nv_bfloat16 *out;
-    int4 *info;                         // per CTA: the segment it leaves to later CTAs
+    int4 *info;                         // per CTA: the segment it leaves to later CTAs; x = -1: none, or it gave up
     float *part_o, *part_ml;
     unsigned int *status;
+    unsigned long long wait_ns;         // limit of a wait on a barrier
+    int starve;                         // steps after which each feed stops (a diagnostic); -1: none
 };
 
 // Query row of vector v = row * G + head of the group (v, G <= 2^16).
@@ -327,6 +329,10 @@ struct Feed {
     __device__ __forceinline__ void start(const AttnArgs &A, const Walk<SR> &at, int segs, int f, uint32_t ring_, uint32_t bar_)
     {
         w = at;
+        if (A.starve >= 0) {
+            w.stop = static_cast<int>(min(static_cast<long long>(w.stop), f + static_cast<long long>(A.starve) * STRIDE));
+            w.end = min(w.end, w.stop);
+        }
         ring = ring_;
         bar = bar_;
         lp = 31 - __clz(A.m.P);
@@ -355,6 +361,12 @@ struct Feed {
         row += STRIDE * SR;
         if (--left == 0) aim(A, segs, w.base + (row - w.s.lo) / SR);
         look();
+    }
+    // Waits for stage st, of a ring in which `filled` hold or await a step.  Where that gives
+    // up, nothing more is issued: the CTA goes on to the end of its run without waiting.
+    __device__ __forceinline__ void wait(const AttnArgs &A, uint32_t bar_, int st, uint32_t phase, int stages, int &filled, int *abort_flag)
+    {
+        if (!ring_wait(bar_, st, phase, filled, stages, abort_flag, A.status, A.wait_ns)) left = filled = 0;
     }
 };
 

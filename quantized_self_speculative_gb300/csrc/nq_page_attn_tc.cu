@@ -74,6 +74,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
     auto bar = [&](int i) { return bar0 + 8u * i; };
     if (threadIdx.x == 0) {
         abort_flag = keep_tmem = 0;
+        A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);             // until the CTA has left a part for the join
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(kRawFull + i), 1);
             mbar_init(bar(kRawEmpty + i), kDecodeWarps);
@@ -90,10 +91,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const Run run = find_run<SR, kThreads, D>(A, segs, kMinRun);
-    if (run.f0 >= run.f1) {
-        if (threadIdx.x == 0) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        return;
-    }
+    if (run.f0 >= run.f1) return;
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(kTmem) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -103,7 +101,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     unsigned char *scales = sm + kBufs * Q::BUF, *ring = scales + kBufs * Q::SCALES;
-    auto wait = [&](int i, int phase) { return mbar_wait_fast(bar(i), static_cast<uint32_t>(phase) & 1u, &abort_flag, A.status); };
+    auto wait = [&](int i, int phase) { return mbar_wait_fast(bar(i), static_cast<uint32_t>(phase) & 1u, &abort_flag, A.status, A.wait_ns); };
     const int steps = run.f1 - run.f0;
     Walk<SR> use;
     use.open(A, run.b, run.base, run.f0, run.f1);
@@ -113,14 +111,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
         Feed<FMT, D, 1, BLKS, 1> feed;
         feed.start(A, use, segs, run.f0, smem_u32(ring), bar(kRawFull));
         int i = 0;
-        for (; i < steps; ++i) {
+        for (; i < steps && feed.left > 0; ++i) {
             const int st = i % Q::STAGES;
             if (!__all_sync(0xffffffffu, wait(kRawEmpty + st, (i / Q::STAGES & 1) ^ 1))) break;
             feed.issue(A, segs, st);
         }
         // every copy issued has landed before the CTA may exit
         volatile int never = 0;
-        for (int k = max(0, i - Q::STAGES); k < i; ++k) mbar_wait(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status);
+        for (int k = max(0, i - Q::STAGES); k < i; ++k) mbar_wait(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
     } else if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ================================================= decode
         const int dw = warp - kSoftWarps, g = lane >> 2, t = lane & 3;
@@ -269,7 +267,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
             else mbar_arrive(bar(kDrain));
             __syncwarp();
             volatile int never = 0;
-            const bool drained = mbar_wait(bar(kDrain), 0, &never, A.status);
+            const bool drained = mbar_wait(bar(kDrain), 0, &never, A.status, A.wait_ns);
             if (!__all_sync(0xffffffffu, drained) && lane == 0) keep_tmem = 1;
         }
     } else {
@@ -477,8 +475,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                 }
             }
             if (i + 1 == steps) {
-                if (threadIdx.x == 0)
-                    A.info[blockIdx.x] = !ends && starts ? make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / run.per, 0) : make_int4(-1, 0, 0, 0);
+                if (threadIdx.x == 0 && !ends && starts)
+                    A.info[blockIdx.x] = make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / run.per, 0);
             } else {
                 use.next(A, segs);
                 fresh = true;

@@ -71,13 +71,11 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
     if (threadIdx.x < Q::STAGES) mbar_init(smem_u32(bars + threadIdx.x), 1);
     if (threadIdx.x == 0) {
         abort_flag = 0;
+        A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);             // until the CTA has left a part for the join
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const Run run = find_run<SR, THREADS, D>(A, segs, kMinRun);
-    if (run.f0 >= run.f1) {
-        if (threadIdx.x == 0) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        return;
-    }
+    if (run.f0 >= run.f1) return;
     unsigned char *decoded = sm, *ring = sm + 2 * Q::DECODED;
     const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(bars);
     Walk<SR> use;
@@ -98,7 +96,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
     // step number f of the run into buffer f % 2: thread = (row, quarter of the row) of K, then of V
     int stage = 0;                            // of the next step to be waited for
     uint32_t phase = 0;
-    auto wait = [&]() { mbar_wait(bar_s + 8 * stage, phase, &abort_flag, A.status); };
+    auto wait = [&]() { feed.wait(A, bar_s, stage, phase, Q::STAGES, filled, &abort_flag); };
     auto advance = [&]() {
         if (++stage == Q::STAGES) {
             stage = 0;
@@ -446,8 +444,8 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
                 }
         }
         if (f + 1 == run.f1) {
-            if (threadIdx.x == 0)
-                A.info[blockIdx.x] = !ends && starts ? make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / run.per, 0) : make_int4(-1, 0, 0, 0);
+            if (threadIdx.x == 0 && !ends && starts && *const_cast<volatile int *>(&abort_flag) == 0)
+                A.info[blockIdx.x] = make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / run.per, 0);
         } else {
             use.next(A, segs);
             fresh = true;

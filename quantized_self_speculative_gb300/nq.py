@@ -142,6 +142,8 @@ def lib():
                 getattr(L, name).restype = i32
             L.nq_selftest_bounded_wait.argtypes = [C.c_uint32, vp]
             L.nq_selftest_bounded_wait.restype = i32
+            L.nq_selftest_page_attn.argtypes = [PP, i32, PM, vp, i64, i32, i32, i32, vp, vp, i32, AO, vp, vp, sz, i32, C.c_uint32, vp]
+            L.nq_selftest_page_attn.restype = i32
             for name in ("nq_packed_bytes", "nq_pack_weights", "nq_draft_gemv", "nq_verify_gemm",
                          "nq_draft_gemv_batch", "nq_verify_gemm_batch", "spec_accept_greedy",
                          "spec_accept_sample", "nq_get_device_status"):
