@@ -20,25 +20,26 @@ constexpr int kTile = kCopyThreads * kCopyUnroll;                // 16-byte unit
 
 // ---------------------------------------------------------------- block scan
 // Exclusive prefix sum of v over the block (1024 threads), total in `sum`.
-__device__ __forceinline__ int block_scan(int v, int *sm, int &sum)
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *sm, T &sum)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    T x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     if (lane == 31) sm[warp] = x;
     __syncthreads();
-    int w = sm[lane];                                            // 32 warps
+    T w = sm[lane];                                              // 32 warps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        const T y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
     }
     sum = __shfl_sync(0xffffffffu, w, 31);
-    const int before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
+    const T before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
     __syncthreads();                                             // sm may be written again
     return before + x - v;
 }
@@ -209,6 +210,7 @@ reserve_kernel(Map m, const int32_t *__restrict__ seqs, const int32_t *__restric
                const int32_t *__restrict__ last, int n, int32_t *__restrict__ granted, int32_t *ws, unsigned int *status)
 {
     __shared__ int sm[32], sm_copies;
+    __shared__ long long sm_wide[32];
     asm volatile("griddepcontrol.launch_dependents;");
     const ReserveWs R = reserve_ws(ws, m.N, n);
     const int tid = threadIdx.x;
@@ -238,8 +240,9 @@ reserve_kernel(Map m, const int32_t *__restrict__ seqs, const int32_t *__restric
         }
     }
     __syncthreads();
-    // ---- pages wanted per request; an entry to be copied is marked -(id + 2)
-    int total = 0;
+    // ---- pages wanted per request; an entry to be copied is marked -(id + 2).  The requests of a call may
+    // want more pages than 32 bits hold: a sum past them is kept as the largest number, which no pool covers
+    long long total = 0;
     for (int i0 = 0; i0 < n; i0 += kScanThreads) {
         const int i = i0 + tid;
         int c = 0;
@@ -259,9 +262,9 @@ reserve_kernel(Map m, const int32_t *__restrict__ seqs, const int32_t *__restric
             }
             c += max(w.need - w.held, 0);
         }
-        int sum;
-        const int pre = block_scan(c, sm, sum);
-        if (i < n) R.before[i] = total + pre;
+        long long sum;
+        const long long pre = total + block_scan(static_cast<long long>(c), sm_wide, sum);
+        if (i < n) R.before[i] = static_cast<int>(min(pre, 0x7fffffffll));
         total += sum;
     }
     // ---- the lowest free ids, until there are enough
@@ -289,7 +292,7 @@ reserve_kernel(Map m, const int32_t *__restrict__ seqs, const int32_t *__restric
         int32_t *t = m.table + static_cast<size_t>(max(w.s, 0)) * m.W;
         int c = max(w.need - w.held, 0);
         for (int j = w.lo; j < min(w.held, w.need); ++j) c += t[j] < -1;
-        const bool give = w.ok && pre + c <= found;
+        const bool give = w.ok && static_cast<long long>(pre) + c <= found;
         if (w.ok && !give) set_status(status, NQ_DEV_POOL_FULL);
         int k = pre;
         for (int j = w.lo; j < min(w.held, w.need); ++j) {
