@@ -506,7 +506,9 @@ NQ_API nq_status nq_page_reserve(const nq_page_map *map, const nq_page_pool *poo
 NQ_API nq_status nq_page_fork(const nq_page_map *map, const int32_t *src, const int32_t *dst, const int32_t *rows,
                               int n, void *ws, size_t ws_bytes, cudaStream_t stream);
 
-/* Slot seqs[i] keeps the pages of its first rows[i] rows and releases the others (rows = 0: all of them). */
+/* Slot seqs[i] keeps the pages of its first rows[i] rows and releases the others (rows = 0: all of them).
+ * A slot that is named more than once keeps the least of its rows.  A slot outside the map, or an entry that
+ * names a page outside the pool, sets NQ_DEV_BAD_PAGE. */
 NQ_API nq_status nq_page_truncate(const nq_page_map *map, const int32_t *seqs, const int32_t *rows, int n,
                                   cudaStream_t stream);
 

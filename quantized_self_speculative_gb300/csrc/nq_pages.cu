@@ -57,7 +57,8 @@ __global__ void init_kernel(Map m)
 }
 
 // ---------------------------------------------------------------- truncate
-// One CTA per slot.
+// One CTA per request.  A slot may be named more than once: an entry is taken out by an
+// exchange, so that one CTA releases its page whatever the others do, and `held` only falls.
 __global__ void __launch_bounds__(kMapThreads)
 truncate_kernel(Map m, const int32_t *__restrict__ seqs, const int32_t *__restrict__ rows, unsigned int *status)
 {
@@ -69,13 +70,13 @@ truncate_kernel(Map m, const int32_t *__restrict__ seqs, const int32_t *__restri
     const int held = min(max(m.held[s], 0), m.W), keep = min(pages_of(rows[blockIdx.x], m.P), held);
     int32_t *t = m.table + static_cast<size_t>(s) * m.W;
     for (int j = keep + threadIdx.x; j < held; j += kMapThreads) {
-        const int p = t[j];
+        const int p = atomicExch(t + j, -1);
         if (p >= 0 && p < m.N) atomicSub(m.ref + p, 1);
-        else set_status(status, NQ_DEV_BAD_PAGE);
-        t[j] = -1;
+        else if (p != -1) set_status(status, NQ_DEV_BAD_PAGE);   // -1: another request for the slot has been here
     }
+    // every thread has read `held`: the first CTA to lower it past an entry has taken that entry out
     __syncthreads();
-    if (threadIdx.x == 0) m.held[s] = keep;
+    if (threadIdx.x == 0) atomicMin(m.held + s, keep);
 }
 
 // ---------------------------------------------------------------- fork

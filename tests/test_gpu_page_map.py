@@ -1,9 +1,12 @@
 """Calls on a page map and a pool at their edges: a slot named twice, requests
 whose total passes 32 bits, empty lists, a pool made on a stream."""
+import random
+
 import pytest
 import torch
 
-from test_gpu_pages import i32
+from paged_helpers import HostMap
+from test_gpu_pages import i32, same
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +26,27 @@ def test_requests_past_32_bits_of_pages(nq):
     got = m.reserve(None, seqs[:17].contiguous(), zero[:17].contiguous(), i32([30] + [W * P] * 16))
     assert got.tolist() == [1] + [0] * 16 and m.table[0, :3].tolist() == [3, 4, -1]
     assert nq.device_status() == nq.NQ_DEV_POOL_FULL
+
+
+def test_truncate_names_a_slot_twice(nq):
+    """Each page is released once, and the least of the rows stays."""
+    S, W, P = 40, 30, 16
+    N = S * W
+    r = random.Random(5)
+    for step in range(12):
+        m, h = nq.PageMap(S, W, N, P), HostMap(S, W, N, P)
+        seqs = list(range(S // 2))
+        last = [r.randint(1, W * P) for _ in seqs]
+        m.reserve(None, i32(seqs), i32([0] * len(seqs)), i32(last))
+        h.reserve(seqs, [0] * len(seqs), last)
+        src, rows = [r.choice(seqs) for _ in seqs], [r.randint(0, W * P) for _ in seqs]
+        rows = [min(x, last[s]) for x, s in zip(rows, src)]
+        m.fork(i32(src), i32([s + S // 2 for s in seqs]), i32(rows))
+        h.fork(src, [s + S // 2 for s in seqs], rows)
+        same(m, h)
+        names = [r.choice([0, 1, 5, 20, 21, r.randrange(S)]) for _ in range(S)]
+        keep = [r.randint(0, W * P) for _ in names]
+        m.truncate(i32(names), i32(keep))
+        h.truncate(names, keep)
+        same(m, h)
+        assert nq.device_status() == 0
