@@ -173,8 +173,9 @@ struct Codes {
 template <int FMT> __host__ __device__ constexpr float odd_scale() { return FMT == kKv4 ? 16.0f : 1.0f; }
 
 // ---------------------------------------------------------------- sequences
-// The rows [lo, hi) of a sequence that any of its queries sees, lo a multiple
-// of SR, as steps.
+// The rows [lo, hi) of a sequence that any of its queries sees, as steps of SR.
+// lo is a multiple of 16 (a block lies in one page), so that no page wholly before
+// the window is looked up; steps may begin anywhere in a page.
 struct Seq {
     int slot, lo, hi, steps;
 };
@@ -196,7 +197,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &A, int b, bool report)
     }
     s.hi = max(n, 0);
     // the first query's own row is hi - M
-    s.lo = A.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(s.hi) - A.M - A.window + 1)) / SR * SR : 0;
+    s.lo = A.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(s.hi) - A.M - A.window + 1)) / 16 * 16 : 0;
     s.steps = s.hi > s.lo ? (s.hi - s.lo + SR - 1) / SR : 0;
     return s;
 }
