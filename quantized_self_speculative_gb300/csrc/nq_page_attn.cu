@@ -213,10 +213,10 @@ attn_kernel(const __grid_constant__ AttnArgs A)
         }
         // rows that every query of the tile sees: no mask needed there
         all_hi = use.s.hi - A.M + m_lo + 1;
-        all_lo = A.window > 0 ? use.s.hi - A.M + m_hi - A.window + 1 : 0;
+        all_lo = first_seen(A, use.s.hi - A.M + m_hi);
         // rows that any of them sees
         any_hi = use.s.hi - A.M + m_hi + 1;
-        any_lo = A.window > 0 ? use.s.hi - A.M + m_lo - A.window + 1 : 0;
+        any_lo = first_seen(A, use.s.hi - A.M + m_lo);
 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -483,7 +483,7 @@ attn_kernel(const __grid_constant__ AttnArgs A)
                             }
                             if (__any_sync(0xffffffffu, bad)) {
                                 for (int m = m_lo; m <= m_hi; ++m) {
-                                    const int hi = use.s.hi - A.M + m + 1, lo = A.window > 0 ? hi - A.window : 0;
+                                    const int hi = use.s.hi - A.M + m + 1, lo = first_seen(A, hi - 1);
                                     product(std::true_type{}, kept(lo, hi, 0), kept(lo, hi, 1), m);
                                 }
                             } else {

@@ -113,6 +113,11 @@ __device__ __forceinline__ float capped(float x, float cap, float inv2)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(x * inv2)));
     return cap * fmaf(-2.0f, r, 1.0f);
 }
+// First row that the query in row `own` sees; no sum passes 32 bits whatever the window.
+__device__ __forceinline__ int first_seen(const AttnArgs &A, int own)
+{
+    return A.window > 0 && own >= A.window ? own - A.window + 1 : 0;
+}
 // max over the eight lanes of a query column, sum likewise
 __device__ __forceinline__ float col_max(float x)
 {
@@ -197,7 +202,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &A, int b, bool report)
     }
     s.hi = max(n, 0);
     // the first query's own row is hi - M
-    s.lo = A.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(s.hi) - A.M - A.window + 1)) / 16 * 16 : 0;
+    s.lo = first_seen(A, s.hi - A.M) / 16 * 16;
     s.steps = s.hi > s.lo ? (s.hi - s.lo + SR - 1) / SR : 0;
     return s;
 }

@@ -331,7 +331,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                 own = use.s.hi - A.M + m;
                 slope2 = X && A.slopes ? A.slopes[hq] * kLog2e : 0.0f;
                 all_hi = use.s.hi - A.M + row_of_vector(A, v0) + 1;
-                all_lo = A.window > 0 ? use.s.hi - A.M + row_of_vector(A, v0 + nv - 1) - A.window + 1 : 0;
+                all_lo = first_seen(A, use.s.hi - A.M + row_of_vector(A, v0 + nv - 1));
                 mref = -INFINITY;
                 mz = lsum = 0.0f;
             }

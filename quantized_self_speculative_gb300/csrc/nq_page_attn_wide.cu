@@ -208,9 +208,9 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
             for (int i = 0; i < TILES; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
             all_hi = use.s.hi - A.M + m_lo + 1;
-            all_lo = A.window > 0 ? use.s.hi - A.M + m_hi - A.window + 1 : 0;
+            all_lo = first_seen(A, use.s.hi - A.M + m_hi);
             any_hi = use.s.hi - A.M + m_hi + 1;
-            any_lo = A.window > 0 ? use.s.hi - A.M + m_lo - A.window + 1 : 0;
+            any_lo = first_seen(A, use.s.hi - A.M + m_lo);
         }
         const int buf = (f - run.f0) & 1;
         const unsigned char *ktile, *vtile;
@@ -382,7 +382,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
                     const uint32_t p0 = j ? pb[BLKS - 1][0][0] : pb[0][0][0], p1 = j ? pb[BLKS - 1][0][1] : pb[0][0][1];
 #pragma unroll 1
                     for (int m = bad ? m_lo : m_hi; m <= m_hi; ++m) {
-                        const int hi = use.s.hi - A.M + m + 1, lo = A.window > 0 ? hi - A.window : 0;
+                        const int hi = use.s.hi - A.M + m + 1, lo = first_seen(A, hi - 1);
                         const uint32_t k0 = bad ? kept(lo, hi, 0) : kept(any_lo, any_hi, 0), k1 = bad ? kept(lo, hi, 1) : kept(any_lo, any_hi, 1);
 #pragma unroll
                         for (int i = 0; i < TILES; ++i) {

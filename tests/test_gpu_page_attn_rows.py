@@ -31,3 +31,15 @@ def test_a_window_leaves_any_page_behind(nq, fmt, planes, g, M, D, G, P):
     got = pool.attention(0, m, q, i32(lens), planes, D ** -0.5, window=window)
     assert nq.device_status() == 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("g", [1, 2, 6])
+def test_the_longest_windows_hide_nothing(nq, fmt, planes, g):
+    """More query rows than rows, under windows up to the largest int32: the same as without one."""
+    lens, M = [3, 1, 8, 40, 0], 9
+    pool, m = cache(nq, lens, 2, 64, 64, 16, kind(nq, fmt), 320)
+    q = query(321, len(lens), M, 2 * g, 64)
+    want = check(nq, pool, m, lens, q, planes, 0.125)
+    for window in (2 ** 31 - 1, 2 ** 31 - 4, 2 ** 31 - 9, 2 ** 30, 48):
+        assert torch.equal(check(nq, pool, m, lens, q, planes, 0.125, window=window), want)
