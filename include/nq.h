@@ -571,10 +571,10 @@ typedef struct {
  * (a multiple of 8).  A query that sees no row gives zeros (a length of 0, or
  * less than M for the first queries).  Rows past len and pages wholly before
  * the window are never used.  A length past max_pages * page_size is clamped
- * and sets NQ_DEV_SEQ_FULL, a needed page outside the pool or a slot outside
- * the map sets NQ_DEV_BAD_PAGE (that output is then unspecified).  planes as
- * in nq_page_read.  Scores, sums and outputs are held in fp32; probabilities
- * enter the second product as 16-bit values.
+ * and sets NQ_DEV_SEQ_FULL; a needed page outside the pool sets NQ_DEV_BAD_PAGE
+ * and its rows count as hidden; a slot outside the map sets it and gives zeros.
+ * planes as in nq_page_read.  Scores, sums and outputs are held in fp32;
+ * probabilities enter the second product as 16-bit values.
  */
 NQ_API size_t nq_page_attn_workspace_bytes(int M, int heads_q, int heads_kv, int head_dim);
 NQ_API nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,

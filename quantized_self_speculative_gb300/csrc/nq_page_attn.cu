@@ -109,11 +109,13 @@ attn_kernel(const __grid_constant__ AttnArgs A)
     Feed<FMT, D, NG, BLKS, kWarps> feed;
     feed.start(A, use, segs, fu, smem_u32(ring), bar_s);
     int stage = 0, next_stage = 0, filled = 0;                   // stages that hold or await a step
-    uint32_t phase = 0;
+    uint32_t phase = 0, gone = 0;                                // gone: blocks that are not there, of the filled stages in order
     auto fill = [&]() {
 #pragma unroll 1
         for (; filled < Q::STAGES && feed.left > 0; ++filled) {
-            feed.issue(A, segs, next_stage);
+            feed.issue(A, segs, next_stage, [&](uint32_t out) {
+                if (out) gone |= out << (BLKS * filled);
+            });
             if (++next_stage == Q::STAGES) next_stage = 0;
         }
     };
@@ -233,10 +235,11 @@ attn_kernel(const __grid_constant__ AttnArgs A)
             feed.wait(A, bar_s, stage, phase, Q::STAGES, filled, &abort_flag);
             const int row0 = use.s.lo + (fu - use.base) * SR;
             const unsigned char *sp = ring + stage * Q::STAGE;
-            const bool masked = row0 < all_lo || row0 + SR > all_hi;
+            const bool masked = row0 < all_lo || row0 + SR > all_hi || (FMT != kBf16 && (gone & ((1u << BLKS) - 1)) != 0);
 #pragma unroll
             for (int j0 = 0; j0 < BLKS; j0 += JB) {
                 if (row0 + 16 * j0 >= any_hi) break;             // not copied, or seen by no query
+                if (FMT == kBf16 && (gone >> j0 & 1u)) continue;
                 // ---- scales of the rows g, g + 8 of each block; log2 of V's
                 float sk[JB][2][NGX], sv[JB][2][NGX], lv[JB][2];
                 if constexpr (FMT != kBf16) {
@@ -258,7 +261,8 @@ attn_kernel(const __grid_constant__ AttnArgs A)
                         for (int j = 0; j < JB; ++j)
 #pragma unroll
                             for (int rr = 0; rr < 2; ++rr) {
-                                const bool none = static_cast<unsigned>(row0 + 16 * (j0 + j) + g + 8 * rr - any_lo) >= static_cast<unsigned>(any_hi - any_lo);
+                                const bool none = static_cast<unsigned>(row0 + 16 * (j0 + j) + g + 8 * rr - any_lo) >= static_cast<unsigned>(any_hi - any_lo) ||
+                                                  (gone >> (j0 + j) & 1u);
 #pragma unroll
                                 for (int gr = 0; gr < NGX; ++gr) {
                                     sk[j][rr][gr] = none ? 0.0f : sk[j][rr][gr];
@@ -379,7 +383,8 @@ attn_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
                                 for (int c = 0; c < 2; ++c) {
                                     // before the window, or (negative) after the query's own row
-                                    const bool hidden = static_cast<unsigned>(own[nt][c] - (row0 + 16 * (j0 + j) + g + 8 * rr)) >= window;
+                                    const bool hidden = static_cast<unsigned>(own[nt][c] - (row0 + 16 * (j0 + j) + g + 8 * rr)) >= window ||
+                                                        (FMT != kBf16 && (gone >> (j0 + j) & 1u));
                                     s[j][rr][c] = hidden ? -INFINITY : s[j][rr][c];
                                     y[j][rr][c] = hidden ? -INFINITY : y[j][rr][c];
                                 }
@@ -541,6 +546,7 @@ attn_kernel(const __grid_constant__ AttnArgs A)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             --filled;
+            gone >>= BLKS;
             fu += kWarps;
             if (++stage == Q::STAGES) {
                 stage = 0;

@@ -302,7 +302,8 @@ __device__ __forceinline__ Run find_run(const AttnArgs &A, int segs, int min_run
 
 // Fills a ring with the steps f, f + STRIDE, .. of a run: the whole warp walks,
 // lane k copies block k of the step (and those that follow it in its page).  The
-// page ids of a step are loaded one step ahead.
+// page ids of a step are loaded one step ahead.  Blocks of a page outside the pool
+// are not copied: `gone` takes their bits, and their rows are masked.
 template <int FMT, int D, int NG, int BLKS, int STRIDE>
 struct Feed {
     static constexpr int SR = 16 * BLKS, BASE = block_base(FMT, D, NG), RESID = block_resid(FMT, D), STAGE = BLKS * (BASE + RESID);
@@ -346,18 +347,20 @@ struct Feed {
         aim(A, segs, f);
         look();
     }
-    __device__ __forceinline__ void issue(const AttnArgs &A, int segs, int st)   // the step into stage st, then on to the next
+    template <typename F>
+    __device__ __forceinline__ void issue(const AttnArgs &A, int segs, int st, F gone)   // the step into stage st, then on to the next
     {
         if (left == 0) return;
         const int k = threadIdx.x & 31, n = min(BLKS, (w.s.hi - row + 15) >> 4), blk = ((row + 16 * k) & (A.m.P - 1)) >> 4;
         const uint32_t b = bar + 8 * st, dst = ring + st * STAGE;
-        if (k == 0) mbar_expect_tx(b, n * (BASE + RESID));
+        const bool bad = k < n && (id < 0 || id >= A.p.N);
+        const uint32_t out = __ballot_sync(0xffffffffu, bad);
+        gone(out);
+        if (k == 0) mbar_expect_tx(b, (n - __popc(out)) * (BASE + RESID));
         __syncwarp();
-        if (k < n && (k == 0 || blk == 0)) {
-            if (id < 0 || id >= A.p.N) {
-                set_status(A.status, NQ_DEV_BAD_PAGE);
-                id = 0;
-            }
+        if (bad) {
+            set_status(A.status, NQ_DEV_BAD_PAGE);
+        } else if (k < n && (k == 0 || blk == 0)) {
             const int x = min(n - k, (1 << (lp - 4)) - blk);                     // blocks side by side in the page
             const uint8_t *src = rec + static_cast<size_t>(id) * A.p.H * A.p.rec;
             bulk_g2s(dst + k * BASE, src + blk * BASE, x * BASE, b);

@@ -65,6 +65,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
     static_assert(Q::STAGES == 4 && kBufs == 4, "barrier numbers");
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) unsigned long long bars[kBars];
+    __shared__ uint32_t gone_of[Q::STAGES], gone_decoded[kBufs];                 // blocks that are not there
     __shared__ int abort_flag, keep_tmem;
     __shared__ uint32_t tmem_slot;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -114,7 +115,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
         for (; i < steps && feed.left > 0; ++i) {
             const int st = i % Q::STAGES;
             if (!__all_sync(0xffffffffu, wait(kRawEmpty + st, (i / Q::STAGES & 1) ^ 1))) break;
-            feed.issue(A, segs, st);
+            feed.issue(A, segs, st, [&](uint32_t out) { gone_of[st] = out; });
         }
         // every copy issued has landed before the CTA may exit
         volatile int never = 0;
@@ -157,6 +158,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                     float sk = __half2float(sc[e & 15]), sv = __half2float(sc[16 + (e & 15)]);
                     sk = sk >= 0.0f && sk <= 65504.0f ? sk : 0.0f;
                     sv = sv >= 0.0f && sv <= 65504.0f ? sv : 0.0f;
+                    if (e == 0) gone_decoded[b] = gone_of[st];
                     f[e] = sk;
                     f[kKeys + e] = sv;
                     f[2 * kKeys + e] = lg2(fmaxf(sv, 3.7252902984619140625e-09f));   // a scale of 0 has codes of 0
@@ -342,6 +344,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
             bool gave_up = false;
             if (active) {
                 tc_fence_after();
+                const uint32_t gone = gone_decoded[i % kBufs];
                 uint32_t s[64];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld16(tq + kColS + 64 * b + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(s + 16 * c));
@@ -372,6 +375,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                     const unsigned d = own - row0;
 #pragma unroll
                     for (int j = 0; j < 64; ++j) s[j] = d - j >= window ? 0xFF800000u : s[j];
+                }
+                if (gone) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) s[j] = gone >> (j >> 4) & 1u ? 0xFF800000u : s[j];
                 }
                 float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};    // with the log2 of V's scales
 #pragma unroll

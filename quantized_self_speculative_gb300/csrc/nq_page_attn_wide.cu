@@ -64,6 +64,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
     constexpr int SR = Q::SR, BLKS = Q::BLKS, KS = D / 16, TILES = D / 16, NGX = FMT == kBf16 ? 1 : NG, COLS = 8 * WARPS, THREADS = 32 * WARPS;
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) unsigned long long bars[Q::STAGES];
+    __shared__ uint32_t gone_of[Q::STAGES], gone_decoded[2];                 // blocks that are not there
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int segs = A.p.H * A.QT;
@@ -87,7 +88,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
     auto fill = [&]() {
 #pragma unroll 1
         for (; filled < Q::STAGES && feed.left > 0; ++filled) {
-            feed.issue(A, segs, next_stage);
+            feed.issue(A, segs, next_stage, [&](uint32_t out) { gone_of[next_stage] = out; });
             if (++next_stage == Q::STAGES) next_stage = 0;
         }
     };
@@ -123,6 +124,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
                     *reinterpret_cast<uint4 *>(to + (((4 * c + w) ^ (r & 7)) << 4)) = make_uint4(k.value(0), k.value(1), k.value(2), k.value(3));
                 }
             }
+            if (threadIdx.x == 0) gone_decoded[buf] = gone_of[stage];
             constexpr int SC = BLKS * 64 * NG / 16;                          // the scales' 16-byte chunks
             if (threadIdx.x < SC) {
                 const int j = threadIdx.x / (4 * NG), k = threadIdx.x % (4 * NG);
@@ -215,9 +217,11 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
         const int buf = (f - run.f0) & 1;
         const unsigned char *ktile, *vtile;
         int tile_step;
+        uint32_t gone;
         const __half *scales = nullptr;
         if constexpr (FMT == kBf16) {
             wait();
+            gone = gone_of[stage];
             ktile = ring + stage * Q::STAGE;
             vtile = ktile + Q::TILE;
             tile_step = Q::BASE;
@@ -227,13 +231,13 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
                 decode(buf ^ 1);
                 advance();
             }
+            gone = gone_decoded[buf];
             ktile = decoded + buf * Q::DECODED;
             vtile = ktile + BLKS * Q::TILE;
             tile_step = Q::TILE;
             scales = reinterpret_cast<const __half *>(ktile + 2 * BLKS * Q::TILE);
         }
         const int row0 = use.s.lo + (f - use.base) * SR;
-        const bool masked = row0 < all_lo || row0 + SR > all_hi;
         if (mine && row0 < any_hi) {
             // ---- S^T of both blocks, per group of K's scales
             float acc[BLKS][NGX][4];
@@ -252,6 +256,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
                         else mma<FMT>(acc[j][k / per], a0, a1, a2, a3, qf[k][0], qf[k][1]);
                     }
             }
+            const bool masked = row0 < all_lo || row0 + SR > all_hi || gone != 0;
             float sk[BLKS][2][NGX], sv[BLKS][2][NGX], lv[BLKS][2];
             if constexpr (FMT != kBf16) {
 #pragma unroll
@@ -268,7 +273,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
                     for (int j = 0; j < BLKS; ++j)
 #pragma unroll
                         for (int rr = 0; rr < 2; ++rr) {
-                            const bool none = static_cast<unsigned>(row0 + 16 * j + g + 8 * rr - any_lo) >= static_cast<unsigned>(any_hi - any_lo);
+                            const bool none = static_cast<unsigned>(row0 + 16 * j + g + 8 * rr - any_lo) >= static_cast<unsigned>(any_hi - any_lo) || (gone >> j & 1u);
 #pragma unroll
                             for (int gr = 0; gr < NGX; ++gr) {
                                 sk[j][rr][gr] = none ? 0.0f : sk[j][rr][gr];
@@ -311,7 +316,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             // before the window, or (negative) after the query's own row
-                            const bool hidden = static_cast<unsigned>(own[c] - (row0 + 16 * j + g + 8 * rr)) >= window;
+                            const bool hidden = static_cast<unsigned>(own[c] - (row0 + 16 * j + g + 8 * rr)) >= window || (gone >> j & 1u);
                             s[j][rr][c] = hidden ? -INFINITY : s[j][rr][c];
                             y[j][rr][c] = hidden ? -INFINITY : y[j][rr][c];
                         }
@@ -361,6 +366,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
                 // only some queries see is rare: then query row by query row (0 times infinity)
 #pragma unroll 1
                 for (int j = 0; j < BLKS; ++j) {
+                    if (gone >> j & 1u) continue;
                     const int blk0 = row0 + 16 * j;
                     auto kept = [&](int lo, int hi, int k) {
                         const int a = blk0 + 2 * t + 8 * k;

@@ -1,9 +1,11 @@
 """Which rows attention over pages counts: pages that a window has left behind,
 windows longer than any sequence, pages that are not there, rows that were not
 finite.  The reference is attention64 (64 bits, its tolerance derived there)."""
+import numpy as np
 import pytest
 import torch
 
+from paged_helpers import HostPool, rows_of
 from test_gpu_page_attn import FORMATS, cache, check, i32, query
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +45,46 @@ def test_the_longest_windows_hide_nothing(nq, fmt, planes, g):
     want = check(nq, pool, m, lens, q, planes, 0.125)
     for window in (2 ** 31 - 1, 2 ** 31 - 4, 2 ** 31 - 9, 2 ** 30, 48):
         assert torch.equal(check(nq, pool, m, lens, q, planes, 0.125, window=window), want)
+
+
+def without(hp, table, q, lens, planes, scale, gone, window=0):
+    """attention64 and its tolerance over the rows that are not gone[b]."""
+    B, M, Hq, D = q.shape
+    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    c = 2.0 ** -8 if hp.bf else 2.0 ** -11
+    for b, n in enumerate(lens):
+        K, V = rows_of(hp, 0, table[b], n, planes)
+        for m in range(M):
+            at = n - M + m
+            seen = np.array([t for t in range(max(0, at - window + 1) if window else 0, at + 1) if not gone[b][t]], int)
+            for h in range(Hq if len(seen) else 0):
+                k, v, x = K[h * hp.H // Hq, seen], V[h * hp.H // Hq, seen], q[b, m, h].astype(np.float64)
+                s = scale * (k @ x)
+                e = 2.0 ** -17 * scale * (np.abs(k) @ np.abs(x)).max()
+                p = np.exp(s - s.max())
+                out[b, m, h] = p @ v / p.sum()
+                tol[b, m, h] = (2.0 ** -8 * np.abs(out[b, m, h]) + (2 * c + 2 * e) * (p @ np.abs(v) / p.sum())
+                                + len(p) * 2.0 ** -24 * np.abs(v).max() / p.sum())
+    return out, tol
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("g,M", VECTORS)
+@pytest.mark.parametrize("D,G,P,window", [(64, 64, 16, 0), (128, 128, 32, 0), (128, 64, 16, 70)])
+def test_rows_of_a_page_outside_the_pool_do_not_count(nq, fmt, planes, g, M, D, G, P, window):
+    """Entries that name no page: first, inner, side by side, last, all of them.  Their rows count as not there,
+    and nothing of another page takes their place."""
+    lens = [5 * P, 3 * P + 1, 7 * P + 5, 9, 4 * P, 6 * P - 3, 2 * P]
+    broken = [[0], [1, 3], [2, 3, 4], [0], [3], [0, 1, 4], []]
+    pool, m = cache(nq, lens, 2, D, G, P, kind(nq, fmt), 340)
+    q = query(341, len(lens), M, 2 * g, D)
+    table = m.table.cpu().numpy().copy()
+    gone = [np.isin(np.arange(n) // P, broken[b]) for b, n in enumerate(lens)]
+    ref, tol = without(HostPool(pool), table, q.float().cpu().numpy(), lens, planes, 0.125, gone, window)
+    for bad in (-1, pool.n_pages, 2 ** 31 - 1, -2 ** 31):
+        for b, js in enumerate(broken):
+            for j in js:
+                m.table[b, j] = bad
+        out = pool.attention(0, m, q, i32(lens), planes, 0.125, window=window).double().cpu().numpy()
+        assert nq.device_status() == nq.NQ_DEV_BAD_PAGE
+        assert (np.abs(out - ref) <= tol).all()
