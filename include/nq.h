@@ -534,8 +534,9 @@ NQ_API nq_status nq_page_copy(const nq_page_pool *pool, const int32_t *src, cons
  * they are rounded.  q_out: bf16 [T][heads_q][head_dim].  NESTED44 rows are
  * quantised like nq_kv_append's.  A row past max_pages * page_size sets
  * NQ_DEV_SEQ_FULL, a slot or page outside the map NQ_DEV_BAD_PAGE; that row is
- * dropped.  A non-finite NESTED44 row sets NQ_DEV_NONFINITE (its value is then
- * unspecified).  No two tokens of a call name the same row.
+ * dropped.  A group of a NESTED44 row that is not finite, or whose scale does
+ * not fit fp16, is stored as zeros and sets NQ_DEV_NONFINITE.  No two tokens of
+ * a call name the same row.
  */
 NQ_API nq_status nq_page_append(const nq_page_pool *pool, int layer, const nq_page_map *map, const nq_rope_plan *rope,
                                 const void *q, const void *k, const void *v, int dtype, int64_t stride,

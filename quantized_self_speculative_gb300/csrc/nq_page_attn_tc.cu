@@ -153,8 +153,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                 if (e < kKeys) {
                     const __half *sc = reinterpret_cast<const __half *>(sp + (e >> 4) * Q::BASE + 32 * RB);
                     float *f = reinterpret_cast<float *>(scales + b * Q::SCALES);
-                    // a scale that is not finite, or negative, counts as 0: rows past the end may hold
-                    // anything, and the value of a row that was not finite is unspecified
+                    // a scale that is not finite, or negative, counts as 0: rows past the end may hold anything
                     float sk = __half2float(sc[e & 15]), sv = __half2float(sc[16 + (e & 15)]);
                     sk = sk >= 0.0f && sk <= 65504.0f ? sk : 0.0f;
                     sv = sv >= 0.0f && sv <= 65504.0f ? sv : 0.0f;

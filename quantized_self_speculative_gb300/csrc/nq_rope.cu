@@ -315,22 +315,29 @@ struct Place {
     }
 };
 
-// One row, quantised in groups of D / NG; true where it is not finite.
+// The larger one; NaN where either is NaN.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// One row, quantised in groups of D / NG; true where it is not finite: its group is
+// then zeros, so that every reader of the cache sees the same.
 template <int D, int NG>
 __device__ __forceinline__ bool store_nested(const Place<D, NG> &at, size_t off, const Vec<D / 32> &x, int lane)
 {
     constexpr int E = D / 32;
-    float amax = 0.0f, nan = 0.0f;
+    float amax = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        amax = fmaxf(amax, fabsf(x.v[e]));
-        nan = __fmaf_rn(x.v[e], 0.0f, nan);                      // NaN if any value is not finite
-    }
+    for (int e = 0; e < E; ++e) amax = max_nan(amax, fabsf(x.v[e]));
 #pragma unroll
-    for (int o = 16 / NG; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int o = 16 / NG; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     // absmax / 7, correctly rounded as in codes_of
     const float q7 = amax * 0.142857142857142857f;
-    const __half sh = __float2half_rn(__fmaf_rn(__fmaf_rn(-q7, 7.0f, amax), 0.142857142857142857f, q7));
+    __half sh = __float2half_rn(__fmaf_rn(__fmaf_rn(-q7, 7.0f, amax), 0.142857142857142857f, q7));
+    const bool bad = !(__half2float(sh) <= 65504.0f);            // a value that is not finite, or past 7 times fp16's largest
+    if (bad) sh = __ushort_as_half(0);
     const float s = __half2float(sh), rs = __frcp_rn(s);
     uint32_t c[E], b, r;
 #pragma unroll
@@ -351,7 +358,7 @@ __device__ __forceinline__ bool store_nested(const Place<D, NG> &at, size_t off,
         to[at.resid] = static_cast<uint8_t>(s == 0.0f ? 0x88u : r);
     }
     if (lane % (32 / NG) == 0) *reinterpret_cast<__half *>(to + at.scale) = sh;
-    return !(nan == 0.0f) || !(s <= 65504.0f);
+    return bad;
 }
 
 // NG = 0: BF16.  Rows of a token in the order q heads, k heads, v heads; a warp

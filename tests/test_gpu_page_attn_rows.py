@@ -88,3 +88,26 @@ def test_rows_of_a_page_outside_the_pool_do_not_count(nq, fmt, planes, g, M, D, 
         out = pool.attention(0, m, q, i32(lens), planes, 0.125, window=window).double().cpu().numpy()
         assert nq.device_status() == nq.NQ_DEV_BAD_PAGE
         assert (np.abs(out - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("planes", [1, 2])
+@pytest.mark.parametrize("g,M", VECTORS)
+@pytest.mark.parametrize("D,G", [(64, 64), (128, 128), (128, 64)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 1e30])
+def test_a_row_that_was_not_finite_is_zeros_to_every_reader(nq, planes, g, M, D, G, value):
+    """Appended to nested pages: its group is stored as zeros and reported, however many queries then read it."""
+    lens = [70, 33]
+    pool, m = cache(nq, lens, 1, D, G, 16, nq.KV_NESTED44, 360)
+    rows = torch.ones(4, 1, D, device="cuda")
+    bad = rows.clone()
+    bad[1, 0, 5] = value
+    bad[3, 0, D - 1] = -value
+    seqs, pos = i32([0, 0, 1, 1]), i32([3, 40, 30, 31])
+    for k, v in ((rows, bad), (bad, rows)):
+        pool.append(0, m, k, v, seqs, pos)
+        assert nq.device_status() == nq.NQ_DEV_NONFINITE
+        got = pool.read(0, m, seqs, pos, planes=planes)
+        x = got[0] if k is bad else got[1]
+        assert (x[1, 0, :G] == 0).all() and (x[3, 0, D - G:] == 0).all() and (x[0] != 0).all() and (x[2] != 0).all()
+        assert (x[1, 0, G:] != 0).all() and (x[3, 0, :D - G] != 0).all()
+        check(nq, pool, m, lens, query(361, 2, M, g, D), planes, D ** -0.5)
