@@ -28,7 +28,7 @@
 // signed numbers themselves: the code under an exponent of 2^10, and one fma on
 // two halves that takes 2^10 and the offset off again.  K's scales multiply S, V's scales multiply P before it is rounded
 // to fp16 (one rounding, 2^-11).  So that no V magnitude underflows there, m is
-// the running maximum of s + log2(scale of V) and P = 2^(s - m) scale <= 2^12.
+// the running maximum of s + log2(scale of V) and P = 2^(s - m) scale <= 2^15.
 // The query is brought to a largest magnitude of 2^10 by a power of two.
 // BF16: K, V and the query as they are, P rounded to bf16 (2^-8); the sum is
 // taken of the rounded P, which takes most of that error out again.
@@ -400,7 +400,7 @@ attn_kernel(const __grid_constant__ AttnArgs A)
                     if (__any_sync(0xffffffffu, top[0] > mref[nt][0] + slack<FMT>() || top[1] > mref[nt][1] + slack<FMT>())) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const float mn = top[c] > mref[nt][c] + slack<FMT>() ? top[c] : mref[nt][c];
+                            const float mn = top[c] > mref[nt][c] + slack<FMT>() ? top[c] - lead<FMT>() : mref[nt][c];
                             const float alpha = ex2(mref[nt][c] == -INFINITY ? -INFINITY : mref[nt][c] - mn);   // nothing yet: 0
                             mref[nt][c] = mn;
                             mz[nt][c] = mn == -INFINITY ? 0.0f : mn;

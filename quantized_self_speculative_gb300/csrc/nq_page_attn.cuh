@@ -10,12 +10,15 @@ namespace nq {
 enum { kBf16 = 0, kKv4 = 1, kKv8 = 2 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-// m is only raised when the maximum has grown by more than 2^slack, so that the
-// accumulators are rarely rescaled.  With fp16 probabilities P <= 2^12 is inside
-// their range (below 2^16), and what falls below its normal part is under 2^-14 of
-// the first maximum; at 6 some row of 32 outgrew it at nearly every step of 64 keys.
-// bf16 rounds P to 2^-8: there the largest P stays 1, which is exact.
-template <int FMT> __host__ __device__ constexpr float slack() { return FMT == kBf16 ? 0.0f : 12.0f; }
+// m is raised to 2^lead below the maximum, and only when the largest P = 2^(s - m) has
+// passed 2^slack, so that the accumulators are rarely rescaled: a factor of 2^12 in
+// between (at 2^6 some row of 32 outgrew it at nearly every step of 64 keys).  fp16
+// holds P <= 2^15, and below its normal part rounds by 2^-25: 2^-28 of the maximum at
+// most, so that the numerator keeps the tails that the sum of the unrounded P counts
+// (n rows: n 2^-28 of it at most).  bf16 has the range of fp32 and rounds P to 2^-8:
+// there the largest P stays 1, which is exact.
+template <int FMT> __host__ __device__ constexpr float lead() { return FMT == kBf16 ? 0.0f : 3.0f; }
+template <int FMT> __host__ __device__ constexpr float slack() { return FMT == kBf16 ? 0.0f : 15.0f; }
 
 struct AttnArgs {
     Pool p;

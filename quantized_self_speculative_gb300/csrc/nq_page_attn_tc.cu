@@ -394,7 +394,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                 }
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 if (__any_sync(0xffffffffu, top > mref + slack<FMT>())) {
-                    const float mn = top > mref + slack<FMT>() ? top : mref, alpha = ex2(mref == -INFINITY ? -INFINITY : mref - mn);
+                    const float mn = top > mref + slack<FMT>() ? top - lead<FMT>() : mref, alpha = ex2(mref == -INFINITY ? -INFINITY : mref - mn);
                     mref = mn;
                     mz = mn == -INFINITY ? 0.0f : mn;
                     lsum *= alpha;

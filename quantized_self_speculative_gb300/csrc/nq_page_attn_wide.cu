@@ -327,7 +327,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
             if (__any_sync(0xffffffffu, top[0] > mref[0] + slack<FMT>() || top[1] > mref[1] + slack<FMT>())) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float mn = top[c] > mref[c] + slack<FMT>() ? top[c] : mref[c];
+                    const float mn = top[c] > mref[c] + slack<FMT>() ? top[c] - lead<FMT>() : mref[c];
                     const float alpha = ex2(mref[c] == -INFINITY ? -INFINITY : mref[c] - mn);    // nothing yet: 0
                     mref[c] = mn;
                     mz[c] = mn == -INFINITY ? 0.0f : mn;

@@ -1,0 +1,33 @@
+"""Scores of attention over pages where they are easily lost: long flat tails,
+caps far above the scores, tiny scales, and queries with a stride of their own."""
+import numpy as np
+import pytest
+import torch
+
+from paged_helpers import HostPool
+from test_gpu_page_attn import i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("planes", [1, 2])
+@pytest.mark.parametrize("heads,batch", [(1, 456), (20, 608), (32, 152)])
+def test_a_long_flat_tail_keeps_its_weight(nq, planes, heads, batch):
+    """2^20 rows of one value, the first with a weight of 1 and each other with 2.45 2^-24: the output is that
+    value.  Weights are rounded to fp16 at 2^3 times the largest (2^-25 2^-3 each), sums of products in fp32
+    (sixteen at a time; one step of 2^-23 of the sum), the output to bf16."""
+    n, D, P = 1 << 20, 64, 256
+    pool = nq.PagePool(1, n // P, P, 1, D, nq.KV_NESTED44, group=64)
+    m = nq.PageMap(1, n // P, n // P, P, table=torch.arange(n // P, dtype=torch.int32, device="cuda")[None].contiguous())
+    k, v = torch.zeros(n, 1, D, device="cuda"), torch.ones(n, 1, D, device="cuda")
+    k[0, 0, 0] = 7.0
+    pool.append(0, m, k, v, torch.zeros(n, dtype=torch.int32, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda"))
+    q = torch.zeros(batch, 1, heads, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    scale = np.log(2.0 ** 24 / 2.45) / 7.0
+    out = pool.attention(0, m, q, i32([n] * batch), planes, scale, seqs=i32([0] * batch)).double()
+    one = HostPool(pool).row(0, 0, 0, 0, 1, planes)[0]
+    tail = (n - 1) * 2.45 * 2.0 ** -24
+    tol = 2.0 ** -8 + n * 2.0 ** -28 / (1 + tail) + n / 16 * 2.0 ** -23
+    assert float((out - one).abs().max()) <= tol * one, float((out - one).abs().max())
+    assert nq.device_status() == 0
