@@ -555,8 +555,8 @@ NQ_API nq_status nq_page_read(const nq_page_pool *pool, int layer, const nq_page
 
 /* What changes the scores of nq_page_attn (host struct). */
 typedef struct {
-    float scale;            /* > 0 */
-    float softcap;          /* 0: none; else s -> softcap tanh(s / softcap) */
+    float scale;            /* > 0, finite */
+    float softcap;          /* 0: none; else (2^-100 .. 2^100) s -> softcap tanh(s / softcap) */
     int32_t window;         /* 0: none; else a query sees its own row and the window-1 before it */
     int32_t pad;
     const float *slopes;    /* NULL, or fp32 [heads_q] device: s -= slope (row of query - row of key) */

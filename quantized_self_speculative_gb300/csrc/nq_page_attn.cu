@@ -124,8 +124,7 @@ attn_kernel(const __grid_constant__ AttnArgs A)
     uint32_t qf[KS][NT][2];
     float cq[NT][2], start[NT][NGX][2], slope2[NT][2], o[TILES][NT][4], mref[NT][2], mz[NT][2], lsum[NT][2];   // mz: mref, 0 for -infinity
     int own[NT][2];                           // row of the query itself; rows (own - window, own] are seen
-    const float inv2 = X && A.softcap > 0.0f ? 2.0f / A.softcap : 0.0f;          // 2^(2 log2(e) x / cap), x in base 2
-    const float cap2 = A.softcap * kLog2e;
+    const float cap2 = A.softcap * kLog2e, inv2 = X && A.softcap > 0.0f ? 1.0f / cap2 : 0.0f;    // of scores in base 2
     const unsigned window = A.window > 0 ? A.window : 0x7fffffffu;
     for (;;) {
         fill();
@@ -832,7 +831,8 @@ static nq_status page_attn(const nq_page_pool *pool, int layer, const nq_page_ma
     const nq::Pool &p = A.p;
     if (layer < 0 || layer >= pool->layers || !q || !len || !out || !opts || batch < 1 || M < 1) return NQ_ERR_ARG;
     if (heads_q < p.H || heads_q % p.H != 0 || (planes != 1 && planes != 2) || (!seqs && batch > A.m.S)) return NQ_ERR_ARG;
-    if (!(opts->scale > 0.0f) || !(opts->softcap >= 0.0f) || opts->window < 0) return NQ_ERR_ARG;
+    if (!(opts->scale > 0.0f && opts->scale <= 3.4028235e38f) || opts->window < 0) return NQ_ERR_ARG;
+    if (opts->softcap != 0.0f && !(opts->softcap >= 0x1p-100f && opts->softcap <= 0x1p100f)) return NQ_ERR_ARG;
     const int G = heads_q / p.H;
     if (static_cast<long long>(M) * G > 65536) return NQ_ERR_SHAPE;
     if (q_stride < static_cast<int64_t>(heads_q) * p.D || q_stride % 8 != 0) return NQ_ERR_SHAPE;

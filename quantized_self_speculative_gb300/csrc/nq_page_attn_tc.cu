@@ -275,7 +275,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
         // ================================================= softmax: thread = query vector
         const int row = warp * 32 + lane;
         const uint32_t tq = tmem + (static_cast<uint32_t>(warp) << 21);          // lanes 32 w ..
-        const float inv2 = X && A.softcap > 0.0f ? 2.0f / A.softcap : 0.0f, cap2 = A.softcap * kLog2e;
+        const float cap2 = A.softcap * kLog2e, inv2 = X && A.softcap > 0.0f ? 1.0f / cap2 : 0.0f;
         const unsigned window = A.window > 0 ? A.window : 0x7fffffffu;
         bool fresh = true, active = false;
         int kvh = 0, v0 = 0, nv = 0, own = 0, all_lo = 0, all_hi = 0, m = 0;
@@ -354,21 +354,27 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 k4 = *reinterpret_cast<const float4 *>(f + j);
-                    float2 x[2] = {f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2_pack(k4.x, k4.y), zero2)),
+                    const float2 x[2] = {f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2_pack(k4.x, k4.y), zero2)),
                                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), f2_pack(k4.z, k4.w), zero2))};
-                    if constexpr (X) {
-                        auto option = [&](float y, int key) {
-                            y *= cq;
-                            if (A.softcap > 0.0f) y = capped(y, cap2, inv2);
-                            return fmaf(slope2, static_cast<float>(row0 + key - own), y);
-                        };
-                        x[0] = make_float2(option(x[0].x, j), option(x[0].y, j + 1));
-                        x[1] = make_float2(option(x[1].x, j + 2), option(x[1].y, j + 3));
+                    s[j] = __float_as_uint(X ? x[0].x * cq : x[0].x);
+                    s[j + 1] = __float_as_uint(X ? x[0].y * cq : x[0].y);
+                    s[j + 2] = __float_as_uint(X ? x[1].x * cq : x[1].x);
+                    s[j + 3] = __float_as_uint(X ? x[1].y * cq : x[1].y);
+                }
+                if constexpr (X) {
+                    if (A.softcap > 0.0f) {
+                        if (masked || gone) {
+                            const unsigned d = own - row0;
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) s[j] = d - j >= window || (gone >> (j >> 4) & 1u) ? 0u : s[j];
+                        }
+                        cap_all(reinterpret_cast<float(&)[64]>(s), cap2, inv2);
                     }
-                    s[j] = __float_as_uint(x[0].x);
-                    s[j + 1] = __float_as_uint(x[0].y);
-                    s[j + 2] = __float_as_uint(x[1].x);
-                    s[j + 3] = __float_as_uint(x[1].y);
+                    if (A.slopes) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            s[j] = __float_as_uint(fmaf(slope2, static_cast<float>(row0 + j - own), __uint_as_float(s[j])));
+                    }
                 }
                 if (masked) {                 // before the window, or (negative) after the query's own row
                     const unsigned d = own - row0;

@@ -139,7 +139,7 @@ attn_wide_kernel(const __grid_constant__ AttnArgs A)
     uint32_t qf[KS][2];
     float cq[2], slope2[2], o[TILES][4], mref[2], mz[2], lsum[2];            // mz: mref, 0 for -infinity
     int own[2];                               // row of the query itself
-    const float inv2 = X && A.softcap > 0.0f ? 2.0f / A.softcap : 0.0f, cap2 = A.softcap * kLog2e;
+    const float cap2 = A.softcap * kLog2e, inv2 = X && A.softcap > 0.0f ? 1.0f / cap2 : 0.0f;
     const unsigned window = A.window > 0 ? A.window : 0x7fffffffu;
 
     if constexpr (FMT != kBf16) {

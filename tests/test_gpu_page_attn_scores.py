@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
-from paged_helpers import HostPool
-from test_gpu_page_attn import i32
+from paged_helpers import HostPool, attention64
+from test_gpu_page_attn import FORMATS, cache, check, i32, query
+from test_gpu_page_attn_rows import VECTORS, kind
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,40 @@ def test_a_long_flat_tail_keeps_its_weight(nq, planes, heads, batch):
     tol = 2.0 ** -8 + n * 2.0 ** -28 / (1 + tail) + n / 16 * 2.0 ** -23
     assert float((out - one).abs().max()) <= tol * one, float((out - one).abs().max())
     assert nq.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("g,M", VECTORS)
+@pytest.mark.parametrize("cap", [2.0 ** 14, 2.0 ** 20, 2.0 ** 60, 2.0 ** 100])
+def test_a_cap_far_above_the_scores_changes_none(nq, fmt, planes, g, M, cap):
+    """cap tanh(x / cap) = x (1 - x^2 / (3 cap^2) ..): below 2^-18 of a score of 100.  The tolerance is that of no cap."""
+    lens = [6, 40, 300, 17]
+    pool, m = cache(nq, lens, 2, 64, 64, 16, kind(nq, fmt), 380)
+    q = query(381, len(lens), M, 2 * g, 64)
+    ref, tol = attention64(HostPool(pool), 0, m.table.cpu().numpy(), q.float().cpu().numpy(), lens, planes, 0.3)
+    out = pool.attention(0, m, q, i32(lens), planes, 0.3, softcap=cap).double().cpu().numpy()
+    assert (np.abs(out - ref) <= tol).all()
+    assert nq.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("cap", [2.0 ** -100, 1e-3, 1.0, 5.0])
+def test_a_cap_far_below_the_scores(nq, fmt, planes, cap):
+    lens = [6, 40, 300, 17]
+    pool, m = cache(nq, lens, 2, 64, 64, 16, kind(nq, fmt), 382)
+    for g, M in VECTORS:
+        check(nq, pool, m, lens, query(383, len(lens), M, 2 * g, 64), planes, 0.3, softcap=cap)
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("fill", [0x7BFF, 0x7F00, 0x7C00])
+@pytest.mark.parametrize("g,M", VECTORS)
+def test_a_far_cap_beside_huge_hidden_scores(nq, fmt, planes, fill, g, M):
+    """Rows past the end hold the largest scale, or values of 10^38: they do not touch the scores beside them."""
+    lens = [6, 41, 300, 17, 1]
+    pool, m = cache(nq, lens, 2, 64, 64, 16, kind(nq, fmt), 390, fill=fill)
+    q = query(391, len(lens), M, 2 * g, 64)
+    for window in (0, 11):
+        ref, tol = attention64(HostPool(pool), 0, m.table.cpu().numpy(), q.float().cpu().numpy(), lens, planes, 0.3, window=window)
+        out = pool.attention(0, m, q, i32(lens), planes, 0.3, softcap=2.0 ** 60, window=window).double().cpu().numpy()
+        assert (np.abs(out - ref) <= tol).all()
