@@ -744,22 +744,35 @@ class PagePool:
                                       self._rows(v_out, shape, "v_out"), _stream(stream)), "nq_page_read")
         return k_out, v_out
 
+    @staticmethod
+    def _queries(q: torch.Tensor):
+        """Address of q [batch][M][heads][head_dim] and the elements between its batch * M rows."""
+        B, M, H, D = q.shape
+        if q.is_contiguous():
+            return _dev(q, torch.bfloat16, "q"), H * D
+        st = q.stride()
+        step = st[1] if M > 1 else st[0] if B > 1 else H * D
+        if (not q.is_cuda or q.dtype != torch.bfloat16 or st[3] != 1 or (st[2] != D and H > 1)
+                or (B > 1 and M > 1 and st[0] != M * st[1])):
+            raise ValueError("q must be a CUDA tensor of torch.bfloat16, its batch * M rows evenly spaced and each contiguous")
+        return q.data_ptr(), step
+
     def attention(self, layer: int, pmap: PageMap, q: torch.Tensor, lens: torch.Tensor, planes: int, scale: float,
                   seqs: Optional[torch.Tensor] = None, softcap: float = 0.0, window: int = 0,
                   slopes: Optional[torch.Tensor] = None, out=None, ws=None, stream=None) -> torch.Tensor:
         """Attention of the last M rows of each sequence, q bf16 [batch][M][heads_q]
-        [head_dim]; sequence b is slot seqs[b] (slot b without seqs) of lens[b]
-        rows.  softcap, window and slopes (fp32 [heads_q]) as in nq_attn_opts."""
+        [head_dim] (its batch * M rows may be strided, each contiguous); sequence
+        b is slot seqs[b] (slot b without seqs) of lens[b] rows.  softcap, window and slopes (fp32 [heads_q]) as in nq_attn_opts."""
         B, M, Hq, D = q.shape
         if D != self.head_dim:
             raise ValueError("q must have the pool's head_dim")
         if slopes is not None and slopes.shape != (Hq,):
             raise ValueError("slopes must be fp32 [heads_q]")
-        given = (_dev(q, torch.bfloat16, "q"), Hq * D, B, M, Hq, None if seqs is None else PageMap._list(seqs, B, "seqs"),
+        given = (*self._queries(q), B, M, Hq, None if seqs is None else PageMap._list(seqs, B, "seqs"),
                  PageMap._list(lens, B, "lens"), int(planes))
         on = _stream(stream)
         if out is None:
-            out = torch.empty_like(q) if stream is None else _empty(q.shape, q.dtype, q.device, stream)
+            out = _empty(q.shape, q.dtype, q.device, stream)
         if ws is None:
             need = self._attn_bytes.get((M, Hq))
             if need is None:

@@ -69,3 +69,22 @@ def test_a_far_cap_beside_huge_hidden_scores(nq, fmt, planes, fill, g, M):
         ref, tol = attention64(HostPool(pool), 0, m.table.cpu().numpy(), q.float().cpu().numpy(), lens, planes, 0.3, window=window)
         out = pool.attention(0, m, q, i32(lens), planes, 0.3, softcap=2.0 ** 60, window=window).double().cpu().numpy()
         assert (np.abs(out - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("g,M", VECTORS + [(3, 1)])
+def test_queries_with_a_stride_of_their_own(nq, fmt, planes, g, M):
+    """The heads of a wider row, read where they lie."""
+    lens = [6, 40, 300, 17]
+    pool, m = cache(nq, lens, 2, 64, 64, 16, kind(nq, fmt), 384)
+    wide = query(385, len(lens), M, 2 * g + 3, 64)
+    q = wide[:, :, 1:1 + 2 * g]
+    want = check(nq, pool, m, lens, q.contiguous(), planes, 0.3)
+    got = pool.attention(0, m, q, i32(lens), planes, 0.3)
+    assert got.is_contiguous() and torch.equal(got, want)
+    bad = [wide[:, :, ::2][:, :, :2], wide.float()[:, :, :2 * g]]
+    if M > 1:
+        bad += [query(386, len(lens), M + 1, 2 * g, 64)[:, 1:], wide[:, :, :2 * g].transpose(0, 1)]
+    for x in bad:
+        with pytest.raises(ValueError):
+            pool.attention(0, m, x, i32([1] * x.shape[0]), planes, 0.3)
