@@ -202,6 +202,8 @@ attn_kernel(const __grid_constant__ AttnArgs A)
                 const float fc = FMT == kBf16 ? 1.0f : __shfl_sync(0xffffffffu, f, 4 * (2 * t + c));
                 // undo the codes' 2^-24 (and, for KV8, the 16) and the query's power of two
                 cq[nt][c] = A.scale * kLog2e * fc * (FMT == kBf16 ? 1.0f : FMT == kKv8 ? 1048576.0f : 16777216.0f);
+                // not 0, which would make NaN of a hidden score: a query of zeros under a tiny scale
+                if constexpr (FMT != kBf16) cq[nt][c] = fmaxf(cq[nt][c], 1.2e-38f);
                 const int mc = row_of_vector(A, vc);
                 own[nt][c] = use.s.hi - A.M + mc;
                 slope2[nt][c] = X && A.slopes ? A.slopes[kvh * A.G + vc - mc * A.G] * kLog2e : 0.0f;

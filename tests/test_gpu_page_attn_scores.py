@@ -88,3 +88,15 @@ def test_queries_with_a_stride_of_their_own(nq, fmt, planes, g, M):
     for x in bad:
         with pytest.raises(ValueError):
             pool.attention(0, m, x, i32([1] * x.shape[0]), planes, 0.3)
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+@pytest.mark.parametrize("scale", [1e-18, 1e-30, 1e-38])
+def test_tiny_scales_and_queries_of_zero(nq, fmt, planes, scale):
+    """All scores equal: the mean of the rows that are seen."""
+    lens = [6, 40, 300, 17]
+    pool, m = cache(nq, lens, 2, 64, 64, 16, kind(nq, fmt), 387)
+    for g, M in VECTORS:
+        q = query(388, len(lens), M, 2 * g, 64)
+        q[:, :, ::2] = 0
+        check(nq, pool, m, lens, q, planes, scale)
