@@ -508,6 +508,14 @@ def _empty(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.T
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _zeros(shape, dtype, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """The same, cleared on that stream."""
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+
 class _Scratch:
     """Workspaces of the calls on one object, kept from call to call (a fork and a
     reservation take 37 us instead of 43, the host's share being all of it): one
@@ -672,16 +680,17 @@ class PageMap:
 
 
 class PagePool:
-    """The pages of all layers (nq_page_pool); data uint8, made here unless given."""
+    """The pages of all layers (nq_page_pool); data uint8, made and cleared here
+    (on `stream`) unless given."""
 
     def __init__(self, layers: int, n_pages: int, page_size: int, heads_kv: int, head_dim: int, fmt: int = KV_NESTED44,
-                 group: int = 128, data: Optional[torch.Tensor] = None, device=None):
+                 group: int = 128, data: Optional[torch.Tensor] = None, device=None, stream=None):
         n = C.c_size_t()
         _check(lib().nq_page_pool_bytes(layers, n_pages, page_size, heads_kv, head_dim, group, fmt, C.byref(n)),
                "nq_page_pool_bytes")
         self.bytes = n.value
         if data is None:
-            data = torch.zeros(n.value, dtype=torch.uint8, device=device or torch.device("cuda"))
+            data = _zeros(n.value, torch.uint8, device or torch.device("cuda"), stream)
         if data.numel() != n.value:
             raise ValueError(f"data must hold {n.value} bytes")
         self.data, self.layers, self.n_pages, self.page_size = data, layers, n_pages, page_size

@@ -50,3 +50,22 @@ def test_truncate_names_a_slot_twice(nq):
         h.truncate(names, keep)
         same(m, h)
         assert nq.device_status() == 0
+
+
+def test_a_pool_made_on_a_stream(nq):
+    """Its clearing is ordered before what that stream appends, not by the current stream."""
+    s = torch.cuda.Stream()
+    seqs, pos = i32([0] * 16), torch.arange(16, dtype=torch.int32, device="cuda")
+    x = torch.ones(16, 1, 64, device="cuda")
+    m = nq.PageMap(1, 1, 1000, 16, table=i32([[999]]))
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                       # the current stream is busy for some milliseconds
+    pool = nq.PagePool(1, 1000, 16, 1, 64, nq.KV_BF16, stream=s)
+    pool.append(0, m, x, x, seqs, pos, stream=s)
+    k, v = pool.read(0, m, seqs, pos, stream=s)
+    s.synchronize()
+    early = (k == 1).all() and (v == 1).all()
+    torch.cuda.synchronize()
+    k, v = pool.read(0, m, seqs, pos)
+    assert early and (k == 1).all() and (v == 1).all()
+    assert (pool.data.view(torch.bfloat16) == 1).sum() == 2 * 16 * 64 and (pool.data == 0).sum() > 0
