@@ -649,6 +649,8 @@ class PageMap:
         lists = self._list(seqs, n, "seqs"), self._list(first, n, "first"), self._list(last, n, "last")
         on = _stream(stream)
         granted = granted if granted is not None else _empty(n, torch.int32, seqs.device, stream)
+        if n == 0:
+            return granted
         ws = self._work(n, ws, stream, on)
         _check(lib().nq_page_reserve(self.ptr, None if pool is None else pool.ptr, *lists, n,
                                      self._list(granted, n, "granted"), ws.data_ptr(), ws.numel(), on),
@@ -659,6 +661,8 @@ class PageMap:
         """Slot dst[i] shares slot src[i]'s first rows[i] rows (all pairs at once)."""
         n = src.shape[0]
         lists = self._list(src, n, "src"), self._list(dst, n, "dst"), self._list(rows, n, "rows")
+        if n == 0:
+            return
         on = _stream(stream)
         ws = self._work(n, ws, stream, on)
         _check(lib().nq_page_fork(self.ptr, *lists, n, ws.data_ptr(), ws.numel(), on), "nq_page_fork")
@@ -666,8 +670,10 @@ class PageMap:
     def truncate(self, seqs, rows, stream=None) -> None:
         """Slot seqs[i] keeps the pages of its first rows[i] rows."""
         n = seqs.shape[0]
-        _check(lib().nq_page_truncate(self.ptr, self._list(seqs, n, "seqs"), self._list(rows, n, "rows"), n,
-                                      _stream(stream)), "nq_page_truncate")
+        lists = self._list(seqs, n, "seqs"), self._list(rows, n, "rows")
+        if n == 0:
+            return
+        _check(lib().nq_page_truncate(self.ptr, *lists, n, _stream(stream)), "nq_page_truncate")
 
     def compact(self, pool: "PagePool", used=None, ws=None, stream=None) -> torch.Tensor:
         """Move the pages in use to the lowest ids; returns how many (int32 [1])."""
@@ -704,8 +710,10 @@ class PagePool:
     def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Copy pages src[i] to dst[i] in every layer."""
         n = src.shape[0]
-        _check(lib().nq_page_copy(self.ptr, PageMap._list(src, n, "src"), PageMap._list(dst, n, "dst"), n,
-                                  _stream(stream)), "nq_page_copy")
+        lists = PageMap._list(src, n, "src"), PageMap._list(dst, n, "dst")
+        if n == 0:
+            return
+        _check(lib().nq_page_copy(self.ptr, *lists, n, _stream(stream)), "nq_page_copy")
 
     def append(self, layer: int, pmap: PageMap, k: torch.Tensor, v: torch.Tensor, seqs: torch.Tensor, pos: torch.Tensor,
                rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
@@ -782,6 +790,8 @@ class PagePool:
         on = _stream(stream)
         if out is None:
             out = _empty(q.shape, q.dtype, q.device, stream)
+        if B == 0:
+            return out
         if ws is None:
             need = self._attn_bytes.get((M, Hq))
             if need is None:

@@ -69,3 +69,26 @@ def test_a_pool_made_on_a_stream(nq):
     k, v = pool.read(0, m, seqs, pos)
     assert early and (k == 1).all() and (v == 1).all()
     assert (pool.data.view(torch.bfloat16) == 1).sum() == 2 * 16 * 64 and (pool.data == 0).sum() > 0
+
+
+def test_empty_lists(nq):
+    """No sequence, no request: nothing happens, as for rotation, append and read."""
+    pool, m = nq.PagePool(1, 4, 16, 2, 64, group=64), nq.PageMap(2, 2, 4, 16)
+    e = i32([])
+    m.reserve(pool, i32([1]), i32([0]), i32([20]))
+    table, held, ref = m.table.clone(), m.held.clone(), m.ref.clone()
+    assert m.reserve(pool, e, e, e).shape == (0,)
+    m.fork(e, e, e)
+    m.truncate(e, e)
+    pool.copy_pages(e, e)
+    q = torch.empty(0, 3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    assert pool.attention(0, m, q, e, 2, 0.1).shape == (0, 3, 4, 64)
+    assert pool.attention(0, m, q, e, 2, 0.1, seqs=e).shape == (0, 3, 4, 64)
+    assert torch.equal(m.table, table) and torch.equal(m.held, held) and torch.equal(m.ref, ref)
+    assert nq.device_status() == 0
+    one = i32([1])
+    for bad in (lambda: m.reserve(pool, e, one, e), lambda: m.fork(e, e, one), lambda: m.truncate(e, one),
+                lambda: pool.copy_pages(e, one), lambda: pool.attention(0, m, q, one, 2, 0.1),
+                lambda: pool.attention(0, m, q.float(), e, 2, 0.1)):
+        with pytest.raises(ValueError):
+            bad()
