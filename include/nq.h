@@ -406,7 +406,7 @@ typedef struct {
     int32_t rot_dim;
     int32_t layout;   /* nq_rope_layout */
     float mscale;
-    float mscale_lo;  /* what the exact factor has beyond its fp32 value: added to it, 0 for none */
+    float mscale_lo;  /* what the exact factor has beyond its fp32 value: added to it, 0 for none (nq_rope_mscale) */
     const uint64_t *rates;
 } nq_rope_plan;
 
@@ -415,6 +415,10 @@ typedef enum { NQ_F32 = 0, NQ_BF16 = 1 } nq_dtype;
 
 NQ_API nq_status nq_rope_rates(int rot_dim, double theta, int scaling, double factor, int old_len, uint64_t *rates,
                                float *mscale);
+
+/* The factor of a scaling in the two fp32 parts that nq_rope_plan takes: mscale as from nq_rope_rates, and what it
+ * lacks of the exact one (host-only; scaling and factor as above). */
+NQ_API nq_status nq_rope_mscale(int scaling, double factor, float *mscale, float *mscale_lo);
 
 /*
  * Rotate x [T][heads][head_dim] by pos int32 [T] (device, >= 0) into out of the

@@ -549,17 +549,27 @@ void launch_append(const Pool &p, const Map &m, const Rope &R, bool rope, const 
 }  // namespace
 }  // namespace nq
 
+extern "C" nq_status nq_rope_mscale(int scaling, double factor, float *mscale, float *mscale_lo)
+{
+    if (!mscale || !mscale_lo || scaling < NQ_ROPE_NONE || scaling > NQ_ROPE_PARTS) return NQ_ERR_ARG;
+    if (scaling != NQ_ROPE_NONE && !(factor >= 1.0 && std::isfinite(factor))) return NQ_ERR_ARG;
+    const double m = scaling == NQ_ROPE_PARTS ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    *mscale = static_cast<float>(m);
+    *mscale_lo = static_cast<float>(m - *mscale);
+    return NQ_OK;
+}
+
 extern "C" nq_status nq_rope_rates(int rot_dim, double theta, int scaling, double factor, int old_len, uint64_t *rates,
                                    float *mscale)
 {
+    float m, m_lo;
     if (!rates || !mscale || !(theta > 1.0) || !std::isfinite(theta)) return NQ_ERR_ARG;
-    if (scaling < NQ_ROPE_NONE || scaling > NQ_ROPE_PARTS) return NQ_ERR_ARG;
-    if (scaling != NQ_ROPE_NONE && !(factor >= 1.0 && std::isfinite(factor))) return NQ_ERR_ARG;
+    if (nq_rope_mscale(scaling, factor, &m, &m_lo) != NQ_OK) return NQ_ERR_ARG;
     if (scaling == NQ_ROPE_PARTS && old_len < 1) return NQ_ERR_ARG;
     if (rot_dim < 8 || rot_dim % 8 != 0 || rot_dim > 128) return NQ_ERR_SHAPE;
     const double two_pi = 6.283185307179586476925286766559;
     if (scaling == NQ_ROPE_NTK) theta *= std::pow(factor, rot_dim / (rot_dim - 2.0));
-    *mscale = scaling == NQ_ROPE_PARTS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    *mscale = m;
     for (int i = 0; i < rot_dim / 2; ++i) {
         double w = std::pow(theta, -2.0 * i / rot_dim);
         if (scaling == NQ_ROPE_LINEAR) w /= factor;

@@ -8,7 +8,6 @@ there is no fallback: a missing library raises immediately.
 from __future__ import annotations
 
 import ctypes as C
-import math
 import os
 import threading
 from dataclasses import dataclass
@@ -121,6 +120,7 @@ def lib():
                 getattr(L, name).restype = i32
             i64, RP, PP, PM, AO = C.c_int64, C.POINTER(nq_rope_plan), C.POINTER(nq_page_pool), C.POINTER(nq_page_map), C.POINTER(nq_attn_opts)
             L.nq_rope_rates.argtypes = [i32, C.c_double, i32, C.c_double, i32, vp, C.POINTER(f32)]
+            L.nq_rope_mscale.argtypes = [i32, C.c_double, C.POINTER(f32), C.POINTER(f32)]
             L.nq_rope.argtypes = [RP, vp, i32, i64, vp, i32, i32, i32, i32, vp, i32, i64, vp]
             L.nq_page_pool_bytes.argtypes = [i32, i32, i32, i32, i32, i32, i32, C.POINTER(sz)]
             L.nq_page_map_init.argtypes = [PM, vp]
@@ -136,7 +136,7 @@ def lib():
             L.nq_page_attn_workspace_bytes.argtypes = [i32, i32, i32, i32]
             L.nq_page_attn_workspace_bytes.restype = sz
             L.nq_page_attn.argtypes = [PP, i32, PM, vp, i64, i32, i32, i32, vp, vp, i32, AO, vp, vp, sz, vp]
-            for name in ("nq_rope_rates", "nq_rope", "nq_page_pool_bytes", "nq_page_map_init", "nq_page_reserve",
+            for name in ("nq_rope_rates", "nq_rope_mscale", "nq_rope", "nq_page_pool_bytes", "nq_page_map_init", "nq_page_reserve",
                          "nq_page_fork", "nq_page_truncate", "nq_page_compact", "nq_page_copy", "nq_page_append",
                          "nq_page_read", "nq_page_attn"):
                 getattr(L, name).restype = i32
@@ -560,16 +560,16 @@ class Rope:
     def __init__(self, rot_dim: int, theta: float = 10000.0, layout: str = "half", scaling: str = "none",
                  factor: float = 1.0, old_len: int = 0, device=None):
         rates = torch.empty(max(rot_dim // 2, 1), dtype=torch.int64)
-        ms = C.c_float()
+        ms, lo = C.c_float(), C.c_float()
         layouts, kinds = ("half", "interleaved"), ("none", "linear", "ntk", "parts")
         if layout not in layouts or scaling not in kinds:
             raise ValueError(f"layout is one of {layouts}, scaling one of {kinds}")
         _check(lib().nq_rope_rates(rot_dim, float(theta), kinds.index(scaling), float(factor), int(old_len),
                                    rates.data_ptr(), C.byref(ms)), "nq_rope_rates")
+        _check(lib().nq_rope_mscale(kinds.index(scaling), float(factor), C.byref(ms), C.byref(lo)), "nq_rope_mscale")
         self.rot_dim, self.mscale = rot_dim, ms.value
-        lo = 0.1 * math.log(factor) + 1.0 - ms.value if scaling == "parts" else 0.0
         self.rates = rates.to(device or torch.device("cuda"))
-        self.struct = nq_rope_plan(rot_dim, layouts.index(layout), ms.value, lo, self.rates.data_ptr())
+        self.struct = nq_rope_plan(rot_dim, layouts.index(layout), ms.value, lo.value, self.rates.data_ptr())
         self.ref = C.byref(self.struct)
 
 
