@@ -480,8 +480,12 @@ cudaError_t launch(const AttnArgs &A, cudaStream_t s, int *grid)
 template <int FMT, int D, int NG>
 cudaError_t launch_x(const AttnArgs &A, int warps, cudaStream_t s, int *grid)
 {
-    if (A.softcap > 0.0f || A.slopes) return warps == 4 ? launch<FMT, D, NG, 4, true>(A, s, grid) : launch<FMT, D, NG, 8, true>(A, s, grid);
-    return warps == 4 ? launch<FMT, D, NG, 4, false>(A, s, grid) : launch<FMT, D, NG, 8, false>(A, s, grid);
+    const bool x = A.softcap > 0.0f || A.slopes;
+    // nested pages with one scale per row come with at most 24 vectors: more go to the tensor cores
+    if constexpr (FMT == kBf16 || NG == 2)
+        if (warps == 8) return x ? launch<FMT, D, NG, 8, true>(A, s, grid) : launch<FMT, D, NG, 8, false>(A, s, grid);
+    if (warps != 4) return cudaErrorInvalidValue;
+    return x ? launch<FMT, D, NG, 4, true>(A, s, grid) : launch<FMT, D, NG, 4, false>(A, s, grid);
 }
 template <int FMT>
 cudaError_t launch_d(const AttnArgs &A, int warps, cudaStream_t s, int *grid)
