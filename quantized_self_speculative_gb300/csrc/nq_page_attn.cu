@@ -786,10 +786,15 @@ cudaError_t launch_join(const AttnArgs &A, int grid, cudaStream_t s)
 
 // Columns (query vectors) per tile.  Up to 16 a warp holds them all and decodes
 // for itself (16 vectors, 16 ragged sequences of the 8-bit view: 38 us against 64
-// on the tensor cores).  More share a CTA's decoded steps: the tensor cores from
-// 25 on where a row of the cache has one scale (36 vectors 66 us against 77, 72
-// vectors 79 against 176), else 8 columns per warp (20 vectors 58 us against 65).
-bool tensor_cores(int vectors, int fmt, int ng) { return vectors > 24 && fmt != kBf16 && ng == 1; }
+// on the tensor cores).  More share a CTA's decoded steps, 8 columns per warp, or
+// the tensor cores where a row of the cache has one scale: these from 25 vectors
+// on for heads of 128, from 33 on for heads of 64, whose steps decode half as much
+// beside the same softmax.  us on the tensor cores / per warp, 8 kv heads, 8-bit
+// view (the 4-bit view is alike):
+//                        heads of 128: 24       28       32       36   heads of 64: 28       32       36
+//   16 of 500..4000 rows       67 / 62  69 / 69  69 / 72  71 / 88       58 / 47  58 / 49  59 / 65
+//   one of 32768 rows          47 / 49  48 / 54  48 / 56  49 / 67       42 / 38  42 / 40  42 / 50
+bool tensor_cores(int vectors, int fmt, int ng, int D) { return vectors > (D == 64 ? 32 : 24) && fmt != kBf16 && ng == 1; }
 int cols_of(int vectors, bool tc)
 {
     if (tc) return vectors < 128 ? (vectors + 7) / 8 * 8 : 128;
@@ -854,7 +859,7 @@ static nq_status page_attn(const nq_page_pool *pool, int layer, const nq_page_ma
     A.G = G;
     A.g_mul = static_cast<unsigned>((0x100000000ull + G - 1) / G);
     const int fmt = p.NG == 0 ? nq::kBf16 : planes == 1 ? nq::kKv4 : nq::kKv8;
-    const bool tc = nq::tensor_cores(M * G, fmt, p.NG);
+    const bool tc = nq::tensor_cores(M * G, fmt, p.NG, p.D);
     const int cols = A.cols = nq::cols_of(M * G, tc);
     A.QT = (M * G + cols - 1) / cols;
     // the kernel numbers the steps of all segments in 32 bits

@@ -1,6 +1,6 @@
 // nq_page_attn_tc.cu -- attention over nested pages for many query vectors per
-// kv head (from 25 on: a verify pass with grouped queries), on the 5th-generation
-// tensor cores.
+// kv head (from 25 on, heads of 64 from 33: a verify pass with grouped queries), on
+// the 5th-generation tensor cores.
 //
 // With many query vectors the products and the decoding bound the time, not
 // HBM.  Here a row of the tensor cores is a query vector (up to 128 per tile):

@@ -1,15 +1,15 @@
 // nq_page_attn_wide.cu -- attention over pages for more than 16 query vectors
 // per kv head (a verify pass with grouped queries: k + 1 rows times the group):
-// nested pages up to 24, and beyond where the tensor-core kernel does not serve
-// (bf16 pages, two scales per row).
+// nested pages up to 24 (heads of 64: 32), and beyond where the tensor-core kernel
+// does not serve (bf16 pages, two scales per row).
 //
 // The same list of steps and the same arithmetic as nq_page_attn.cu, but here
 // decoding the codes and the products bound the time, not HBM: with 20 query
 // vectors that kernel would decode every block for each of two tiles.  So a CTA
 // decodes a step once, into fp16 tiles in shared memory (codes as signed
-// numbers, exact; the scales stay apart), and its four warps hold the query
-// columns between them, up to two tiles of 8 each: every warp takes all rows for
-// its own columns, and nothing is merged within a CTA.  While the warps work on
+// numbers, exact; the scales stay apart), and its four or eight warps hold the
+// query columns between them, a tile of 8 each: every warp takes all rows for its
+// own columns, and nothing is merged within a CTA.  While the warps work on
 // one step they decode the next; one barrier per step.  bf16 pages need no
 // decoding: the ring's stages are the tiles.
 // Measured (GB300): 16 sequences of 500..4000 rows, 8 kv heads of 128, 20 query
@@ -481,7 +481,7 @@ template <int FMT, int D, int NG>
 cudaError_t launch_x(const AttnArgs &A, int warps, cudaStream_t s, int *grid)
 {
     const bool x = A.softcap > 0.0f || A.slopes;
-    // nested pages with one scale per row come with at most 24 vectors: more go to the tensor cores
+    // nested pages with one scale per row come with at most 32 vectors: more go to the tensor cores
     if constexpr (FMT == kBf16 || NG == 2)
         if (warps == 8) return x ? launch<FMT, D, NG, 8, true>(A, s, grid) : launch<FMT, D, NG, 8, false>(A, s, grid);
     if (warps != 4) return cudaErrorInvalidValue;
