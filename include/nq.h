@@ -484,8 +484,8 @@ NQ_API size_t nq_page_workspace_bytes(const nq_page_map *map, int n);
 
 /*
  * Before rows first[i] .. last[i]-1 of slot seqs[i] are written: take pages so
- * that the slot holds ceil(last/page_size) of them, and give it a page of its
- * own wherever one of those rows lies on a page it shares (copy on write: the
+ * that the slot holds ceil(last/page_size) of them (none where there are no such
+ * rows), and give it a page of its own wherever one lies on a page it shares (copy on write: the
  * page's other rows are copied in every layer of pool; pool NULL skips the
  * copies).  Where all holders of a shared page ask in one call, the last of
  * them in order keeps it.  Requests are served in order; one that the free

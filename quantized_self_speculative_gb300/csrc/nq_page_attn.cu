@@ -10,8 +10,8 @@
 // dealt out in equal runs to a persistent grid, so ragged lengths balance
 // whatever they are (they are only known on the device).  The four warps of a
 // CTA take every fourth step of its run; each keeps its own softmax state and
-// its own ring of stages, filled by bulk copies of whole blocks that its lane
-// 0 issues ahead, across segment borders.  At a segment's end the warps' states
+// its own ring of stages, filled by bulk copies of whole blocks that its lanes
+// issue ahead, a block each, across segment borders.  At a segment's end the warps' states
 // merge; a segment cut by runs leaves partial states that a second, dependent
 // launch joins.  More than 16 query vectors per kv head share a CTA's decoded
 // rows instead: nq_page_attn_wide.cu, nq_page_attn_tc.cu (cols_of below).

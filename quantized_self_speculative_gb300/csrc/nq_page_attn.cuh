@@ -1,4 +1,4 @@
-// nq_page_attn.cuh -- what the two attention kernels over the paged cache share:
+// nq_page_attn.cuh -- what the three attention kernels over the paged cache share:
 // the list of steps and its runs, the ring of bulk copies, small arithmetic.
 #pragma once
 
