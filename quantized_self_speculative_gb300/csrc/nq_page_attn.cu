@@ -11,9 +11,9 @@
 // whatever they are (they are only known on the device).  The four warps of a
 // CTA take every fourth step of its run; each keeps its own softmax state and
 // its own ring of stages, filled by bulk copies of whole blocks that its lanes
-// issue ahead, a block each, across segment borders.  At a segment's end the warps' states
-// merge; a segment cut by runs leaves partial states that a second, dependent
-// launch joins.  More than 16 query vectors per kv head share a CTA's decoded
+// issue ahead, a block each, across segment borders.  At a segment's end the
+// warps' states merge; a segment cut by runs leaves partial states that a second,
+// dependent launch joins.  More than 16 query vectors per kv head share a CTA's decoded
 // rows instead: nq_page_attn_wide.cu, nq_page_attn_tc.cu (cols_of below).
 //
 // Arithmetic.  S^T = K Q^T and O^T = V^T P^T on the warp MMA (m16n8k16, fp32
@@ -26,20 +26,21 @@
 // small halves with some 18 bits, which moves a score by 10^-5 or so.  In O that
 // would show where large weights meet codes of zero, so V's codes become the
 // signed numbers themselves: the code under an exponent of 2^10, and one fma on
-// two halves that takes 2^10 and the offset off again.  K's scales multiply S, V's scales multiply P before it is rounded
-// to fp16 (one rounding, 2^-11).  So that no V magnitude underflows there, m is
-// the running maximum of s + log2(scale of V) and P = 2^(s - m) scale <= 2^15.
+// two halves that takes 2^10 and the offset off again.  K's scales multiply S, V's
+// scales multiply P before it is rounded to fp16 (one rounding, 2^-11).  So that no
+// V magnitude underflows there, m follows the running maximum of s + log2(scale of
+// V) and P = 2^(s - m) scale <= 2^15.
 // The query is brought to a largest magnitude of 2^10 by a power of two.
 // BF16: K, V and the query as they are, P rounded to bf16 (2^-8); the sum is
 // taken of the rounded P, which takes most of that error out again.
 //
 // Measured (GB300, 2070 MHz, one query row).  bf16, 4 sequences of 40001..131072
 // rows, 8 kv heads of 128: 252 us, 6.8 TB/s, the measured copy rate.  131072 rows
-// x 32 kv heads of 128: 8-bit view 171 us, 6.4 TB/s (94%); 4-bit view 119 us, 4.7
-// TB/s (69%), bound by instruction issue: 293 warp instructions per block of 16
+// x 32 kv heads of 128: 8-bit view 171 us, 6.4 TB/s (94%); 4-bit view 121 us, 4.6
+// TB/s (67%), bound by instruction issue: 298 warp instructions per block of 16
 // rows (placing codes, scales, softmax) would need 3.0 per cycle and SM to keep up
-// with HBM; the 12 warps that registers allow reach 2.1 (MMA pipe 23% busy).  32768 rows of the 4-bit view: 38 us,
-// some 10 of them launch, first fills, merge and join.
+// with HBM; the 12 warps that registers allow reach 2.1 (MMA pipe 23% busy).  32768
+// rows of the 4-bit view: 39 us, some 10 of them launch, first fills, merge and join.
 #include <atomic>
 
 #include "nq_page_attn.cuh"
@@ -785,8 +786,9 @@ cudaError_t launch_join(const AttnArgs &A, int grid, cudaStream_t s)
 }
 
 // Columns (query vectors) per tile.  Up to 16 a warp holds them all and decodes
-// for itself (16 vectors, 16 ragged sequences of the 8-bit view: 38 us against 64
-// on the tensor cores).  More share a CTA's decoded steps, 8 columns per warp, or
+// for itself (16 vectors, 16 ragged sequences of the 8-bit view: 38 us against 53
+// with a CTA's shared decoding; 5 to 16 vectors, all formats and head sizes: 0.5 to
+// 0.9 of its time).  More share a CTA's decoded steps, 8 columns per warp, or
 // the tensor cores where a row of the cache has one scale: these from 25 vectors
 // on for heads of 128, from 33 on for heads of 64, whose steps decode half as much
 // beside the same softmax.  us on the tensor cores / per warp, 8 kv heads, 8-bit

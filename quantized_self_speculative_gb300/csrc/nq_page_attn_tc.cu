@@ -21,7 +21,7 @@
 // runs, partial states and join as the other kernels.
 //
 // Measured (GB300): 16 sequences of 301..4099 rows, 8 kv heads of 128, 9 rows x 4
-// heads = 36 query vectors, 8-bit view: 67 us for 79 MB (12 us at the copy rate).
+// heads = 36 query vectors, 8-bit view: 65 us for 79 MB (12 us at the copy rate).
 // Per step of 64 rows the softmax warps take some 1730 cycles, the decoders 1300,
 // the tensor pipe 512: bound by the softmax chain (load S, scale, maximum, exp2,
 // store P), and by the ends of segments, where the pipeline drains.
@@ -343,12 +343,12 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
             bool gave_up = false;
             if (active) {
                 tc_fence_after();
-                const uint32_t gone = gone_decoded[i % kBufs];
                 uint32_t s[64];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld16(tq + kColS + 64 * b + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(s + 16 * c));
                 tc_wait_ld();
                 const float *f = reinterpret_cast<const float *>(scales + i % kBufs * Q::SCALES);
+                const uint32_t gone = gone_decoded[i % kBufs];
                 // scores in base 2 (X), or what cq makes scores of; two keys at a time in packed fp32
                 const unsigned long long zero2 = f2_pack(0.0f, 0.0f), cq2 = f2_pack(cq, cq);
 #pragma unroll
@@ -376,14 +376,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs A)
                             s[j] = __float_as_uint(fmaf(slope2, static_cast<float>(row0 + j - own), __uint_as_float(s[j])));
                     }
                 }
-                if (masked) {                 // before the window, or (negative) after the query's own row
+                if (masked || gone) {         // before the window, or (negative) after the query's own row; not there
                     const unsigned d = own - row0;
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) s[j] = d - j >= window ? 0xFF800000u : s[j];
-                }
-                if (gone) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) s[j] = gone >> (j >> 4) & 1u ? 0xFF800000u : s[j];
+                    for (int j = 0; j < 64; ++j) s[j] = d - j >= window || (gone >> (j >> 4) & 1u) ? 0xFF800000u : s[j];
                 }
                 float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};    // with the log2 of V's scales
 #pragma unroll

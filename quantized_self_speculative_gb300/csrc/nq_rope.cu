@@ -13,12 +13,13 @@
 // lane and a half pair is one shuffle away.
 //
 // Measured (GB300, 2070 MHz).  Rotation, 16384 tokens x 32 heads x 128, bf16 to
-// bf16: 43.5 us, 6.2 TB/s, HBM bound (91% of the copy rate).  Append, 8191 tokens,
-// 32 + 32 + 32 heads x 128, fp32 to nested groups of 64: 110 us, 4.9 TB/s, bound
-// by instruction issue (some 110 warp instructions per row: maximum over the
-// group, two correctly rounded quotients, the codes).  Read of the same rows:
-// 44 us, 4.6 TB/s, bound by latency: 64-byte pieces of four heads at a time.
-// A small call (144 tokens, 48 heads) takes 4 us, one launch.
+// bf16: 43.5 us, 6.2 TB/s, HBM bound (91% of the copy rate; fp32 in and out 83 us,
+// 95%).  Append, 8191 tokens, 32 + 32 + 32 heads x 128, fp32 to nested groups of 64:
+// 109 us, 5.0 TB/s, bound by instruction issue (some 110 warp instructions per row:
+// maximum over the group, two correctly rounded quotients, the codes); to bf16
+// pages 94 us (95%).  Read of the same rows: 44 us, 4.6 TB/s, bound by latency:
+// 64-byte pieces of four heads at a time; from bf16 pages 47 us (84%).  A small call
+// (144 tokens, 48 heads) takes 4.9 us, its read 2.3 us, one launch each.
 #include <cmath>
 
 #include "nq_page.cuh"
@@ -26,7 +27,7 @@
 namespace nq {
 namespace {
 
-constexpr int kWarps = 4;               // short CTAs end together: append of 8191 tokens 106 us against 109 with 8
+constexpr int kWarps = 4;               // short CTAs end together: append of 8191 tokens 3% faster than with 8
 
 struct Rope {
     int rot, layout;
@@ -500,10 +501,10 @@ nq_status rope_of(const nq_rope_plan *r, int head_dim, Rope &out)
 }
 // Heads per warp: up to 48 for prompts, where the sines of a token serve them all,
 // and down to one, so that a small call spreads over the machine (16 warps per SM).
-// Append of 8191 tokens, 96 heads (before the fixed-point sines, 4 us): 106 us with two runs, 116 with three (of q, k
-// and v rows, which cost unlike), 128 with twelve of 8.  Of 144 tokens, 48 heads:
-// 6.7 us; 12.1 in runs of 32, 8.2 with twice the warps.  Rotating 16384 tokens of
-// 32 heads: 43 us whole, 46 in runs of 8.
+// Append of 8191 tokens, 96 heads: 109 us with two runs, 119 with three (of q, k
+// and v rows, which cost unlike), 132 with twelve of 8.  Of 144 tokens, 48 heads:
+// 4.9 us; 8.5 in runs of 32, 6.5 with twice the warps.  Rotating 16384 tokens of
+// 32 heads: 44 us whole, 51 in runs of 8.
 int heads_per_warp(long long T, int heads)
 {
     int chunks = (heads + 47) / 48;
