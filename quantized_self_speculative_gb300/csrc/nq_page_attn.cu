@@ -794,8 +794,8 @@ cudaError_t launch_join(const AttnArgs &A, int grid, cudaStream_t s)
 // beside the same softmax.  us on the tensor cores / per warp, 8 kv heads, 8-bit
 // view (the 4-bit view is alike):
 //                        heads of 128: 24       28       32       36   heads of 64: 28       32       36
-//   16 of 500..4000 rows       67 / 62  69 / 69  69 / 72  71 / 88       58 / 47  58 / 49  59 / 65
-//   one of 32768 rows          47 / 49  48 / 54  48 / 56  49 / 67       42 / 38  42 / 40  42 / 50
+//   16 of 500..4000 rows       64 / 62  66 / 69  66 / 71  68 / 88       57 / 47  58 / 49  58 / 65
+//   one of 32768 rows          46 / 49  46 / 55  47 / 56  47 / 67       41 / 38  42 / 40  42 / 50
 bool tensor_cores(int vectors, int fmt, int ng, int D) { return vectors > (D == 64 ? 32 : 24) && fmt != kBf16 && ng == 1; }
 int cols_of(int vectors, bool tc)
 {

@@ -22,7 +22,7 @@
 //
 // Measured (GB300): 16 sequences of 301..4099 rows, 8 kv heads of 128, 9 rows x 4
 // heads = 36 query vectors, 8-bit view: 65 us for 79 MB (12 us at the copy rate).
-// Per step of 64 rows the softmax warps take some 1730 cycles, the decoders 1300,
+// Per step of 64 rows the softmax warps take some 1700 cycles, the decoders 1300,
 // the tensor pipe 512: bound by the softmax chain (load S, scale, maximum, exp2,
 // store P), and by the ends of segments, where the pipeline drains.
 #include <atomic>

@@ -8,7 +8,7 @@
 // few KB of ids: bound by launches and the latency of scans (cutting back and
 // extending 16 slots over 4096 pages: two calls, three launches, 11 us).  A request's
 // pages are handed out by one thread: room for a prompt of 131072 rows in pages
-// of 16 takes some 240 us, of 32768 rows 75 us, and 16 such at once 185 us.
+// of 16 takes some 230 us, of 32768 rows 70 us, and 16 such at once 180 us.
 #include "nq_page.cuh"
 
 namespace nq {
