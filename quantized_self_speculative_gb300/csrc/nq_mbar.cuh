@@ -98,8 +98,10 @@ __device__ __forceinline__ bool ring_wait(uint32_t bar, int st, uint32_t parity,
         if (*abort_flag || global_ns() - t0 > limit_ns) mine = ok = false;
     ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
     if (ok) return true;
-    *abort_flag = 1;
-    set_status(status, NQ_DEV_TIMEOUT);
+    if (*abort_flag == 0) {                   // the first to give up
+        *abort_flag = 1;
+        set_status(status, NQ_DEV_TIMEOUT);
+    }
 #pragma unroll 1
     for (t0 = global_ns(); n > 0 && global_ns() - t0 <= limit_ns;)
         if (mbar_try(bar + 8 * st, parity)) {
