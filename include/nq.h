@@ -575,8 +575,8 @@ typedef struct {
  * [batch][M][heads_q][head_dim], q with q_stride elements between the M rows
  * (a multiple of 8).  A query that sees no row gives zeros (a length of 0, or
  * less than M for the first queries).  Rows past len and pages wholly before
- * the window are never used.  A length past max_pages * page_size is clamped
- * and sets NQ_DEV_SEQ_FULL; a needed page outside the pool sets NQ_DEV_BAD_PAGE
+ * the window are never used.  A length past max_pages * page_size, or past 2^31 -
+ * 4096, is clamped and sets NQ_DEV_SEQ_FULL; a needed page outside the pool sets NQ_DEV_BAD_PAGE
  * and its rows count as hidden; a slot outside the map sets it and gives zeros.
  * planes as in nq_page_read.  Scores, sums and outputs are held in fp32;
  * probabilities enter the second product as 16-bit values.

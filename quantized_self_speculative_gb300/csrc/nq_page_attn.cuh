@@ -221,7 +221,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &A, int b, bool report)
 {
     Seq s;
     s.slot = A.seqs ? A.seqs[b] : b;
-    const long long cap = static_cast<long long>(A.m.W) * A.m.P;
+    const long long cap = min(static_cast<long long>(A.m.W) * A.m.P, 0x7ffff000ll);   // rows of a step past the last one stay in 32 bits
     int n = A.len[b];
     if (n > cap) {
         n = static_cast<int>(cap);

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from paged_helpers import HostPool, rows_of
+from paged_helpers import HostPool, attention64, rows_of
 from test_gpu_page_attn import FORMATS, cache, check, i32, query
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +111,24 @@ def test_a_row_that_was_not_finite_is_zeros_to_every_reader(nq, planes, g, M, D,
         assert (x[1, 0, :G] == 0).all() and (x[3, 0, D - G:] == 0).all() and (x[0] != 0).all() and (x[2] != 0).all()
         assert (x[1, 0, G:] != 0).all() and (x[3, 0, :D - G] != 0).all()
         check(nq, pool, m, lens, query(361, 2, M, g, D), planes, D ** -0.5)
+
+
+@pytest.mark.parametrize("fmt,planes", FORMATS)
+def test_lengths_up_to_the_largest(nq, fmt, planes):
+    """2^27 - 1 pages that are all one and the same: row t is row t mod 16, wherever the window lies.  Lengths past
+    2^31 - 4096 are clamped and reported."""
+    W, P, D = (1 << 27) - 1, 16, 64
+    pool, small = cache(nq, [P], 1, D, D, P, kind(nq, fmt), 370)
+    one = int(small.table[0, 0])
+    m = nq.PageMap(1, W, pool.n_pages, P, table=torch.full((1, W), one, dtype=torch.int32, device="cuda"))
+    few = np.full((1, 20), one)
+    most = 2 ** 31 - 4096
+    for g, M in VECTORS:
+        q = query(371, 1, M, g, D)
+        for n in (most - 7, most - 64, most, most + 1, W * P - 9, W * P, 2 ** 31 - 1):
+            at = min(n, most)
+            n0 = 256 + at % 16
+            ref, tol = attention64(HostPool(pool), 0, few, q.float().cpu().numpy(), [n0], planes, 0.125, window=70)
+            out = pool.attention(0, m, q, i32([n]), planes, 0.125, window=70).double().cpu().numpy()
+            assert nq.device_status() == (nq.NQ_DEV_SEQ_FULL if n > most else 0)
+            assert (np.abs(out - ref) <= tol).all()
