@@ -73,6 +73,7 @@ typedef enum {
 #define NQ_DEV_SEQ_FULL  0x10u  /* spec_round_commit: a sequence buffer was full, tokens dropped */
 #define NQ_DEV_BAD_PAGE  0x20u  /* a page id, sequence slot or row outside the map or the pool */
 #define NQ_DEV_POOL_FULL 0x40u  /* nq_page_reserve: too few free pages for a request */
+#define NQ_DEV_BAD_TREE  0x80u  /* nq_tree_plan: a node above which not only lower nodes lie */
 
 /*
  * Weight formats (SpecQuant Sec. III.A tiers; BitNest Fig. 3 planes).
@@ -586,6 +587,91 @@ NQ_API nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_page
                               int64_t q_stride, int batch, int M, int heads_q, const int32_t *seqs,
                               const int32_t *len, int planes, const nq_attn_opts *opts, uint16_t *out, void *ws,
                               size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------- trees of drafted tokens
+ * Instead of one chain a draft may propose a tree per sequence: node m is a
+ * token, parents[m] < m the node that it follows, -1 where it follows the last
+ * committed row, less than -1 a node that is not used (ragged trees of a batch).
+ * By convention node 0 is the last committed token itself, whose row the pass
+ * computes, and the drafted tokens lie below it.  In the cache node m is row
+ * base + m (base committed rows), at position base + depth(m), depth 0 for
+ * parent -1.  A node sees the committed rows, the nodes on its way up and itself.
+ * Host struct; batch <= 65535 for the acceptance, nodes <= 1024.
+ */
+typedef struct {
+    int32_t batch, nodes;
+    int32_t window;           /* that of the attention (nq_attn_opts), 0: none */
+    int32_t pad;
+    const int32_t *parents;   /* device int32 [batch][nodes] */
+    int32_t *depth;           /* device int32 [batch][nodes], written by nq_tree_plan; -1: not used */
+    uint32_t *bits;           /* device uint32 [batch][nodes][ceil(nodes / 32)], likewise: bit j of node m where it sees node j */
+} nq_tree;
+
+/*
+ * Depths and masks from the parents; one plan serves all layers of a round.  A
+ * node whose parent is not below its own number, or is a node that is not used,
+ * counts as not used and sets NQ_DEV_BAD_TREE.
+ */
+NQ_API nq_status nq_tree_plan(const nq_tree *tree, cudaStream_t stream);
+
+/*
+ * Greedy acceptance along trees (the tree form of spec_accept_greedy):
+ *   t_m = argmax_x logits[b][m][x] (lowest index on ties);  n_0 = 0;
+ *   n_{j+1} = the lowest child c of n_j with tokens[b][c] == t_{n_j}, while there is one;
+ *   out_tok[b][j] = t_{n_j}, path[b][j] = n_j, j < out_cnt[b] <= width; then -1 pads.
+ * tokens: int32 [batch][nodes] (that of node 0 is not used); logits: fp32
+ * [batch][nodes][V]; out_tok, path: int32 [batch][width]; out_cnt: int32 [batch],
+ * 0 where node 0 is not used.  1 <= width <= nodes; a walk that is longer ends
+ * there.  Only the logits of the walk are read; one that is not finite sets
+ * NQ_DEV_NONFINITE (that row's output is then unspecified).  A token outside
+ * [0, V) matches nothing and sets NQ_DEV_BAD_TOKEN.  V <= 524288.  out_tok and
+ * out_cnt go on to spec_round_commit with k = width - 1.
+ */
+NQ_API nq_status spec_accept_tree(const nq_tree *tree, const int32_t *tokens, const float *logits, int V, int width,
+                                  int32_t *out_tok, int32_t *out_cnt, int32_t *path, cudaStream_t stream);
+
+/*
+ * After acceptance: rows first[i] + path[i][j] of slot seqs[i] become rows first[i]
+ * + j, j < count[i], in every layer of the pool (the accepted path moves next to
+ * the committed rows).  path: int32 [n][width], rising from >= 0 within a sequence;
+ * all of its rows are read before they are overwritten.  A sequence whose path does
+ * not rise, or with a count outside 0 .. width, or a slot outside the map, is left
+ * out whole and sets NQ_DEV_BAD_PAGE; a move from or to a row without a page is left
+ * out (NQ_DEV_BAD_PAGE, past the last page NQ_DEV_SEQ_FULL).  The slots of a call
+ * are distinct, and the rows written lie on pages that no other slot holds (as
+ * nq_page_reserve gives them).
+ */
+NQ_API nq_status nq_page_keep(const nq_page_pool *pool, const nq_page_map *map, const int32_t *seqs, const int32_t *first,
+                              const int32_t *path, const int32_t *count, int n, int width, cudaStream_t stream);
+
+/*
+ * nq_page_append with positions of their own for the rotation: token t is row
+ * rows[t], rotated by at[t] >= 0 (a tree's nodes: base + m and base + depth).
+ */
+NQ_API nq_status nq_page_append_at(const nq_page_pool *pool, int layer, const nq_page_map *map, const nq_rope_plan *rope,
+                                   const void *q, const void *k, const void *v, int dtype, int64_t stride,
+                                   const int32_t *seqs, const int32_t *rows, const int32_t *at, int T, int heads_q,
+                                   uint16_t *q_out, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------- between two linears
+ * Root-mean-square norm of M rows of K values, with the residual's addition before it:
+ *   s = x + add (rounded once to x's type, into sum);  y = s / sqrt(mean(s^2) + eps) * weight,
+ * without add s = x and sum is NULL.  x, add and weight each fp32 or bf16
+ * (nq_dtype); add and weight may be NULL; sum has x's type and may be x itself.
+ * Rows lie *_stride elements apart (multiples of 8, at least K), those of y and xq K.
+ * y: bf16 [M][K], or NULL.  xq, sx: NULL, or int8 [M][K] and fp32 [M] as
+ * nq_quantize_act_int8 gives them, of the fp32 y (not of its bf16 rounding):
+ * sx = max|y| / 127, codes clamp(rint(y / sx), -127, 127), zeros where sx is 0.
+ * At least one of y and xq.  Sums in fp32; a row's result does not depend on M.
+ * A row whose sum of squares is not a finite fp32 (or, for codes, whose y is not)
+ * sets NQ_DEV_NONFINITE; its codes and sx are zero.  K a multiple of 8 up to
+ * 16384, eps > 0.
+ */
+NQ_API nq_status nq_rms_norm(const void *x, int x_dtype, int64_t x_stride, const void *add, int add_dtype, int64_t add_stride,
+                             const void *weight, int w_dtype, float eps, int M, int K, void *sum, int64_t sum_stride,
+                             uint16_t *y, int8_t *xq, float *sx, cudaStream_t stream);
 
 /*
  * Greedy acceptance that allocates nothing and takes no workspace: the same

@@ -368,8 +368,8 @@ template <int D, int NG, typename TI>
 __global__ void __launch_bounds__(kWarps * 32)
 append_kernel(Pool p, Map m, Rope R, bool rope, const TI *__restrict__ q, const TI *__restrict__ k,
               const TI *__restrict__ v, long long stride, const int32_t *__restrict__ seqs,
-              const int32_t *__restrict__ pos, int T, int Hq, int per, int chunks, __nv_bfloat16 *__restrict__ q_out,
-              unsigned int *status)
+              const int32_t *__restrict__ pos, const int32_t *__restrict__ angle, int T, int Hq, int per, int chunks,
+              __nv_bfloat16 *__restrict__ q_out, unsigned int *status)
 {
     constexpr int E = D / 32;
     const long long wi = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -381,7 +381,7 @@ append_kernel(Pool p, Map m, Rope R, bool rope, const TI *__restrict__ q, const 
     const Row w = row_of(p, m, seqs[t], ps, status, lane == 0 && h1 > Hq);
     Turn<E> tn{};
     const bool turned = rope && h0 < Hq + H;
-    if (turned) tn = make_turn<E>(R, ps, lane, false);
+    if (turned) tn = make_turn<E>(R, angle[t], lane, false);
     const long long at = t * stride + lane * E;
     if (h0 < Hq) {
         __nv_bfloat16 *to = q_out + (t * Hq + h0) * D + lane * E;
@@ -537,14 +537,14 @@ void launch_rope_t(const Rope &R, const void *x, int xt, long long xs, const int
 
 template <int D, int NG, typename TI>
 void launch_append(const Pool &p, const Map &m, const Rope &R, bool rope, const void *q, const void *k, const void *v,
-                   long long stride, const int32_t *seqs, const int32_t *pos, int T, int Hq, void *q_out,
+                   long long stride, const int32_t *seqs, const int32_t *pos, const int32_t *angle, int T, int Hq, void *q_out,
                    unsigned int *status, cudaStream_t s)
 {
     const int all = Hq + 2 * p.H, per = heads_per_warp(T, all), chunks = (all + per - 1) / per;
     const long long warps = static_cast<long long>(T) * chunks;
     append_kernel<D, NG, TI><<<static_cast<unsigned>((warps + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(
         p, m, R, rope, static_cast<const TI *>(q), static_cast<const TI *>(k), static_cast<const TI *>(v), stride, seqs,
-        pos, T, Hq, per, chunks, static_cast<__nv_bfloat16 *>(q_out), status);
+        pos, angle, T, Hq, per, chunks, static_cast<__nv_bfloat16 *>(q_out), status);
 }
 
 }  // namespace
@@ -607,16 +607,16 @@ extern "C" nq_status nq_rope(const nq_rope_plan *rope, const void *x, int x_dtyp
     return nq::cuda_status(cudaGetLastError());
 }
 
-extern "C" nq_status nq_page_append(const nq_page_pool *pool, int layer, const nq_page_map *map,
-                                    const nq_rope_plan *rope, const void *q, const void *k, const void *v, int dtype,
-                                    int64_t stride, const int32_t *seqs, const int32_t *pos, int T, int heads_q,
-                                    uint16_t *q_out, cudaStream_t stream)
+extern "C" nq_status nq_page_append_at(const nq_page_pool *pool, int layer, const nq_page_map *map,
+                                       const nq_rope_plan *rope, const void *q, const void *k, const void *v, int dtype,
+                                       int64_t stride, const int32_t *seqs, const int32_t *pos, const int32_t *angle, int T,
+                                       int heads_q, uint16_t *q_out, cudaStream_t stream)
 {
     nq::Pool p;
     nq::Map m;
     nq_status st = nq::pool_map_of(pool, map, p, m, false);
     if (st != NQ_OK) return st;
-    if (layer < 0 || layer >= pool->layers || !k || !v || !seqs || !pos || T < 1) return NQ_ERR_ARG;
+    if (layer < 0 || layer >= pool->layers || !k || !v || !seqs || !pos || !angle || T < 1) return NQ_ERR_ARG;
     if (!(dtype == NQ_F32 || dtype == NQ_BF16)) return NQ_ERR_ARG;
     if (q ? (heads_q < 1 || !q_out) : (heads_q != 0 || q_out != nullptr)) return NQ_ERR_ARG;
     if (heads_q > 65536) return NQ_ERR_SHAPE;
@@ -628,7 +628,7 @@ extern "C" nq_status nq_page_append(const nq_page_pool *pool, int layer, const n
         if (st != NQ_OK) return st;
     }
     if (!nq::aligned16(k) || !nq::aligned16(v) || !nq::aligned16(q) || !nq::aligned16(q_out) || !nq::aligned4(seqs) ||
-        !nq::aligned4(pos))
+        !nq::aligned4(pos) || !nq::aligned4(angle))
         return NQ_ERR_ALIGN;
     if (static_cast<double>(T) * (heads_q + 2.0 * p.H) / nq::kWarps > 2147483000.0) return NQ_ERR_SHAPE;
     unsigned int *status = nq::device_status_ptr();
@@ -637,9 +637,9 @@ extern "C" nq_status nq_page_append(const nq_page_pool *pool, int layer, const n
     auto go = [&](auto d, auto ng) {
         constexpr int D = decltype(d)::value, NG = decltype(ng)::value;
         if (dtype == NQ_F32)
-            nq::launch_append<D, NG, float>(p, m, R, rope != nullptr, q, k, v, stride, seqs, pos, T, heads_q, q_out, status, stream);
+            nq::launch_append<D, NG, float>(p, m, R, rope != nullptr, q, k, v, stride, seqs, pos, angle, T, heads_q, q_out, status, stream);
         else
-            nq::launch_append<D, NG, __nv_bfloat16>(p, m, R, rope != nullptr, q, k, v, stride, seqs, pos, T, heads_q, q_out, status, stream);
+            nq::launch_append<D, NG, __nv_bfloat16>(p, m, R, rope != nullptr, q, k, v, stride, seqs, pos, angle, T, heads_q, q_out, status, stream);
     };
     using std::integral_constant;
     const integral_constant<int, 64> d64;
@@ -650,6 +650,14 @@ extern "C" nq_status nq_page_append(const nq_page_pool *pool, int layer, const n
     if (p.D == 64) p.NG == 0 ? go(d64, bf) : go(d64, g1);
     else p.NG == 0 ? go(d128, bf) : p.NG == 1 ? go(d128, g1) : go(d128, g2);
     return nq::cuda_status(cudaGetLastError());
+}
+
+extern "C" nq_status nq_page_append(const nq_page_pool *pool, int layer, const nq_page_map *map,
+                                    const nq_rope_plan *rope, const void *q, const void *k, const void *v, int dtype,
+                                    int64_t stride, const int32_t *seqs, const int32_t *pos, int T, int heads_q,
+                                    uint16_t *q_out, cudaStream_t stream)
+{
+    return nq_page_append_at(pool, layer, map, rope, q, k, v, dtype, stride, seqs, pos, pos, T, heads_q, q_out, stream);
 }
 
 extern "C" nq_status nq_page_read(const nq_page_pool *pool, int layer, const nq_page_map *map, const int32_t *seqs,

@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libnq.so")
 NQ_OK, NQ_ERR_ARG, NQ_ERR_SHAPE, NQ_ERR_ALIGN, NQ_ERR_CUDA = 0, 1, 2, 3, 4
 NQ_ERR_NONFINITE, NQ_ERR_TIMEOUT, NQ_ERR_WORKSPACE, NQ_ERR_TOKEN = 5, 6, 7, 8
 NQ_DEV_NONFINITE, NQ_DEV_BAD_TOKEN, NQ_DEV_TIMEOUT, NQ_DEV_ACT_RANGE, NQ_DEV_SEQ_FULL = 0x1, 0x2, 0x4, 0x8, 0x10
-NQ_DEV_BAD_PAGE, NQ_DEV_POOL_FULL = 0x20, 0x40
+NQ_DEV_BAD_PAGE, NQ_DEV_POOL_FULL, NQ_DEV_BAD_TREE = 0x20, 0x40, 0x80
 KV_NESTED44, KV_BF16 = 0, 1
 FMT_NESTED44, FMT_INT4, FMT_FP8E4M3_ROW, FMT_FP16 = 0, 1, 2, 3
 
@@ -65,6 +65,11 @@ class nq_page_map(C.Structure):
 class nq_attn_opts(C.Structure):
     _fields_ = [("scale", C.c_float), ("softcap", C.c_float), ("window", C.c_int32), ("pad", C.c_int32),
                 ("slopes", C.c_void_p)]
+
+
+class nq_tree(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("nodes", C.c_int32), ("window", C.c_int32), ("pad", C.c_int32),
+                ("parents", C.c_void_p), ("depth", C.c_void_p), ("bits", C.c_void_p)]
 
 
 def lib():
@@ -136,6 +141,14 @@ def lib():
             L.nq_page_attn_workspace_bytes.argtypes = [i32, i32, i32, i32]
             L.nq_page_attn_workspace_bytes.restype = sz
             L.nq_page_attn.argtypes = [PP, i32, PM, vp, i64, i32, i32, i32, vp, vp, i32, AO, vp, vp, sz, vp]
+            TR = C.POINTER(nq_tree)
+            L.nq_tree_plan.argtypes = [TR, vp]
+            L.spec_accept_tree.argtypes = [TR, vp, vp, i32, i32, vp, vp, vp, vp]
+            L.nq_page_keep.argtypes = [PP, PM, vp, vp, vp, vp, i32, i32, vp]
+            L.nq_page_append_at.argtypes = [PP, i32, PM, RP, vp, vp, vp, i32, i64, vp, vp, vp, i32, i32, vp, vp]
+            L.nq_rms_norm.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, f32, i32, i32, vp, i64, vp, vp, vp, vp]
+            for name in ("nq_tree_plan", "spec_accept_tree", "nq_page_keep", "nq_page_append_at", "nq_rms_norm"):
+                getattr(L, name).restype = i32
             for name in ("nq_rope_rates", "nq_rope_mscale", "nq_rope", "nq_page_pool_bytes", "nq_page_map_init", "nq_page_reserve",
                          "nq_page_fork", "nq_page_truncate", "nq_page_compact", "nq_page_copy", "nq_page_append",
                          "nq_page_read", "nq_page_attn"):
@@ -595,6 +608,98 @@ def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Ten
     return out
 
 
+# ---------------------------------------------------------------- between two linears
+def _matrix(t: torch.Tensor, M: int, K: int, what: str):
+    """Address, type and row stride of fp32 or bf16 [M][K], each row contiguous."""
+    if not t.is_cuda or t.dtype not in _DT or t.shape != (M, K) or (t.stride(1) != 1 and K > 1):
+        raise ValueError(f"{what} must be a CUDA tensor of fp32 or bf16, shape {(M, K)}, contiguous within a row")
+    return t.data_ptr(), _DT[t.dtype], t.stride(0) if M > 1 else K
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, add: Optional[torch.Tensor] = None,
+             quantize: bool = False, sum_out: Optional[torch.Tensor] = None, y=None, xq=None, sx=None, stream=None):
+    """Root-mean-square norm of the rows of x [M][K] (fp32 or bf16; rows may be
+    strided), of x + add where add is given (nq_rms_norm).  Returns (s, y): s the
+    sum in x's type (in sum_out, which may be x; x itself without add), y bf16; with
+    quantize (s, xq, sx): int8 codes and fp32 row scales for LinearA8Batch."""
+    if x.dim() != 2:
+        raise ValueError("x must be fp32 or bf16 [M][K]")
+    M, K = x.shape
+    xp = _matrix(x, M, K, "x")
+    ap = (None, 0, 0) if add is None else _matrix(add, M, K, "add")
+    if weight is not None and (weight.shape != (K,) or weight.dtype not in _DT or not weight.is_cuda or not weight.is_contiguous()):
+        raise ValueError("weight must be a contiguous CUDA tensor of fp32 or bf16 [K]")
+    if sum_out is not None and (add is None or sum_out.dtype != x.dtype):
+        raise ValueError("sum_out comes with add and has x's type")
+    if (y is not None) if quantize else (xq is not None or sx is not None):
+        raise ValueError("y without quantize, xq and sx with it")
+    s = x if add is None else sum_out if sum_out is not None else _empty((M, K), x.dtype, x.device, stream)
+    sp = (None, 0, 0) if add is None else _matrix(s, M, K, "sum_out")
+    if quantize:
+        xq = xq if xq is not None else _empty((M, K), torch.int8, x.device, stream)
+        sx = sx if sx is not None else _empty((M,), torch.float32, x.device, stream)
+        if xq.shape != (M, K) or sx.shape != (M,):
+            raise ValueError("xq must be int8 [M][K], sx fp32 [M]")
+        out = None, _dev(xq, torch.int8, "xq"), _dev(sx, torch.float32, "sx")
+    else:
+        y = y if y is not None else _empty((M, K), torch.bfloat16, x.device, stream)
+        if y.shape != (M, K):
+            raise ValueError("y must be bf16 [M][K]")
+        out = _dev(y, torch.bfloat16, "y"), None, None
+    if M:
+        _check(lib().nq_rms_norm(*xp, *ap, None if weight is None else weight.data_ptr(), 0 if weight is None else _DT[weight.dtype],
+                                 float(eps), M, K, sp[0], sp[2], *out, _stream(stream)), "nq_rms_norm")
+    return (s, xq, sx) if quantize else (s, y)
+
+
+# ---------------------------------------------------------------- trees of drafted tokens
+class Tree:
+    """Trees of drafted tokens, one per sequence (nq_tree): parents int32
+    [batch][nodes], each below its node's number; -1 follows the committed rows, less
+    marks a node that is not used.  By convention node 0 is the last committed
+    token.  Made once a round: depth int32 [batch][nodes] (-1: not used) and bits
+    int32 [batch][nodes][ceil(nodes / 32)] serve all layers.  window as in the
+    attention that uses it."""
+
+    def __init__(self, parents: torch.Tensor, window: int = 0, stream=None):
+        if parents.dim() != 2:
+            raise ValueError("parents must be int32 [batch][nodes]")
+        self.batch, self.nodes = parents.shape
+        self.parents, self.window = parents, int(window)
+        p = _dev(parents, torch.int32, "parents")
+        self.depth = _empty((self.batch, self.nodes), torch.int32, parents.device, stream)
+        self.bits = _empty((self.batch, self.nodes, -(-self.nodes // 32)), torch.int32, parents.device, stream)
+        self.struct = nq_tree(self.batch, self.nodes, self.window, 0, p, self.depth.data_ptr(), self.bits.data_ptr())
+        self.ref = C.byref(self.struct)
+        if self.batch:
+            _check(lib().nq_tree_plan(self.ref, _stream(stream)), "nq_tree_plan")
+
+    def positions(self, base: torch.Tensor) -> torch.Tensor:
+        """Positions int32 [batch][nodes] of the nodes above base int32 [batch] committed rows (a node not used: base's)."""
+        return base[:, None] + self.depth.clamp(min=0)
+
+
+def accept_tree(tokens: torch.Tensor, logits: torch.Tensor, tree: Tree, width: Optional[int] = None, out_tok=None, out_cnt=None,
+                path=None, stream=None):
+    """Greedy acceptance along the trees (spec_accept_tree): tokens int32
+    [batch][nodes], logits fp32 [batch][nodes][V].  Returns the emitted tokens
+    [batch][width], their number [batch] and the nodes that emitted them [batch][width]."""
+    B, M = tree.batch, tree.nodes
+    width = M if width is None else int(width)
+    if tokens.shape != (B, M) or logits.dim() != 3 or logits.shape[:2] != (B, M):
+        raise ValueError("tokens must be [batch][nodes] and logits [batch][nodes][V]")
+    mk = lambda t, *s: t if t is not None else _empty(s, torch.int32, logits.device, stream)  # noqa: E731
+    out_tok, out_cnt, path = mk(out_tok, B, width), mk(out_cnt, B), mk(path, B, width)
+    if out_tok.shape != (B, width) or out_cnt.shape != (B,) or path.shape != (B, width):
+        raise ValueError("out_tok and path must be int32 [batch][width], out_cnt int32 [batch]")
+    if B:
+        _check(lib().spec_accept_tree(tree.ref, _dev(tokens, torch.int32, "tokens"), _dev(logits, torch.float32, "logits"),
+                                      logits.shape[2], width, _dev(out_tok, torch.int32, "out_tok"),
+                                      _dev(out_cnt, torch.int32, "out_cnt"), _dev(path, torch.int32, "path"), _stream(stream)),
+               "spec_accept_tree")
+    return out_tok, out_cnt, path
+
+
 # ---------------------------------------------------------------- paged KV cache
 class PageMap:
     """Which pages the sequence slots hold (nq_page_map).  Device tensors int32:
@@ -717,10 +822,11 @@ class PagePool:
 
     def append(self, layer: int, pmap: PageMap, k: torch.Tensor, v: torch.Tensor, seqs: torch.Tensor, pos: torch.Tensor,
                rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
-               stream=None) -> Optional[torch.Tensor]:
+               stream=None, at: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
         """Store k, v [T][heads_kv][head_dim] (fp32 or bf16) as row pos[t] of slot
-        seqs[t], k rotated by pos; with q [T][heads_q][head_dim] returns the
-        rotated queries in bf16.  q, k and v may be columns of one tensor."""
+        seqs[t], k rotated by pos (by at, where given: a tree's nodes); with q
+        [T][heads_q][head_dim] returns the rotated queries in bf16.  q, k and v may
+        be columns of one tensor."""
         T, H, D = k.shape[0], self.heads_kv, self.head_dim
         if k.dtype not in _DT:
             raise ValueError("k must be fp32 or bf16")
@@ -734,13 +840,29 @@ class PagePool:
             q_out = _empty((T, Hq, D), torch.bfloat16, q.device, stream)
         if T == 0:
             return q_out
-        _check(lib().nq_page_append(self.ptr, layer, pmap.ptr, None if rope is None else rope.ref,
-                                    None if q is None else _heads(q, T, Hq, D, k.dtype, "q"),
-                                    _heads(k, T, H, D, k.dtype, "k"), _heads(v, T, H, D, k.dtype, "v"), _DT[k.dtype],
-                                    stride, PageMap._list(seqs, T, "seqs"), PageMap._list(pos, T, "pos"), T, Hq,
-                                    None if q is None else self._rows(q_out, (T, Hq, D), "q_out"), _stream(stream)),
-               "nq_page_append")
+        rows = PageMap._list(pos, T, "pos")
+        _check(lib().nq_page_append_at(self.ptr, layer, pmap.ptr, None if rope is None else rope.ref,
+                                       None if q is None else _heads(q, T, Hq, D, k.dtype, "q"),
+                                       _heads(k, T, H, D, k.dtype, "k"), _heads(v, T, H, D, k.dtype, "v"), _DT[k.dtype],
+                                       stride, PageMap._list(seqs, T, "seqs"), rows,
+                                       rows if at is None else PageMap._list(at, T, "at"), T, Hq,
+                                       None if q is None else self._rows(q_out, (T, Hq, D), "q_out"), _stream(stream)),
+               "nq_page_append_at")
         return q_out
+
+    def keep(self, pmap: PageMap, seqs: torch.Tensor, first: torch.Tensor, path: torch.Tensor, count: torch.Tensor,
+             stream=None) -> None:
+        """Rows first[i] + path[i][j] of slot seqs[i] become rows first[i] + j,
+        j < count[i], in every layer: the accepted path (int32 [n][width], rising) of
+        a tree whose nodes were appended from row first[i] on."""
+        if path.dim() != 2:
+            raise ValueError("path must be int32 [n][width]")
+        n, width = path.shape
+        lists = (PageMap._list(seqs, n, "seqs"), PageMap._list(first, n, "first"), _dev(path, torch.int32, "path"),
+                 PageMap._list(count, n, "count"))
+        if n == 0 or width == 0:
+            return
+        _check(lib().nq_page_keep(self.ptr, pmap.ptr, *lists, n, width, _stream(stream)), "nq_page_keep")
 
     @staticmethod
     def _rows(t: torch.Tensor, shape, what: str) -> int:
