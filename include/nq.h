@@ -655,6 +655,21 @@ NQ_API nq_status nq_page_append_at(const nq_page_pool *pool, int layer, const nq
                                    uint16_t *q_out, cudaStream_t stream);
 
 /*
+ * nq_page_attn of trees: tree->nodes query rows for each of tree->batch sequences,
+ * whose newest `nodes` rows are the trees' (len counts them all, used or not).
+ * Node m sees the committed rows t < len - nodes at positions t, and its nodes (bits)
+ * at positions len - nodes + depth; window and slopes go by positions, and
+ * opts->window has to be the plan's.  A node that is not used gives zeros, and
+ * its row, which may hold anything, is used by no other.  Everything else
+ * as in nq_page_attn.
+ */
+NQ_API size_t nq_page_attn_tree_workspace_bytes(int nodes, int heads_q, int heads_kv, int head_dim);
+NQ_API nq_status nq_page_attn_tree(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,
+                                   int64_t q_stride, int heads_q, const int32_t *seqs, const int32_t *len, int planes,
+                                   const nq_attn_opts *opts, const nq_tree *tree, uint16_t *out, void *ws,
+                                   size_t ws_bytes, cudaStream_t stream);
+
+/*
  * ---------------------------------------------------------------- between two linears
  * Root-mean-square norm of M rows of K values, with the residual's addition before it:
  *   s = x + add (rounded once to x's type, into sum);  y = s / sqrt(mean(s^2) + eps) * weight,

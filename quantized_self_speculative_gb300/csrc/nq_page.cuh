@@ -90,4 +90,13 @@ inline nq_status pool_map_of(const nq_page_pool *p, const nq_page_map *m, Pool &
     return p->n_pages == m->n_pages && p->page_size == m->page_size ? NQ_OK : NQ_ERR_SHAPE;
 }
 
+// Trees of drafted tokens (nq_tree).
+constexpr int kMaxNodes = 1024;
+inline nq_status tree_of(const nq_tree *t)
+{
+    if (!t || t->batch < 1 || t->nodes < 1 || t->window < 0 || !t->parents || !t->depth || !t->bits) return NQ_ERR_ARG;
+    if (t->nodes > kMaxNodes) return NQ_ERR_SHAPE;
+    return aligned4(t->parents) && aligned4(t->depth) && aligned4(t->bits) ? NQ_OK : NQ_ERR_ALIGN;
+}
+
 }  // namespace nq

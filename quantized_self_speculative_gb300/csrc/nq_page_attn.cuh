@@ -37,6 +37,9 @@ struct AttnArgs {
     unsigned int *status;
     unsigned long long wait_ns;         // limit of a wait on a barrier
     int starve;                         // steps after which each feed stops (a diagnostic); -1: none
+    const uint32_t *tree_bits;          // trees (the kernels' T forms): what node m of sequence b sees, and its depth
+    const int32_t *tree_depth;
+    int tree_words;
 };
 
 // Query row of vector v = row * G + head of the group (v, G <= 2^16).
@@ -45,6 +48,9 @@ __device__ __forceinline__ int row_of_vector(const AttnArgs &A, int v) { return 
 // More than 16 query vectors per kv head: tiles of A.cols columns, *grid CTAs.
 cudaError_t attn_wide(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);   // nq_page_attn_wide.cu, 32 or 64
 cudaError_t attn_tc(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);     // nq_page_attn_tc.cu, up to 128
+// Trees: the T forms of the first two.
+cudaError_t attn_tree(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);        // nq_page_attn_tree.cu, 8 or 16
+cudaError_t attn_tree_wide(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);   // nq_page_attn_tree_wide.cu, 32 or 64
 // Bytes of a block of 16 rows: base (or bf16), and refinement where it is read.
 __host__ __device__ constexpr int block_base(int fmt, int D, int NG) { return fmt == kBf16 ? 64 * D : 16 * D + 64 * NG; }
 __host__ __device__ constexpr int block_resid(int fmt, int D) { return fmt == kKv8 ? 16 * D : 0; }
@@ -150,6 +156,29 @@ __device__ __forceinline__ int first_seen(const AttnArgs &A, int own)
 {
     return A.window > 0 && own >= A.window ? own - A.window + 1 : 0;
 }
+// The tree of a sequence of which `base` rows are committed: node j lies in row base + j.
+struct TreeOf {
+    const uint32_t *bits;
+    const int32_t *depth;
+    int base, M, words;
+    __device__ __forceinline__ TreeOf() {}
+    __device__ __forceinline__ TreeOf(const AttnArgs &A, int b, int hi)
+        : bits(A.tree_bits + static_cast<size_t>(b) * A.M * A.tree_words), depth(A.tree_depth + static_cast<size_t>(b) * A.M), base(hi - A.M), M(A.M),
+          words(A.tree_words)
+    {
+    }
+    __device__ __forceinline__ bool used(int m) const { return depth[m] >= 0; }
+    // a row that some node's query may see: one of an unused node may hold anything
+    __device__ __forceinline__ bool live(int row) const { return row < base || (row - base < M && used(row - base)); }
+    __device__ __forceinline__ int position(int row) const { return row < base || row - base >= M ? row : base + depth[row - base]; }
+    // whether node m, at position `own`, sees a row (the window of the nodes is in their bits)
+    __device__ __forceinline__ bool sees(int m, int own, int row, unsigned window) const
+    {
+        const int j = row - base;
+        if (j < 0) return static_cast<unsigned>(own - row) < window;
+        return j < M && (bits[static_cast<size_t>(m) * words + (j >> 5)] >> (j & 31) & 1u);
+    }
+};
 // max over the eight lanes of a query column, sum likewise
 __device__ __forceinline__ float col_max(float x)
 {

@@ -1,0 +1,14 @@
+// nq_page_attn_tree_wide.cu -- attention of trees over pages for more than 16 query
+// vectors per kv head: the T form of nq_page_attn_wide.cuh (masks as in
+// nq_page_attn_tree.cu).
+#include "nq_page_attn_wide.cuh"
+
+namespace nq {
+
+cudaError_t attn_tree_wide(int fmt, const AttnArgs &A, cudaStream_t s, int *grid)
+{
+    const int warps = A.cols / 8;
+    return fmt == kBf16 ? launch_d<kBf16, true>(A, warps, s, grid) : fmt == kKv4 ? launch_d<kKv4, true>(A, warps, s, grid) : launch_d<kKv8, true>(A, warps, s, grid);
+}
+
+}  // namespace nq

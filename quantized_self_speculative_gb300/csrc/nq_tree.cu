@@ -23,8 +23,6 @@ namespace nq {
 namespace {
 
 // ---------------------------------------------------------------- plan
-constexpr int kMaxNodes = 1024;
-
 __global__ void __launch_bounds__(kMaxNodes)
 plan_kernel(const int32_t *__restrict__ parents, int M, int words, int window, int32_t *__restrict__ depth,
             uint32_t *__restrict__ bits, unsigned int *status)
@@ -288,13 +286,6 @@ keep_kernel(Pool p, Map m, const int32_t *__restrict__ seqs, const int32_t *__re
         if (sto) *sto = sc;
         __syncwarp();
     }
-}
-
-nq_status tree_of(const nq_tree *t)
-{
-    if (!t || t->batch < 1 || t->nodes < 1 || t->window < 0 || !t->parents || !t->depth || !t->bits) return NQ_ERR_ARG;
-    if (t->nodes > kMaxNodes) return NQ_ERR_SHAPE;
-    return aligned4(t->parents) && aligned4(t->depth) && aligned4(t->bits) ? NQ_OK : NQ_ERR_ALIGN;
 }
 
 }  // namespace

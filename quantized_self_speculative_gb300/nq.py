@@ -147,7 +147,10 @@ def lib():
             L.nq_page_keep.argtypes = [PP, PM, vp, vp, vp, vp, i32, i32, vp]
             L.nq_page_append_at.argtypes = [PP, i32, PM, RP, vp, vp, vp, i32, i64, vp, vp, vp, i32, i32, vp, vp]
             L.nq_rms_norm.argtypes = [vp, i32, i64, vp, i32, i64, vp, i32, f32, i32, i32, vp, i64, vp, vp, vp, vp]
-            for name in ("nq_tree_plan", "spec_accept_tree", "nq_page_keep", "nq_page_append_at", "nq_rms_norm"):
+            L.nq_page_attn_tree_workspace_bytes.argtypes = [i32, i32, i32, i32]
+            L.nq_page_attn_tree_workspace_bytes.restype = sz
+            L.nq_page_attn_tree.argtypes = [PP, i32, PM, vp, i64, i32, vp, vp, i32, AO, TR, vp, vp, sz, vp]
+            for name in ("nq_page_attn_tree", "nq_tree_plan", "spec_accept_tree", "nq_page_keep", "nq_page_append_at", "nq_rms_norm"):
                 getattr(L, name).restype = i32
             for name in ("nq_rope_rates", "nq_rope_mscale", "nq_rope", "nq_page_pool_bytes", "nq_page_map_init", "nq_page_reserve",
                          "nq_page_fork", "nq_page_truncate", "nq_page_compact", "nq_page_copy", "nq_page_append",
@@ -809,7 +812,7 @@ class PagePool:
         self.struct = nq_page_pool(layers, n_pages, page_size, heads_kv, head_dim, group, fmt, 0,
                                    _dev(data, torch.uint8, "data"))
         self.ptr = C.byref(self.struct)
-        self._attn_bytes = {}            # workspace size by (M, heads_q)
+        self._attn_bytes = {}            # workspace size by (M, heads_q), with and without a tree
         self._scratch = _Scratch(data.device)
 
     def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
@@ -898,10 +901,13 @@ class PagePool:
 
     def attention(self, layer: int, pmap: PageMap, q: torch.Tensor, lens: torch.Tensor, planes: int, scale: float,
                   seqs: Optional[torch.Tensor] = None, softcap: float = 0.0, window: int = 0,
-                  slopes: Optional[torch.Tensor] = None, out=None, ws=None, stream=None) -> torch.Tensor:
+                  slopes: Optional[torch.Tensor] = None, out=None, ws=None, stream=None,
+                  tree: Optional[Tree] = None) -> torch.Tensor:
         """Attention of the last M rows of each sequence, q bf16 [batch][M][heads_q]
         [head_dim] (its batch * M rows may be strided, each contiguous); sequence
-        b is slot seqs[b] (slot b without seqs) of lens[b] rows.  softcap, window and slopes (fp32 [heads_q]) as in nq_attn_opts."""
+        b is slot seqs[b] (slot b without seqs) of lens[b] rows.  softcap, window and slopes (fp32 [heads_q]) as in nq_attn_opts.
+        With a tree (of the same window) the M rows are its nodes: each sees the rows
+        before them, the nodes above it and itself (nq_page_attn_tree)."""
         B, M, Hq, D = q.shape
         if D != self.head_dim:
             raise ValueError("q must have the pool's head_dim")
@@ -909,20 +915,27 @@ class PagePool:
             raise ValueError("slopes must be fp32 [heads_q]")
         given = (*self._queries(q), B, M, Hq, None if seqs is None else PageMap._list(seqs, B, "seqs"),
                  PageMap._list(lens, B, "lens"), int(planes))
+        if tree is not None and (tree.batch, tree.nodes) != (B, M):
+            raise ValueError("q must have the tree's batch and nodes")
         on = _stream(stream)
         if out is None:
             out = _empty(q.shape, q.dtype, q.device, stream)
         if B == 0:
             return out
         if ws is None:
-            need = self._attn_bytes.get((M, Hq))
+            need = self._attn_bytes.get((M, Hq, tree is None))
             if need is None:
-                need = self._attn_bytes[M, Hq] = max(lib().nq_page_attn_workspace_bytes(M, Hq, self.heads_kv, D), 16)
+                size = lib().nq_page_attn_workspace_bytes if tree is None else lib().nq_page_attn_tree_workspace_bytes
+                need = self._attn_bytes[M, Hq, tree is None] = max(size(M, Hq, self.heads_kv, D), 16)
             ws = self._scratch.get(need, stream, on)
         else:
             _dev(ws, torch.uint8, "ws")
         o = nq_attn_opts(float(scale), float(softcap), int(window), 0,
                          None if slopes is None else _dev(slopes, torch.float32, "slopes"))
+        if tree is not None:
+            _check(lib().nq_page_attn_tree(self.ptr, layer, pmap.ptr, given[0], given[1], *given[4:], C.byref(o), tree.ref,
+                                           self._rows(out, (B, M, Hq, D), "out"), ws.data_ptr(), ws.numel(), on), "nq_page_attn_tree")
+            return out
         _check(lib().nq_page_attn(self.ptr, layer, pmap.ptr, *given, C.byref(o), self._rows(out, (B, M, Hq, D), "out"),
                                   ws.data_ptr(), ws.numel(), on), "nq_page_attn")
         return out

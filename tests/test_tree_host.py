@@ -75,3 +75,20 @@ def test_append_at(nq):
         a = list(good)
         a[i] = v
         assert L.nq_page_append_at(pool_map(nq)[0], 0, pool_map(nq)[1], *a, None) == st, (i, v)
+
+
+def test_attention(nq):
+    L = nq.lib()
+    opts = lambda **kw: C.byref(nq.nq_attn_opts(*{**dict(scale=0.1, softcap=0.0, window=0, pad=0, slopes=None), **kw}.values()))  # noqa: E731
+    call = lambda t, q=P, stride=256, hq=2, seqs=None, lens=P, planes=2, o=None, out=P, ws=P, n=1 << 40, layer=0: L.nq_page_attn_tree(  # noqa: E731
+        pool_map(nq)[0], layer, pool_map(nq)[1], q, stride, hq, seqs, lens, planes, o or opts(), t, out, ws, n, None)
+    for kw, st in BAD_TREES:
+        assert call(tree(nq, **kw)) == st, kw
+    good = tree(nq)
+    for kw, st in [(dict(q=None), 1), (dict(lens=None), 1), (dict(out=None), 1), (dict(hq=3), 1), (dict(hq=0), 1), (dict(planes=0), 1),
+                   (dict(o=opts(scale=-1.0)), 1), (dict(o=opts(window=3)), 1), (dict(layer=1), 1), (dict(stride=128), 2), (dict(stride=260), 2),
+                   (dict(q=P + 8), 3), (dict(seqs=P + 2), 3), (dict(ws=P + 4), 3)]:
+        assert call(good, **kw) == st, kw
+    assert call(tree(nq, batch=3)) == nq.NQ_ERR_ARG          # more sequences than slots
+    assert call(tree(nq, window=3)) == nq.NQ_ERR_ARG         # another window than the plan's
+    assert L.nq_page_attn_tree_workspace_bytes(1025, 8, 2, 128) == 0 and L.nq_page_attn_tree_workspace_bytes(4, 3, 2, 128) == 0

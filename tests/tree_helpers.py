@@ -80,7 +80,7 @@ def tree_attention64(hp, layer, table, q, lens, planes, scale, parents, softcap=
             at = base + d
             rows = np.array(list(range(max(base, 0))) + [base + j for j in up if base + j >= 0], np.int64)
             pos = np.array(list(range(max(base, 0))) + [base + k for k, j in enumerate(up) if base + j >= 0], np.int64)
-            seen = pos > at - window if window else pos >= 0
+            seen = pos > at - (window or 1 << 40)         # (positions below 0 where a sequence is shorter than its tree)
             rows, pos = rows[seen], pos[seen]
             if len(rows) == 0:
                 continue
