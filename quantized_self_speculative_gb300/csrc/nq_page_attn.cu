@@ -152,9 +152,11 @@ int cols_of(int vectors, bool tc)
     return vectors <= 8 ? 8 : vectors <= 16 ? 16 : vectors <= 32 ? 32 : 64;
 }
 
-int tree_cols(int vectors, int fmt, int ng)
+// Trees: the same rule, but a tile of the tensor cores holds up to 256 vectors, even shares of what there is.
+int tree_cols(int vectors, bool tc)
 {
-    return vectors <= 8 ? 8 : vectors <= 16 ? 16 : vectors <= 32 || (fmt != kBf16 && ng == 1) ? 32 : 64;
+    const int tiles = (vectors + 255) / 256;
+    return tc ? ((vectors + tiles - 1) / tiles + 7) / 8 * 8 : cols_of(vectors, false);
 }
 
 // Workspace: info, then partial states of two segments per CTA; enough for any
@@ -162,9 +164,10 @@ int tree_cols(int vectors, int fmt, int ng)
 struct Ws {
     size_t ml, o, total;
 };
-Ws ws_of(int vectors, int D)
+Ws ws_of(int vectors, int D, bool tree)
 {
-    const size_t ctas = 4 * static_cast<size_t>(sm_count()), cols = 2 * static_cast<size_t>(sm_count()) * (vectors <= 8 ? 32 : vectors <= 16 ? 48 : 128);
+    const size_t ctas = 4 * static_cast<size_t>(sm_count()),
+                 cols = 2 * static_cast<size_t>(sm_count()) * (vectors <= 8 ? 32 : vectors <= 16 ? 48 : tree && vectors > 128 ? 256 : 128);
     Ws w;
     w.ml = ctas * sizeof(int4);
     w.o = w.ml + cols * 8;
@@ -179,7 +182,7 @@ extern "C" size_t nq_page_attn_workspace_bytes(int M, int heads_q, int heads_kv,
 {
     if (M < 1 || heads_kv < 1 || heads_q < heads_kv || heads_q % heads_kv != 0 || !(head_dim == 64 || head_dim == 128)) return 0;
     if (static_cast<long long>(M) * (heads_q / heads_kv) > 65536) return 0;
-    return nq::ws_of(M * (heads_q / heads_kv), head_dim).total;
+    return nq::ws_of(M * (heads_q / heads_kv), head_dim, false).total;
 }
 
 // starve and wait_ns as in AttnArgs
@@ -203,7 +206,7 @@ static nq_status page_attn(const nq_page_pool *pool, int layer, const nq_page_ma
     if (!nq::aligned16(q) || !nq::aligned16(out) || !nq::aligned16(ws) || !nq::aligned4(seqs) || !nq::aligned4(len) ||
         !nq::aligned4(opts->slopes))
         return NQ_ERR_ALIGN;
-    const nq::Ws w = nq::ws_of(M * G, p.D);
+    const nq::Ws w = nq::ws_of(M * G, p.D, tree != nullptr);
     if (!ws || ws_bytes < w.total) return NQ_ERR_WORKSPACE;
     A.status = nq::device_status_ptr();
     if (!A.status) return NQ_ERR_CUDA;
@@ -216,8 +219,8 @@ static nq_status page_attn(const nq_page_pool *pool, int layer, const nq_page_ma
     A.G = G;
     A.g_mul = static_cast<unsigned>((0x100000000ull + G - 1) / G);
     const int fmt = p.NG == 0 ? nq::kBf16 : planes == 1 ? nq::kKv4 : nq::kKv8;
-    const bool tc = !tree && nq::tensor_cores(M * G, fmt, p.NG, p.D);
-    const int cols = A.cols = tree ? nq::tree_cols(M * G, fmt, p.NG) : nq::cols_of(M * G, tc);
+    const bool tc = nq::tensor_cores(M * G, fmt, p.NG, p.D);
+    const int cols = A.cols = tree ? nq::tree_cols(M * G, tc) : nq::cols_of(M * G, tc);
     A.QT = (M * G + cols - 1) / cols;
     // the kernel numbers the steps of all segments in 32 bits
     if (static_cast<double>(batch) * p.H * A.QT * (static_cast<double>(A.m.W) * A.m.P / 16 + 2) > 2.0e9) return NQ_ERR_SHAPE;
@@ -241,7 +244,8 @@ static nq_status page_attn(const nq_page_pool *pool, int layer, const nq_page_ma
     A.part_o = reinterpret_cast<float *>(wb + w.o);
     int grid = 0;
     cudaError_t e;
-    if (tree) e = cols > 16 ? nq::attn_tree_wide(fmt, A, stream, &grid) : nq::attn_tree(fmt, A, stream, &grid);
+    if (tree && tc) e = nq::attn_tree_tc(fmt, A, stream, &grid);
+    else if (tree) e = cols > 16 ? nq::attn_tree_wide(fmt, A, stream, &grid) : nq::attn_tree(fmt, A, stream, &grid);
     else if (tc) e = nq::attn_tc(fmt, A, stream, &grid);
     else if (cols > 16) e = nq::attn_wide(fmt, A, stream, &grid);
     else if (fmt == nq::kBf16) e = nq::launch_d<nq::kBf16, false>(cols / 8, A, stream, &grid);
@@ -262,7 +266,8 @@ extern "C" nq_status nq_page_attn(const nq_page_pool *pool, int layer, const nq_
 
 extern "C" size_t nq_page_attn_tree_workspace_bytes(int nodes, int heads_q, int heads_kv, int head_dim)
 {
-    return nodes > 1024 ? 0 : nq_page_attn_workspace_bytes(nodes, heads_q, heads_kv, head_dim);
+    if (nodes > nq::kMaxNodes || nq_page_attn_workspace_bytes(nodes, heads_q, heads_kv, head_dim) == 0) return 0;
+    return nq::ws_of(nodes * (heads_q / heads_kv), head_dim, true).total;
 }
 
 extern "C" nq_status nq_page_attn_tree(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,

@@ -48,9 +48,10 @@ __device__ __forceinline__ int row_of_vector(const AttnArgs &A, int v) { return 
 // More than 16 query vectors per kv head: tiles of A.cols columns, *grid CTAs.
 cudaError_t attn_wide(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);   // nq_page_attn_wide.cu, 32 or 64
 cudaError_t attn_tc(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);     // nq_page_attn_tc.cu, up to 128
-// Trees: the T forms of the first two.
+// Trees: the T forms of the first two, and a tensor-core kernel of their own.
 cudaError_t attn_tree(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);        // nq_page_attn_tree.cu, 8 or 16
 cudaError_t attn_tree_wide(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);   // nq_page_attn_tree_wide.cu, 32 or 64
+cudaError_t attn_tree_tc(int fmt, const AttnArgs &A, cudaStream_t s, int *grid);     // nq_page_attn_tree_tc.cu, up to 256
 // Bytes of a block of 16 rows: base (or bf16), and refinement where it is read.
 __host__ __device__ constexpr int block_base(int fmt, int D, int NG) { return fmt == kBf16 ? 64 * D : 16 * D + 64 * NG; }
 __host__ __device__ constexpr int block_resid(int fmt, int D) { return fmt == kKv8 ? 16 * D : 0; }

@@ -1,0 +1,565 @@
+// nq_page_attn_tree_tc.cu -- attention of trees over nested pages for many query
+// vectors per kv head, on the 5th-generation tensor cores.
+//
+// A tree of 32 nodes with four query heads per kv head is 128 query vectors, of 64
+// nodes with seven 448: products, softmax and decoding bound the time, not HBM.  As
+// in nq_page_attn_tc.cu a row of the tensor cores is a query vector and a step is 64
+// cache rows, decoded once into signed fp16 codes (exact; K's scales multiply S, V's
+// multiply P).  One warp per scheduler does not fill the softmax's dependent chain
+// (load S, scale, maximum, exp2, store P: some 1700 cycles for 64 keys), so that here
+// two groups of four softmax warps work at once:
+//   KS = false (129 .. 256 vectors): group g has vectors 128 g .. of the tile, both take
+//     every step, which is decoded once for 256 vectors.
+//   KS = true (up to 128 vectors): both have the same vectors, group g takes the steps
+//     g, g + 2, .. with a state of its own; group 0 merges the two at a segment's end
+//     (row r of both accumulators lies in the same lane of tensor memory).
+// Q lies in shared memory.  S is double-buffered per group, and P takes the place of
+// its S.  V needs no transpose: its rows along N are an MN-major operand.
+//
+// Warp roles, handing on through mbarriers (all waits bounded):
+//   0-7   softmax: group w / 4, lane quarter w % 4 of tensor memory; also Q in, O out
+//   8-13  decode: stage -> K, V, scales
+//   14    issues the MMAs: S one (KS: two) steps ahead of P V
+//   15    feeds the ring of raw blocks
+// Runs, partial states and join as in the other kernels; one CTA per SM.
+#include <atomic>
+
+#include "nq_page_attn.cuh"
+#include "nq_tcgen.cuh"
+
+namespace nq {
+namespace {
+
+constexpr int kGroups = 2, kGroupWarps = 4, kSoftWarps = kGroups * kGroupWarps, kDecodeWarps = 6;
+constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp + 1;
+constexpr int kThreads = (kFeedWarp + 1) * 32;              // four warps per scheduler: 128 registers
+constexpr int kMinRun = 2;              // steps per CTA
+constexpr int kKeys = 64;               // cache rows per step
+constexpr int kTmem = 512;              // columns: S (P) of group g, buffer b at 64 (2 g + b), O of group g at 256 + 128 g
+constexpr uint32_t kColO = 256;
+
+template <int FMT, int D, bool KS>
+struct Tt {
+    static constexpr int BASE = block_base(FMT, D, 1), RESID = block_resid(FMT, D);
+    static constexpr int BLKS = kKeys / 16, STAGE = BLKS * (BASE + RESID);
+    static constexpr int Q_BYTES = 128 * D * 2, Q_TILES = KS ? 1 : 2;
+    static constexpr int K_BYTES = kKeys * D * 2, PANEL = kKeys * 128;       // 64 dimensions of 64 rows
+    static constexpr int BUF = 2 * K_BYTES;                                  // K, V of one step
+    static constexpr int SCALES = 3 * kKeys * 4;                             // K's, V's, log2 of V's
+    static constexpr int BUFS = KS ? 4 : 3;                                  // decoded steps
+    static constexpr int AHEAD = KS ? 2 : 1;                                 // S is issued that many steps before P V
+    static constexpr int STAGES = 3;
+    static constexpr int SMEM = Q_TILES * Q_BYTES + BUFS * (BUF + SCALES) + STAGES * STAGE;
+    static_assert(SMEM <= 227 * 1024 - 2048, "shared memory");
+};
+
+// Barriers by number.
+constexpr int kRawFull = 0, kRawEmpty = 4, kKvFull = 8, kKvEmpty = 12, kSFull = 16, kPFull = 20, kPvDone = 24, kQFull = 28, kState = 29, kDrain = 30,
+              kBars = 31;
+
+// Bits of the 32 rows from `row` on that node m of the tree sees, at position `own`; rows in front of a window that
+// ends at `from` are hidden among the committed ones (the nodes' own bits hold the window).
+__device__ __forceinline__ uint32_t seen32(const TreeOf &t, int m, int from, int row)
+{
+    const int j = row - t.base, w = j >> 5;                      // w = -1: the border of the committed rows lies in the word
+    if (j <= -32) return from <= row ? 0xffffffffu : from >= row + 32 ? 0u : 0xffffffffu << (from - row);
+    const uint32_t *b = t.bits + static_cast<size_t>(m) * t.words;
+    const uint32_t lo = w < 0 ? 0xffffffffu : w < t.words ? b[w] : 0u, hi = w + 1 < t.words ? b[w + 1] : 0u;
+    uint32_t x = __funnelshift_r(lo, hi, j & 31);
+    const int cut = min(from, t.base) - row;                     // committed rows before the window
+    if (cut > 0) x &= cut >= 32 ? 0u : 0xffffffffu << cut;
+    return x;
+}
+
+template <int FMT, int D, bool X, bool KS>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
+{
+    using Q = Tt<FMT, D, KS>;
+    constexpr int SR = kKeys, BLKS = Q::BLKS, RB = D / 2;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    __shared__ __align__(8) unsigned long long bars[kBars];
+    __shared__ uint32_t gone_of[Q::STAGES], gone_decoded[Q::BUFS];               // blocks that are not there
+    __shared__ float2 state[KS ? 128 : 1];                                       // of group 1, for group 0
+    __shared__ int abort_flag, keep_tmem;
+    __shared__ uint32_t tmem_slot;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int segs = A.p.H * A.QT;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const uint32_t bar0 = smem_u32(bars);
+    auto bar = [&](int i) { return bar0 + 8u * i; };
+    if (threadIdx.x == 0) {
+        abort_flag = keep_tmem = 0;
+        A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);             // until the CTA has left a part for the join
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(kRawFull + i), 1);
+            mbar_init(bar(kRawEmpty + i), kDecodeWarps);
+            mbar_init(bar(kKvFull + i), kDecodeWarps);
+            mbar_init(bar(kKvEmpty + i), 1);
+            mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kPFull + i), kGroupWarps);
+            mbar_init(bar(kPvDone + i), 1);
+        }
+        mbar_init(bar(kQFull), KS ? kGroupWarps : kSoftWarps);
+        mbar_init(bar(kState), kGroupWarps);
+        mbar_init(bar(kDrain), 32);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    const Run run = find_run<SR, kThreads, D>(A, segs, kMinRun);
+    if (run.f0 >= run.f1) return;
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(kTmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    unsigned char *bufs = sm + Q::Q_TILES * Q::Q_BYTES, *scales = bufs + Q::BUFS * Q::BUF, *ring = scales + Q::BUFS * Q::SCALES;
+    auto wait = [&](int i, int phase) { return mbar_wait_fast(bar(i), static_cast<uint32_t>(phase) & 1u, &abort_flag, A.status, A.wait_ns); };
+    const int steps = run.f1 - run.f0;
+    Walk<SR> use;
+    use.open(A, run.b, run.base, run.f0, run.f1);
+
+    if (warp == kFeedWarp) {
+        // ================================================= raw blocks into the ring
+        Feed<FMT, D, 1, BLKS, 1> feed;
+        feed.start(A, use, segs, run.f0, smem_u32(ring), bar(kRawFull));
+        int i = 0;
+        for (; i < steps && feed.left > 0; ++i) {
+            const int st = i % Q::STAGES;
+            if (!__all_sync(0xffffffffu, wait(kRawEmpty + st, (i / Q::STAGES & 1) ^ 1))) break;
+            feed.issue(A, segs, st, [&](uint32_t out) { gone_of[st] = out; });
+        }
+        // every copy issued has landed before the CTA may exit
+        volatile int never = 0;
+        for (int k = max(0, i - Q::STAGES); k < i; ++k) mbar_wait(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
+    } else if (warp == kMmaWarp) {
+        // ================================================= MMAs
+        const uint32_t idesc_s = f16_idesc(128, kKeys), idesc_o = f16_idesc(128, D) | kMajorMN_B;
+        const uint64_t q_desc = sw128_desc(smem_u32(sm)), kv_desc = sw128_desc(smem_u32(bufs)), v_desc = sw128_desc_mn(smem_u32(bufs) + Q::K_BYTES, Q::PANEL);
+        uint32_t issued_by = 0, leader;
+        int ns[kGroups] = {}, np[kGroups] = {};                  // S and P V products issued by group
+        int i0 = 0, seg_no = 0;                                  // first step of the segment (part), in steps of the run
+        bool ok = true;
+        while (ok && i0 < steps) {
+            const int n = use.end - max(use.base, run.f0);       // its steps
+            int issued = 0;
+            auto scores = [&](int k) {                           // S of its step k
+                const int i = i0 + k;
+                bool w = wait(kKvFull + i % Q::BUFS, i / Q::BUFS & 1);
+                if (k == 0) w = w && wait(kQFull, seg_no & 1);
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    if (KS && (k & 1) != g) continue;
+                    // the buffer's P of two steps ago has been used
+                    w = w && (ns[g] < 2 || wait(kPvDone + 2 * g + (ns[g] & 1), (ns[g] - 2) >> 1));
+                    if (!__all_sync(0xffffffffu, w)) return false;
+                    tc_fence_after();
+                    // 16 dimensions on: 32 bytes, or the next panel of 64 (descriptors count in 16 bytes)
+                    const uint64_t kt = kv_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4)), qt = q_desc + (KS ? 0 : g * (Q::Q_BYTES >> 4));
+                    if (elect_one(leader)) {
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d)
+                            tc_mma_ss(tmem + 64 * (2 * g + (ns[g] & 1)), qt + (d >> 2) * (128 * 128 >> 4) + (d & 3) * 2,
+                                      kt + (d >> 2) * (Q::PANEL >> 4) + (d & 3) * 2, idesc_s, d != 0);
+                        tc_commit(bar(kSFull + 2 * g + (ns[g] & 1)));
+                    }
+                    __syncwarp();
+                    issued_by |= 1u << leader;
+                    ++ns[g];
+                }
+                return true;
+            };
+            for (int k = 0; k < n && ok; ++k) {
+                for (; ok && issued < n && issued <= k + Q::AHEAD; ++issued) ok = scores(issued);
+                if (!ok) break;
+                const int i = i0 + k;
+                const uint64_t vt = v_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4));
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    if (KS && (k & 1) != g) continue;
+                    ok = ok && __all_sync(0xffffffffu, wait(kPFull + 2 * g + (np[g] & 1), np[g] >> 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one(leader)) {
+#pragma unroll
+                        for (int d = 0; d < kKeys / 16; ++d)
+                            tc_mma(tmem + kColO + 128 * g, tmem + 64 * (2 * g + (np[g] & 1)) + 8 * d, vt + d * (2048 >> 4), idesc_o,
+                                   k >= (KS ? kGroups : 1) || d != 0);
+                        tc_commit(bar(kPvDone + 2 * g + (np[g] & 1)));
+                        if (KS || g + 1 == kGroups) tc_commit(bar(kKvEmpty + i % Q::BUFS));
+                    }
+                    __syncwarp();
+                    issued_by |= 1u << leader;
+                    ++np[g];
+                }
+            }
+            i0 += n;
+            ++seg_no;
+            if (i0 < steps) use.next(A, segs);
+        }
+        // every MMA has completed before tensor memory is freed, whatever ended the loop
+        if (issued_by) {
+            if ((issued_by >> lane) & 1u) tc_commit(bar(kDrain));
+            else mbar_arrive(bar(kDrain));
+            __syncwarp();
+            volatile int never = 0;
+            const bool drained = mbar_wait(bar(kDrain), 0, &never, A.status, A.wait_ns);
+            if (!__all_sync(0xffffffffu, drained) && lane == 0) keep_tmem = 1;
+        }
+    } else if (warp >= kSoftWarps) {
+        // ================================================= decode
+        const int dt = threadIdx.x - 32 * kSoftWarps;
+        for (int i = 0; i < steps; ++i) {
+            const int st = i % Q::STAGES, b = i % Q::BUFS;
+            if (!__all_sync(0xffffffffu, wait(kRawFull + st, i / Q::STAGES & 1) && wait(kKvEmpty + b, (i / Q::BUFS & 1) ^ 1))) break;
+            const unsigned char *sp = ring + st * Q::STAGE;
+            unsigned char *buf = bufs + b * Q::BUF;
+            // thread = (K or V, row, 16-byte chunk of nibbles): four words of eight values, in the order 0 4 1 5 2 6 3 7
+            // that the masks give (Q's columns follow it, and O's are put back)
+            constexpr int CH = RB / 16;                          // 4 (D = 128) or 2
+#pragma unroll
+            for (int e = dt; e < 2 * kKeys * CH; e += 32 * kDecodeWarps) {
+                const int v = e / (kKeys * CH), r = e / CH % kKeys, c = e % CH, at = v * 16 * RB + nib_off(RB, r & 15, 16 * c);
+                uint4 x = *reinterpret_cast<const uint4 *>(sp + (r >> 4) * Q::BASE + at), y = make_uint4(0, 0, 0, 0);
+                if constexpr (FMT == kKv8) y = *reinterpret_cast<const uint4 *>(sp + BLKS * Q::BASE + (r >> 4) * Q::RESID + at);
+                // chunks of the upper 64 dimensions in another order: then eight lanes write to eight banks
+                const bool swap = c >= 2;
+                const uint32_t xw[4] = {swap ? x.z : x.x, swap ? x.w : x.y, swap ? x.x : x.z, swap ? x.y : x.w};
+                const uint32_t yw[4] = {swap ? y.z : y.x, swap ? y.w : y.y, swap ? y.x : y.z, swap ? y.y : y.w};
+                unsigned char *to = buf + v * Q::K_BYTES + (c >> 1) * Q::PANEL + r * 128;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const Codes<FMT> k(xw[w], yw[w]);
+                    const int chunk = 4 * (c & 1) + (swap ? w ^ 2 : w);
+                    *reinterpret_cast<uint4 *>(to + ((chunk ^ (r & 7)) << 4)) = make_uint4(k.value(0), k.value(1), k.value(2), k.value(3));
+                }
+            }
+            if (dt < kKeys) {
+                const __half *sc = reinterpret_cast<const __half *>(sp + (dt >> 4) * Q::BASE + 32 * RB);
+                float *f = reinterpret_cast<float *>(scales + b * Q::SCALES);
+                // a scale that is not finite, or negative, counts as 0: rows that no query sees may hold anything
+                float sk = __half2float(sc[dt & 15]), sv = __half2float(sc[16 + (dt & 15)]);
+                sk = sk >= 0.0f && sk <= 65504.0f ? sk : 0.0f;
+                sv = sv >= 0.0f && sv <= 65504.0f ? sv : 0.0f;
+                if (dt == 0) gone_decoded[b] = gone_of[st];
+                f[dt] = sk;
+                f[kKeys + dt] = sv;
+                f[2 * kKeys + dt] = lg2(fmaxf(sv, 3.7252902984619140625e-09f));  // a scale of 0 has codes of 0
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read, and the next copy writes, through the async proxy
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(kKvFull + b));
+                mbar_arrive(bar(kRawEmpty + st));
+            }
+        }
+    } else {
+        // ================================================= softmax: thread = query vector
+        const int g = warp >> 2, r = (warp & 3) * 32 + lane, row = KS ? r : 128 * g + r;      // row of the tensor cores; vector of the tile
+        const uint32_t tq = tmem + (static_cast<uint32_t>(warp & 3) << 21), to = tq + kColO + 128 * g;
+        const float cap2 = A.softcap * kLog2e, inv2 = X && A.softcap > 0.0f ? 1.0f / cap2 : 0.0f;
+        int cnt = 0, i0 = 0, seg_no = 0;                         // the group's steps so far; the segment's first step
+        auto segment = [&]() {                                   // false where a wait gave up
+            const int n = use.end - max(use.base, run.f0);
+            const int kvh = use.seg / A.QT, v0 = (use.seg - kvh * A.QT) * A.cols, nv = min(A.cols, A.M * A.G - v0);
+            const bool active = (row & ~31) < nv, valid = row < nv;
+            const int v = v0 + (valid ? row : nv - 1), m = row_of_vector(A, v), hq = kvh * A.G + v - m * A.G;
+            const TreeOf tree(A, use.b, use.s.hi);
+            const bool used = tree.used(m);
+            const int own = tree.base + tree.depth[m], from = first_seen(A, own);
+            // ---- the segment's query rows into shared memory
+            float cq = 0.0f;
+            if (active) {
+                const uint4 *qr = reinterpret_cast<const uint4 *>(A.q + (static_cast<long long>(use.b) * A.M + m) * A.q_stride + hq * D);
+                float top = 0.0f;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 x = qr[c];
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
+                }
+                // largest magnitude to [2^10, 2^11) by a power of two
+                const int up = min(137 - static_cast<int>(__float_as_uint(top) >> 23), 120);
+                const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                cq = fmaxf(A.scale * kLog2e * (FMT == kKv8 ? 0.0625f : 1.0f) * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1.2e-38f);
+                if (!KS || g == 0) {
+                    unsigned char *qs = sm + (KS ? 0 : g * Q::Q_BYTES) + r * 128;
+#pragma unroll 4
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 x = qr[c];
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        float f[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            f[2 * k] = __uint_as_float(w[k] << 16) * by;
+                            f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * by;
+                        }
+                        *reinterpret_cast<uint4 *>(qs + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(pack_h(f[0], f[4]), pack_h(f[1], f[5]), pack_h(f[2], f[6]), pack_h(f[3], f[7]));
+                    }
+                }
+            }
+            if (!KS || g == 0) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tc_fence_before();            // group 0 has read both accumulators of the segment before
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kQFull));
+            } else if (!__all_sync(0xffffffffu, wait(kQFull, seg_no))) {         // group 0 has taken the state of the segment before
+                return false;
+            }
+            const float slope2 = X && A.slopes ? A.slopes[hq] * kLog2e : 0.0f;
+            const int all_hi = tree.base, all_lo = first_seen(A, use.s.hi - 1);
+            float mref = -INFINITY, mz = 0.0f, lsum = 0.0f;
+#pragma unroll 1
+            for (int k = KS ? g : 0; k < n; k += KS ? kGroups : 1, ++cnt) {
+                const int i = i0 + k, b = cnt & 1, row0 = use.s.lo + (run.f0 + i - use.base) * SR;
+                const bool begins = k < (KS ? kGroups : 1), masked = row0 < all_lo || row0 + SR > all_hi;
+                const uint32_t tS = tq + 64 * (2 * g + b);
+                if (!__all_sync(0xffffffffu, wait(kSFull + 2 * g + b, cnt >> 1))) return false;
+                if (active) {
+                    tc_fence_after();
+                    uint32_t s[64];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc_ld16(tS + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(s + 16 * c));
+                    tc_wait_ld();
+                    const float *f = reinterpret_cast<const float *>(scales + i % Q::BUFS * Q::SCALES);
+                    const uint32_t gone = gone_decoded[i % Q::BUFS];
+                    // scores in base 2 (X), or what cq makes scores of; two keys at a time in packed fp32
+                    const unsigned long long zero2 = f2_pack(0.0f, 0.0f), cq2 = f2_pack(cq, cq);
+#pragma unroll
+                    for (int j = 0; j < 64; j += 4) {
+                        const float4 k4 = *reinterpret_cast<const float4 *>(f + j);
+                        const float2 x[2] = {f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), f2_pack(k4.x, k4.y), zero2)),
+                                       f2_unpack(f2_fma(f2_pack(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), f2_pack(k4.z, k4.w), zero2))};
+                        s[j] = __float_as_uint(X ? x[0].x * cq : x[0].x);
+                        s[j + 1] = __float_as_uint(X ? x[0].y * cq : x[0].y);
+                        s[j + 2] = __float_as_uint(X ? x[1].x * cq : x[1].x);
+                        s[j + 3] = __float_as_uint(X ? x[1].y * cq : x[1].y);
+                    }
+                    uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+                    if (masked || gone) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            vis[h] = masked ? seen32(tree, m, from, row0 + 32 * h) : 0xffffffffu;
+                            if (gone >> (2 * h) & 1u) vis[h] &= 0xffff0000u;
+                            if (gone >> (2 * h + 1) & 1u) vis[h] &= 0x0000ffffu;
+                        }
+                    }
+                    if constexpr (X) {
+                        if (A.softcap > 0.0f) {
+                            if (masked || gone) {
+#pragma unroll
+                                for (int j = 0; j < 64; ++j) s[j] = vis[j >> 5] >> (j & 31) & 1u ? s[j] : 0u;
+                            }
+                            cap_all(reinterpret_cast<float(&)[64]>(s), cap2, inv2);
+                        }
+                        if (A.slopes) {
+                            if (row0 + SR > tree.base) {
+#pragma unroll
+                                for (int j = 0; j < 64; ++j)
+                                    s[j] = __float_as_uint(fmaf(slope2, static_cast<float>(tree.position(row0 + j) - own), __uint_as_float(s[j])));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(fmaf(slope2, static_cast<float>(row0 + j - own), __uint_as_float(s[j])));
+                            }
+                        }
+                    }
+                    if (masked || gone) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) s[j] = vis[j >> 5] >> (j & 31) & 1u ? s[j] : 0xFF800000u;
+                    }
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};    // with the log2 of V's scales
+#pragma unroll
+                    for (int j = 0; j < 64; j += 4) {
+                        const float4 l4 = *reinterpret_cast<const float4 *>(f + 2 * kKeys + j);
+                        const unsigned long long x0 = f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])),
+                                                 x1 = f2_pack(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+                        const float2 y0 = f2_unpack(X ? f2_add(x0, f2_pack(l4.x, l4.y)) : f2_fma(x0, cq2, f2_pack(l4.x, l4.y))),
+                                     y1 = f2_unpack(X ? f2_add(x1, f2_pack(l4.z, l4.w)) : f2_fma(x1, cq2, f2_pack(l4.z, l4.w)));
+                        tops[0] = fmaxf(tops[0], y0.x);
+                        tops[1] = fmaxf(tops[1], y0.y);
+                        tops[2] = fmaxf(tops[2], y1.x);
+                        tops[3] = fmaxf(tops[3], y1.y);
+                    }
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    if (__any_sync(0xffffffffu, top > mref + slack<FMT>())) {
+                        const float mn = top > mref + slack<FMT>() ? top - lead<FMT>() : mref, alpha = ex2(mref == -INFINITY ? -INFINITY : mref - mn);
+                        mref = mn;
+                        mz = mn == -INFINITY ? 0.0f : mn;
+                        lsum *= alpha;
+                        if (!begins) {        // O of the steps before, once their product is complete
+                            if (!__all_sync(0xffffffffu, wait(kPvDone + 2 * g + (b ^ 1), (cnt - 1) >> 1))) return false;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tc_ld16(to + 16 * c, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tc_st16(to + 16 * c, o);
+                            }
+                            tc_wait_st();
+                        }
+                    }
+                    unsigned long long sum0 = f2_pack(lsum, 0.0f), sum1 = zero2;
+                    const unsigned long long less = f2_pack(-mz, -mz);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pr[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 v4 = *reinterpret_cast<const float4 *>(f + kKeys + 32 * c + j);
+                            const int q = 32 * c + j;
+                            const unsigned long long x0 = f2_pack(__uint_as_float(s[q]), __uint_as_float(s[q + 1])),
+                                                     x1 = f2_pack(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3]));
+                            const float2 a0 = f2_unpack(X ? f2_add(x0, less) : f2_fma(x0, cq2, less)),
+                                         a1 = f2_unpack(X ? f2_add(x1, less) : f2_fma(x1, cq2, less));
+                            const unsigned long long e0 = f2_pack(ex2(a0.x), ex2(a0.y)), e1 = f2_pack(ex2(a1.x), ex2(a1.y));
+                            sum0 = f2_add(sum0, e0);
+                            sum1 = f2_add(sum1, e1);
+                            const float2 p0 = f2_unpack(f2_fma(e0, f2_pack(v4.x, v4.y), zero2)), p1 = f2_unpack(f2_fma(e1, f2_pack(v4.z, v4.w), zero2));
+                            pr[j / 2] = pack_h(p0.x, p0.y);
+                            pr[j / 2 + 1] = pack_h(p1.x, p1.y);
+                        }
+                        tc_st16(tS + 16 * c, pr);
+                    }
+                    const float2 sum = f2_unpack(f2_add(sum0, sum1));
+                    lsum = sum.x + sum.y;
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kPFull + 2 * g + b));
+            }
+
+            // ---- the segment's end: the group's last product
+            if (n > (KS ? g : 0) && !__all_sync(0xffffffffu, wait(kPvDone + 2 * g + (cnt - 1 & 1), (cnt - 1) >> 1))) return false;
+            if (KS && g == 1) {
+                state[r] = make_float2(mref, lsum);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kState));
+                return true;
+            }
+            float f0 = 1.0f, f1 = 0.0f;
+            if constexpr (KS) {
+                if (!__all_sync(0xffffffffu, wait(kState, seg_no))) return false;
+                const float2 two = state[r];
+                const float mn = fmaxf(mref, two.x), mm = mn == -INFINITY ? 0.0f : mn;
+                f0 = ex2(mref - mm);
+                f1 = ex2(two.x - mm);
+                mref = mn;
+                lsum = lsum * f0 + (n > 1 ? two.y * f1 : 0.0f);
+            }
+            const bool starts = use.base >= run.f0, ends = use.base + use.s.steps <= run.f1, whole = starts && ends;
+            if (active) {
+                tc_fence_after();
+                if (!used) {                  // its query may have been anything
+                    mref = -INFINITY;
+                    lsum = 0.0f;
+                }
+                const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0)) * A.cols + row;
+                const float fo = (FMT == kKv8 ? 0.0625f : 1.0f) * (!whole ? 1.0f : lsum == 0.0f ? 0.0f : 1.0f / lsum);
+                f0 *= fo;
+                f1 *= fo;
+                __nv_bfloat16 *dst = A.out + ((static_cast<size_t>(use.b) * A.M + m) * A.Hq + hq) * D;
+                float *po = A.part_o + slot * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    float x[16];
+                    tc_ld16(to + 16 * c, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[e]) * f0;
+                    if (KS && n > 1) {        // (of one step group 1 has had none, and its accumulator may hold anything)
+                        tc_ld16(to + 128 + 16 * c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(o[e]), f1, x[e]);
+                    }
+                    if (!used)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+                    if (valid) {
+                        // columns 0 4 1 5 2 6 3 7 of each eight dimensions
+                        if (whole) {
+                            uint4 *d = reinterpret_cast<uint4 *>(dst + 16 * c);
+                            d[0] = make_uint4(pack_b(x[0], x[2]), pack_b(x[4], x[6]), pack_b(x[1], x[3]), pack_b(x[5], x[7]));
+                            d[1] = make_uint4(pack_b(x[8], x[10]), pack_b(x[12], x[14]), pack_b(x[9], x[11]), pack_b(x[13], x[15]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 8) {
+                                *reinterpret_cast<float4 *>(po + 16 * c + e) = make_float4(x[e], x[e + 2], x[e + 4], x[e + 6]);
+                                *reinterpret_cast<float4 *>(po + 16 * c + e + 4) = make_float4(x[e + 1], x[e + 3], x[e + 5], x[e + 7]);
+                            }
+                        }
+                    }
+                }
+                if (!whole && valid) {
+                    A.part_ml[slot * 2] = mref;
+                    A.part_ml[slot * 2 + 1] = lsum;
+                }
+            }
+            if (i0 + n == steps && threadIdx.x == 0 && !ends && starts)
+                A.info[blockIdx.x] = make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / run.per, 0);
+            return true;
+        };
+#pragma unroll 1
+        while (segment()) {
+            i0 += use.end - max(use.base, run.f0);
+            ++seg_no;
+            if (i0 >= steps) break;
+            use.next(A, segs);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp && keep_tmem == 0) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+    }
+}
+
+template <int FMT, int D, bool X, bool KS>
+cudaError_t launch(const AttnArgs &A, cudaStream_t s, int *grid)
+{
+    using Q = Tt<FMT, D, KS>;
+    static std::atomic<bool> done[64];          // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!done[dev].load()) {
+        e = cudaFuncSetAttribute(attn_tree_tc_kernel<FMT, D, X, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Q::SMEM);
+        if (e != cudaSuccess) return e;
+        done[dev].store(true);
+    }
+    *grid = sm_count();
+    attn_tree_tc_kernel<FMT, D, X, KS><<<*grid, kThreads, Q::SMEM, s>>>(A);
+    return cudaGetLastError();
+}
+template <int FMT, int D>
+cudaError_t launch_x(const AttnArgs &A, cudaStream_t s, int *grid)
+{
+    const bool x = A.softcap > 0.0f || A.slopes;
+    if (A.cols <= 128) return x ? launch<FMT, D, true, true>(A, s, grid) : launch<FMT, D, false, true>(A, s, grid);
+    return x ? launch<FMT, D, true, false>(A, s, grid) : launch<FMT, D, false, false>(A, s, grid);
+}
+
+}  // namespace
+
+cudaError_t attn_tree_tc(int fmt, const AttnArgs &A, cudaStream_t s, int *grid)
+{
+    if (fmt == kKv4) return A.p.D == 128 ? launch_x<kKv4, 128>(A, s, grid) : launch_x<kKv4, 64>(A, s, grid);
+    return A.p.D == 128 ? launch_x<kKv8, 128>(A, s, grid) : launch_x<kKv8, 64>(A, s, grid);
+}
+
+}  // namespace nq

@@ -1,5 +1,5 @@
 // nq_tcgen.cuh -- the 5th-generation tensor cores as the kernels here use them:
-// A in tensor memory, B in shared memory (K-major, 128-byte swizzle), fp16
+// A in tensor memory or shared memory, B in shared memory (128-byte swizzle), fp16
 // operands, fp32 accumulators in tensor memory.
 #pragma once
 
@@ -37,6 +37,13 @@ __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint32_t a_tmem, uint64_
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
                  ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
+// The same with A in shared memory
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -66,6 +73,16 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr)
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
            (static_cast<uint64_t>(2) << 61);
 }
+// The same for an operand whose rows (of 64 elements, 128 bytes) run along M or N and
+// follow each other along K: eight rows to a swizzled group, groups 1024 bytes apart
+// (stride byte offset), the next 64 elements `panel` bytes on (leading byte offset).
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t panel)
+{
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(panel >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+constexpr uint32_t kMajorMN_B = 1u << 16;   // of an instruction descriptor: B is laid out that way
 // Instruction descriptor of kind::f16: fp32 accumulators, fp16 A and B, both
 // K-major, N >> 3 at bit 17, M >> 4 at bit 24.
 __host__ __device__ constexpr uint32_t f16_idesc(int m, int n)
