@@ -118,6 +118,90 @@ join_kernel(const __grid_constant__ AttnArgs A)
     reinterpret_cast<uint32_t *>(A.out + row * D)[threadIdx.x] = pack_b(x0 * f, x1 * f);
 }
 
+// The same for trees, whose segments have many vectors: CTA (i, v) takes eight of them.  Of a
+// segment in a few parts a warp takes a vector (a CTA per vector takes 29 us for 128 segments
+// of 128 vectors in two or three parts each); of one in many the warps share each vector's.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+join_tree_kernel(const __grid_constant__ AttnArgs A)
+{
+    constexpr int E = D / 32, U = 4;
+    __shared__ float sm_m[kJoinWarps][kJoinWarps], sm_l[kJoinWarps][kJoinWarps];
+    __shared__ __align__(16) float sm_o[kJoinWarps][kJoinWarps][D];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 in = A.info[blockIdx.x];
+    if (in.x < 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x, n = in.z - first + 1;
+    const int kvh = in.y / A.QT, c0 = blockIdx.y * kJoinWarps, v0 = (in.y % A.QT) * A.cols, nv = min(A.cols, A.M * A.G - v0);
+    struct State {
+        float m, l, o[E];
+    };
+    auto add = [](State &s, float m, float l, const float (&o)[E]) {
+        const float mn = fmaxf(s.m, m), mz = mn == -INFINITY ? 0.0f : mn, a = ex2(s.m - mz), f = ex2(m - mz);
+        s.l = s.l * a + l * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.o[e] = s.o[e] * a + o[e] * f;
+        s.m = mn;
+    };
+    auto parts = [&](int col, int r0, int step) {                // of parts r0, r0 + step, ..
+        State s = {-INFINITY, 0.0f, {}};
+        for (; r0 < n; r0 += U * step) {
+            float mm[U], ll[U], oo[U][E];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * step;
+                mm[u] = -INFINITY;
+                ll[u] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) oo[u][e] = 0.0f;
+                if (r < n) {
+                    const size_t at = (2 * static_cast<size_t>(first + r) + (r == 0 ? 1 : 0)) * A.cols + col;
+                    const float2 ml = *reinterpret_cast<const float2 *>(A.part_ml + at * 2);
+                    mm[u] = ml.x;
+                    ll[u] = ml.y;
+                    const float *p = A.part_o + at * D + lane * E;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) oo[u][e] = p[e];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) add(s, mm[u], ll[u], oo[u]);
+        }
+        return s;
+    };
+    State s;
+    if (n <= 2 * kJoinWarps) {
+        if (c0 + warp >= nv) return;
+        s = parts(c0 + warp, 0, 1);
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < kJoinWarps && c0 + j < nv; ++j) {
+            s = parts(c0 + j, warp, kJoinWarps);
+            if (lane == 0) {
+                sm_m[j][warp] = s.m;
+                sm_l[j][warp] = s.l;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) sm_o[j][warp][lane * E + e] = s.o[e];
+        }
+        __syncthreads();
+        if (c0 + warp >= nv) return;
+        s = {-INFINITY, 0.0f, {}};
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            float o[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = sm_o[warp][w][lane * E + e];
+            add(s, sm_m[warp][w], sm_l[warp][w], o);
+        }
+    }
+    const float f = s.l == 0.0f ? 0.0f : 1.0f / s.l;
+    const int v = v0 + c0 + warp, mv = row_of_vector(A, v);
+    uint32_t *to = reinterpret_cast<uint32_t *>(A.out + ((static_cast<size_t>(in.x) * A.M + mv) * A.Hq + kvh * A.G + v - mv * A.G) * D) + lane * (E / 2);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) to[e / 2] = pack_b(s.o[e] * f, s.o[e + 1] * f);
+}
+
 // ---------------------------------------------------------------- host side
 cudaError_t launch_join(const AttnArgs &A, int grid, cudaStream_t s)
 {
@@ -126,11 +210,14 @@ cudaError_t launch_join(const AttnArgs &A, int grid, cudaStream_t s)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, A.M * A.G < A.cols ? A.M * A.G : A.cols);
+    const int vectors = A.M * A.G < A.cols ? A.M * A.G : A.cols;
+    const bool tree = A.tree_bits != nullptr;
+    cfg.gridDim = dim3(grid, tree ? (vectors + kJoinWarps - 1) / kJoinWarps : vectors);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (tree) return cudaLaunchKernelEx(&cfg, A.p.D == 128 ? join_tree_kernel<128> : join_tree_kernel<64>, A);
     return cudaLaunchKernelEx(&cfg, A.p.D == 128 ? join_kernel<128> : join_kernel<64>, A);
 }
 

@@ -18,9 +18,8 @@
 //
 // Warp roles, handing on through mbarriers (all waits bounded):
 //   0-7   softmax: group w / 4, lane quarter w % 4 of tensor memory; also Q in, O out
-//   8-13  decode: stage -> K, V, scales
-//   14    issues the MMAs: S one (KS: two) steps ahead of P V
-//   15    feeds the ring of raw blocks
+//   8-13  decode: stage -> K, V, scales; the last of them, which has less of it, also feeds the ring of raw blocks
+//   14-15 issue the MMAs of group 0, 1: S one of the group's steps ahead of P V
 // Runs, partial states and join as in the other kernels; one CTA per SM.
 #include <atomic>
 
@@ -31,8 +30,8 @@ namespace nq {
 namespace {
 
 constexpr int kGroups = 2, kGroupWarps = 4, kSoftWarps = kGroups * kGroupWarps, kDecodeWarps = 6;
-constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp + 1;
-constexpr int kThreads = (kFeedWarp + 1) * 32;              // four warps per scheduler: 128 registers
+constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp - 1;
+constexpr int kThreads = (kMmaWarp + kGroups) * 32;            // four warps per scheduler: 128 registers
 constexpr int kMinRun = 2;              // steps per CTA
 constexpr int kKeys = 64;               // cache rows per step
 constexpr int kTmem = 512;              // columns: S (P) of group g, buffer b at 64 (2 g + b), O of group g at 256 + 128 g
@@ -47,7 +46,6 @@ struct Tt {
     static constexpr int BUF = 2 * K_BYTES;                                  // K, V of one step
     static constexpr int SCALES = 3 * kKeys * 4;                             // K's, V's, log2 of V's
     static constexpr int BUFS = KS ? 4 : 3;                                  // decoded steps
-    static constexpr int AHEAD = KS ? 2 : 1;                                 // S is issued that many steps before P V
     static constexpr int STAGES = 3;
     static constexpr int SMEM = Q_TILES * Q_BYTES + BUFS * (BUF + SCALES) + STAGES * STAGE;
     static_assert(SMEM <= 227 * 1024 - 2048, "shared memory");
@@ -55,7 +53,7 @@ struct Tt {
 
 // Barriers by number.
 constexpr int kRawFull = 0, kRawEmpty = 4, kKvFull = 8, kKvEmpty = 12, kSFull = 16, kPFull = 20, kPvDone = 24, kQFull = 28, kState = 29, kDrain = 30,
-              kBars = 31;
+              kBars = 32;
 
 // Bits of the 32 rows from `row` on that node m of the tree sees, at position `own`; rows in front of a window that
 // ends at `from` are hidden among the committed ones (the nodes' own bits hold the window).
@@ -71,6 +69,10 @@ __device__ __forceinline__ uint32_t seen32(const TreeOf &t, int m, int from, int
     return x;
 }
 
+// A value that is the same on all lanes, so that the compiler knows it: what tcgen05.mma takes lies in uniform registers, and
+// an operand that it cannot prove uniform costs some 190 cycles per MMA instead of 34 to 66.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 template <int FMT, int D, bool X, bool KS>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
@@ -81,9 +83,10 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
     __shared__ __align__(8) unsigned long long bars[kBars];
     __shared__ uint32_t gone_of[Q::STAGES], gone_decoded[Q::BUFS];               // blocks that are not there
     __shared__ float2 state[KS ? 128 : 1];                                       // of group 1, for group 0
+    __shared__ float cq_of[Q::Q_TILES * 128];                                    // factor of a query's scores
     __shared__ int abort_flag, keep_tmem;
     __shared__ uint32_t tmem_slot;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int segs = A.p.H * A.QT;
     asm volatile("griddepcontrol.launch_dependents;");
     const uint32_t bar0 = smem_u32(bars);
@@ -95,14 +98,14 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             mbar_init(bar(kRawFull + i), 1);
             mbar_init(bar(kRawEmpty + i), kDecodeWarps);
             mbar_init(bar(kKvFull + i), kDecodeWarps);
-            mbar_init(bar(kKvEmpty + i), 1);
+            mbar_init(bar(kKvEmpty + i), KS ? 1 : kGroups);
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPFull + i), kGroupWarps);
             mbar_init(bar(kPvDone + i), 1);
         }
         mbar_init(bar(kQFull), KS ? kGroupWarps : kSoftWarps);
-        mbar_init(bar(kState), kGroupWarps);
-        mbar_init(bar(kDrain), 32);
+        mbar_init(bar(kState), kGroupWarps + 1);
+        for (int g = 0; g < kGroups; ++g) mbar_init(bar(kDrain + g), 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const Run run = find_run<SR, kThreads, D>(A, segs, kMinRun);
@@ -114,86 +117,68 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = uniform(tmem_slot);
     unsigned char *bufs = sm + Q::Q_TILES * Q::Q_BYTES, *scales = bufs + Q::BUFS * Q::BUF, *ring = scales + Q::BUFS * Q::SCALES;
     auto wait = [&](int i, int phase) { return mbar_wait_fast(bar(i), static_cast<uint32_t>(phase) & 1u, &abort_flag, A.status, A.wait_ns); };
-    const int steps = run.f1 - run.f0;
+    const int steps = uniform(run.f1 - run.f0);
     Walk<SR> use;
     use.open(A, run.b, run.base, run.f0, run.f1);
 
-    if (warp == kFeedWarp) {
-        // ================================================= raw blocks into the ring
-        Feed<FMT, D, 1, BLKS, 1> feed;
-        feed.start(A, use, segs, run.f0, smem_u32(ring), bar(kRawFull));
-        int i = 0;
-        for (; i < steps && feed.left > 0; ++i) {
-            const int st = i % Q::STAGES;
-            if (!__all_sync(0xffffffffu, wait(kRawEmpty + st, (i / Q::STAGES & 1) ^ 1))) break;
-            feed.issue(A, segs, st, [&](uint32_t out) { gone_of[st] = out; });
-        }
-        // every copy issued has landed before the CTA may exit
-        volatile int never = 0;
-        for (int k = max(0, i - Q::STAGES); k < i; ++k) mbar_wait(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
-    } else if (warp == kMmaWarp) {
-        // ================================================= MMAs
-        const uint32_t idesc_s = f16_idesc(128, kKeys), idesc_o = f16_idesc(128, D) | kMajorMN_B;
-        const uint64_t q_desc = sw128_desc(smem_u32(sm)), kv_desc = sw128_desc(smem_u32(bufs)), v_desc = sw128_desc_mn(smem_u32(bufs) + Q::K_BYTES, Q::PANEL);
+    if (warp >= kMmaWarp) {
+        // ================================================= MMAs of group g
+        constexpr int STRIDE = KS ? kGroups : 1;
+        const int g = warp - kMmaWarp;
+        const uint32_t idesc_s = f16_idesc(128, kKeys), idesc_o = f16_idesc(128, D) | kMajorMN_B, ts = tmem + 128 * g, to = tmem + kColO + 128 * g;
+        const uint64_t q_desc = sw128_desc(smem_u32(sm) + (KS ? 0 : g * Q::Q_BYTES)), k_desc = sw128_desc(smem_u32(bufs)),
+                       v_desc = sw128_desc_mn(smem_u32(bufs) + Q::K_BYTES, Q::PANEL);
         uint32_t issued_by = 0, leader;
-        int ns[kGroups] = {}, np[kGroups] = {};                  // S and P V products issued by group
+        int ns = 0, np = 0;                                      // S and P V products issued
         int i0 = 0, seg_no = 0;                                  // first step of the segment (part), in steps of the run
         bool ok = true;
         while (ok && i0 < steps) {
-            const int n = use.end - max(use.base, run.f0);       // its steps
-            int issued = 0;
-            auto scores = [&](int k) {                           // S of its step k
-                const int i = i0 + k;
-                bool w = wait(kKvFull + i % Q::BUFS, i / Q::BUFS & 1);
-                if (k == 0) w = w && wait(kQFull, seg_no & 1);
+            const int n = uniform(use.end - max(use.base, run.f0));   // its steps; the group's: from g on, every second (KS), or all
+            ok = __all_sync(0xffffffffu, wait(kQFull, seg_no));
+            if (KS && g == 1 && lane == 0) mbar_arrive(bar(kState));  // so that no barrier gets two phases ahead of a warp without steps
+            auto scores = [&](int k) {
+                const int i = uniform(i0 + k), b = uniform(ns & 1);
+                // decoded, and the buffer's P of two steps ago has been used
+                if (!__all_sync(0xffffffffu, wait(kKvFull + i % Q::BUFS, i / Q::BUFS) && (ns < 2 || wait(kPvDone + 2 * g + b, (ns - 2) >> 1)))) return false;
+                tc_fence_after();
+                // 16 dimensions on: 32 bytes, or the next panel of 64 (descriptors count in 16 bytes)
+                const uint64_t kt = k_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4));
+                if (elect_one(leader)) {
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    if (KS && (k & 1) != g) continue;
-                    // the buffer's P of two steps ago has been used
-                    w = w && (ns[g] < 2 || wait(kPvDone + 2 * g + (ns[g] & 1), (ns[g] - 2) >> 1));
-                    if (!__all_sync(0xffffffffu, w)) return false;
-                    tc_fence_after();
-                    // 16 dimensions on: 32 bytes, or the next panel of 64 (descriptors count in 16 bytes)
-                    const uint64_t kt = kv_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4)), qt = q_desc + (KS ? 0 : g * (Q::Q_BYTES >> 4));
-                    if (elect_one(leader)) {
-#pragma unroll
-                        for (int d = 0; d < D / 16; ++d)
-                            tc_mma_ss(tmem + 64 * (2 * g + (ns[g] & 1)), qt + (d >> 2) * (128 * 128 >> 4) + (d & 3) * 2,
-                                      kt + (d >> 2) * (Q::PANEL >> 4) + (d & 3) * 2, idesc_s, d != 0);
-                        tc_commit(bar(kSFull + 2 * g + (ns[g] & 1)));
-                    }
-                    __syncwarp();
-                    issued_by |= 1u << leader;
-                    ++ns[g];
+                    for (int d = 0; d < D / 16; ++d)
+                        tc_mma_ss(ts + 64 * b, q_desc + (d >> 2) * (128 * 128 >> 4) + (d & 3) * 2, kt + (d >> 2) * (Q::PANEL >> 4) + (d & 3) * 2, idesc_s, d != 0);
+                    tc_commit(bar(kSFull + 2 * g + b));
                 }
+                __syncwarp();
+                issued_by |= 1u << leader;
+                ++ns;
                 return true;
             };
-            for (int k = 0; k < n && ok; ++k) {
-                for (; ok && issued < n && issued <= k + Q::AHEAD; ++issued) ok = scores(issued);
-                if (!ok) break;
-                const int i = i0 + k;
-                const uint64_t vt = v_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4));
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    if (KS && (k & 1) != g) continue;
-                    ok = ok && __all_sync(0xffffffffu, wait(kPFull + 2 * g + (np[g] & 1), np[g] >> 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one(leader)) {
-#pragma unroll
-                        for (int d = 0; d < kKeys / 16; ++d)
-                            tc_mma(tmem + kColO + 128 * g, tmem + 64 * (2 * g + (np[g] & 1)) + 8 * d, vt + d * (2048 >> 4), idesc_o,
-                                   k >= (KS ? kGroups : 1) || d != 0);
-                        tc_commit(bar(kPvDone + 2 * g + (np[g] & 1)));
-                        if (KS || g + 1 == kGroups) tc_commit(bar(kKvEmpty + i % Q::BUFS));
-                    }
-                    __syncwarp();
-                    issued_by |= 1u << leader;
-                    ++np[g];
+            const int k0 = KS ? g : 0;
+            if (ok && k0 < n) ok = scores(k0);
+            for (int k = k0; ok && k < n; k += STRIDE) {
+                if (k + STRIDE < n && !scores(k + STRIDE)) {
+                    ok = false;
+                    break;
                 }
+                const int i = uniform(i0 + k), b = uniform(np & 1);
+                ok = __all_sync(0xffffffffu, wait(kPFull + 2 * g + b, np >> 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vt = v_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4));
+                const uint32_t more = uniform(k != k0);
+                if (elect_one(leader)) {
+#pragma unroll
+                    for (int d = 0; d < kKeys / 16; ++d) tc_mma(to, ts + 64 * b + 8 * d, vt + d * (2048 >> 4), idesc_o, d != 0 ? 1u : more);
+                    tc_commit(bar(kPvDone + 2 * g + b));
+                    tc_commit(bar(kKvEmpty + i % Q::BUFS));
+                }
+                __syncwarp();
+                issued_by |= 1u << leader;
+                ++np;
             }
             i0 += n;
             ++seg_no;
@@ -201,18 +186,34 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
         }
         // every MMA has completed before tensor memory is freed, whatever ended the loop
         if (issued_by) {
-            if ((issued_by >> lane) & 1u) tc_commit(bar(kDrain));
-            else mbar_arrive(bar(kDrain));
+            if ((issued_by >> lane) & 1u) tc_commit(bar(kDrain + g));
+            else mbar_arrive(bar(kDrain + g));
             __syncwarp();
             volatile int never = 0;
-            const bool drained = mbar_wait(bar(kDrain), 0, &never, A.status, A.wait_ns);
+            const bool drained = mbar_wait(bar(kDrain + g), 0, &never, A.status, A.wait_ns);
             if (!__all_sync(0xffffffffu, drained) && lane == 0) keep_tmem = 1;
         }
     } else if (warp >= kSoftWarps) {
-        // ================================================= decode
+        // ================================================= raw blocks into the ring, and from there decoded
         const int dt = threadIdx.x - 32 * kSoftWarps;
+        Feed<FMT, D, 1, BLKS, 1> feed;
+        feed.left = 0;
+        int fed = 0;
+        auto fill = [&]() {
+            const int st = fed % Q::STAGES;
+            feed.issue(A, segs, st, [&](uint32_t out) { gone_of[st] = out; });
+            ++fed;
+        };
+        if (warp == kFeedWarp) {
+            feed.start(A, use, segs, run.f0, smem_u32(ring), bar(kRawFull));
+            while (fed < Q::STAGES && feed.left > 0) fill();
+        }
         for (int i = 0; i < steps; ++i) {
             const int st = i % Q::STAGES, b = i % Q::BUFS;
+            if (warp == kFeedWarp && i > 0 && feed.left > 0) {   // the stage of the step before, which the other warps have just read as well
+                if (!__all_sync(0xffffffffu, wait(kRawEmpty + (i - 1) % Q::STAGES, (i - 1) / Q::STAGES & 1))) break;
+                fill();
+            }
             if (!__all_sync(0xffffffffu, wait(kRawFull + st, i / Q::STAGES & 1) && wait(kKvEmpty + b, (i / Q::BUFS & 1) ^ 1))) break;
             const unsigned char *sp = ring + st * Q::STAGE;
             unsigned char *buf = bufs + b * Q::BUF;
@@ -255,6 +256,9 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                 mbar_arrive(bar(kRawEmpty + st));
             }
         }
+        // every copy issued has landed before the CTA may exit
+        volatile int never = 0;
+        for (int k = max(0, fed - Q::STAGES); k < fed; ++k) mbar_wait(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
     } else {
         // ================================================= softmax: thread = query vector
         const int g = warp >> 2, r = (warp & 3) * 32 + lane, row = KS ? r : 128 * g + r;      // row of the tensor cores; vector of the tile
@@ -269,38 +273,42 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             const TreeOf tree(A, use.b, use.s.hi);
             const bool used = tree.used(m);
             const int own = tree.base + tree.depth[m], from = first_seen(A, own);
-            // ---- the segment's query rows into shared memory
-            float cq = 0.0f;
-            if (active) {
-                const uint4 *qr = reinterpret_cast<const uint4 *>(A.q + (static_cast<long long>(use.b) * A.M + m) * A.q_stride + hq * D);
-                float top = 0.0f;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 x = qr[c];
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            // ---- the warp's query rows into shared memory: 16-byte chunks, neighbouring lanes in a row
+            if (active && (!KS || g == 0)) {
+                constexpr int CH = D / 8, RPI = 32 / CH, N = 32 / RPI;           // chunks per row, rows per load
+                const int c = lane % CH;
+                uint4 x[N];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
+                for (int k = 0; k < N; ++k) {
+                    const int vk = (row & ~31) + k * RPI + lane / CH, mk = row_of_vector(A, v0 + vk);
+                    x[k] = make_uint4(0, 0, 0, 0);
+                    if (vk < nv)
+                        x[k] = *reinterpret_cast<const uint4 *>(A.q + (static_cast<long long>(use.b) * A.M + mk) * A.q_stride +
+                                                                (kvh * A.G + v0 + vk - mk * A.G) * D + 8 * c);
                 }
-                // largest magnitude to [2^10, 2^11) by a power of two
-                const int up = min(137 - static_cast<int>(__float_as_uint(top) >> 23), 120);
-                const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-                cq = fmaxf(A.scale * kLog2e * (FMT == kKv8 ? 0.0625f : 1.0f) * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1.2e-38f);
-                if (!KS || g == 0) {
-                    unsigned char *qs = sm + (KS ? 0 : g * Q::Q_BYTES) + r * 128;
-#pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 x = qr[c];
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                        float f[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            f[2 * k] = __uint_as_float(w[k] << 16) * by;
-                            f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * by;
-                        }
-                        *reinterpret_cast<uint4 *>(qs + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(pack_h(f[0], f[4]), pack_h(f[1], f[5]), pack_h(f[2], f[6]), pack_h(f[3], f[7]));
+                for (int k = 0; k < N; ++k) {
+                    const int rk = (r & ~31) + k * RPI + lane / CH;
+                    const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                    float f[8], top = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        f[2 * u] = __uint_as_float(w[u] << 16);
+                        f[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u);
+                        top = fmaxf(top, fmaxf(fabsf(f[2 * u]), fabsf(f[2 * u + 1])));
                     }
+#pragma unroll
+                    for (int o = 1; o < CH; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    // largest magnitude to [2^10, 2^11) by a power of two
+                    const int up = min(137 - static_cast<int>(__float_as_uint(top) >> 23), 120);
+                    const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                    if (c == 0)
+                        cq_of[(KS ? 0 : 128 * g) + rk] = fmaxf(A.scale * kLog2e * (FMT == kKv8 ? 0.0625f : 1.0f) *
+                                                               __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1.2e-38f);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) f[u] *= by;
+                    *reinterpret_cast<uint4 *>(sm + (KS ? 0 : g * Q::Q_BYTES) + rk * 128 + (c >> 3) * (128 * 128) + (((c & 7) ^ (rk & 7)) << 4)) =
+                        make_uint4(pack_h(f[0], f[4]), pack_h(f[1], f[5]), pack_h(f[2], f[6]), pack_h(f[3], f[7]));
                 }
             }
             if (!KS || g == 0) {
@@ -311,7 +319,7 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             } else if (!__all_sync(0xffffffffu, wait(kQFull, seg_no))) {         // group 0 has taken the state of the segment before
                 return false;
             }
-            const float slope2 = X && A.slopes ? A.slopes[hq] * kLog2e : 0.0f;
+            const float cq = cq_of[(KS ? 0 : 128 * g) + r], slope2 = X && A.slopes ? A.slopes[hq] * kLog2e : 0.0f;
             const int all_hi = tree.base, all_lo = first_seen(A, use.s.hi - 1);
             float mref = -INFINITY, mz = 0.0f, lsum = 0.0f;
 #pragma unroll 1
@@ -470,33 +478,30 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                 __nv_bfloat16 *dst = A.out + ((static_cast<size_t>(use.b) * A.M + m) * A.Hq + hq) * D;
                 float *po = A.part_o + slot * D;
 #pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t o[16];
-                    float x[16];
-                    tc_ld16(to + 16 * c, o);
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[2][16], o1[2][16];
+                    float x[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tc_ld16(to + c + 16 * h, o[h]);
+                        if (KS && n > 1) tc_ld16(to + 128 + c + 16 * h, o1[h]);
+                    }
                     tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[e]) * f0;
-                    if (KS && n > 1) {        // (of one step group 1 has had none, and its accumulator may hold anything)
-                        tc_ld16(to + 128 + 16 * c, o);
-                        tc_wait_ld();
+                    for (int e = 0; e < 32; ++e) x[e] = used ? __uint_as_float(o[e >> 4][e & 15]) * f0 : 0.0f;
+                    if (KS && n > 1 && used)  // (of one step group 1 has had none, and its accumulator may hold anything)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(o[e]), f1, x[e]);
-                    }
-                    if (!used)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+                        for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o1[e >> 4][e & 15]), f1, x[e]);
                     if (valid) {
                         // columns 0 4 1 5 2 6 3 7 of each eight dimensions
-                        if (whole) {
-                            uint4 *d = reinterpret_cast<uint4 *>(dst + 16 * c);
-                            d[0] = make_uint4(pack_b(x[0], x[2]), pack_b(x[4], x[6]), pack_b(x[1], x[3]), pack_b(x[5], x[7]));
-                            d[1] = make_uint4(pack_b(x[8], x[10]), pack_b(x[12], x[14]), pack_b(x[9], x[11]), pack_b(x[13], x[15]));
-                        } else {
 #pragma unroll
-                            for (int e = 0; e < 16; e += 8) {
-                                *reinterpret_cast<float4 *>(po + 16 * c + e) = make_float4(x[e], x[e + 2], x[e + 4], x[e + 6]);
-                                *reinterpret_cast<float4 *>(po + 16 * c + e + 4) = make_float4(x[e + 1], x[e + 3], x[e + 5], x[e + 7]);
+                        for (int e = 0; e < 32; e += 8) {
+                            if (whole) {
+                                *reinterpret_cast<uint4 *>(dst + c + e) =
+                                    make_uint4(pack_b(x[e], x[e + 2]), pack_b(x[e + 4], x[e + 6]), pack_b(x[e + 1], x[e + 3]), pack_b(x[e + 5], x[e + 7]));
+                            } else {
+                                *reinterpret_cast<float4 *>(po + c + e) = make_float4(x[e], x[e + 2], x[e + 4], x[e + 6]);
+                                *reinterpret_cast<float4 *>(po + c + e + 4) = make_float4(x[e + 1], x[e + 3], x[e + 5], x[e + 7]);
                             }
                         }
                     }
