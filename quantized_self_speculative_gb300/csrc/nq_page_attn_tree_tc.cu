@@ -471,44 +471,71 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                     mref = -INFINITY;
                     lsum = 0.0f;
                 }
-                const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0)) * A.cols + row;
+                const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (starts ? 1 : 0)) * A.cols;
                 const float fo = (FMT == kKv8 ? 0.0625f : 1.0f) * (!whole ? 1.0f : lsum == 0.0f ? 0.0f : 1.0f / lsum);
                 f0 *= fo;
                 f1 *= fo;
-                __nv_bfloat16 *dst = A.out + ((static_cast<size_t>(use.b) * A.M + m) * A.Hq + hq) * D;
-                float *po = A.part_o + slot * D;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[2][16], o1[2][16];
-                    float x[32];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tc_ld16(to + c + 16 * h, o[h]);
-                        if (KS && n > 1) tc_ld16(to + 128 + c + 16 * h, o1[h]);
-                    }
+                if (!whole && valid) *reinterpret_cast<float2 *>(A.part_ml + 2 * (slot + row)) = make_float2(mref, lsum);
+                // a thread has a row, but 32 rows are written 128 bytes at a time: they turn in the warp's share of Q's
+                // place, which no product reads any more
+                unsigned char *turn = sm + (KS ? 0 : g * Q::Q_BYTES) + (r & ~31) * 128;
+                auto columns = [&](int c, float (&x)[16]) {      // of the row, in the order of the dimensions
+                    uint32_t o[16];
+                    tc_ld16(to + c, o);
                     tc_wait_ld();
+                    // columns 0 4 1 5 2 6 3 7 of each eight dimensions
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = used ? __uint_as_float(o[e >> 4][e & 15]) * f0 : 0.0f;
-                    if (KS && n > 1 && used)  // (of one step group 1 has had none, and its accumulator may hold anything)
+                    for (int e = 0; e < 16; ++e) x[(e & 8) + ((e & 7) >> 1) + 4 * (e & 1)] = used ? __uint_as_float(o[e]) * f0 : 0.0f;
+                    if (KS && n > 1) {        // (of one step group 1 has had none, and its accumulator may hold anything)
+                        tc_ld16(to + 128 + c, o);
+                        tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = fmaf(__uint_as_float(o1[e >> 4][e & 15]), f1, x[e]);
-                    if (valid) {
-                        // columns 0 4 1 5 2 6 3 7 of each eight dimensions
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            if (whole) {
-                                *reinterpret_cast<uint4 *>(dst + c + e) =
-                                    make_uint4(pack_b(x[e], x[e + 2]), pack_b(x[e + 4], x[e + 6]), pack_b(x[e + 1], x[e + 3]), pack_b(x[e + 5], x[e + 7]));
-                            } else {
-                                *reinterpret_cast<float4 *>(po + c + e) = make_float4(x[e], x[e + 2], x[e + 4], x[e + 6]);
-                                *reinterpret_cast<float4 *>(po + c + e + 4) = make_float4(x[e + 1], x[e + 3], x[e + 5], x[e + 7]);
-                            }
+                        for (int e = 0; e < 16; ++e) {
+                            const int d = (e & 8) + ((e & 7) >> 1) + 4 * (e & 1);
+                            x[d] = used ? fmaf(__uint_as_float(o[e]), f1, x[d]) : 0.0f;
                         }
                     }
-                }
-                if (!whole && valid) {
-                    A.part_ml[slot * 2] = mref;
-                    A.part_ml[slot * 2 + 1] = lsum;
+                };
+                auto put = [&](int k, uint4 v) { *reinterpret_cast<uint4 *>(turn + lane * 128 + ((k ^ (lane & 7)) << 4)) = v; };
+                auto rows_out = [&](auto address) {              // address(row of the tile, its 16-byte chunk)
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int rr = 4 * k + lane / 8, vk = (row & ~31) + rr;
+                        if (vk < nv) *reinterpret_cast<uint4 *>(address(vk, lane & 7)) = *reinterpret_cast<const uint4 *>(turn + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                    }
+                    __syncwarp();
+                };
+                if (whole) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 64) {
+#pragma unroll 1
+                        for (int h = 0; h < 4; ++h) {
+                            float x[16];
+                            columns(c + 16 * h, x);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                put(2 * h + k, make_uint4(pack_b(x[8 * k], x[8 * k + 1]), pack_b(x[8 * k + 2], x[8 * k + 3]),
+                                                          pack_b(x[8 * k + 4], x[8 * k + 5]), pack_b(x[8 * k + 6], x[8 * k + 7])));
+                        }
+                        rows_out([&](int vk, int k) {
+                            const int mk = row_of_vector(A, v0 + vk);
+                            return A.out + ((static_cast<size_t>(use.b) * A.M + mk) * A.Hq + kvh * A.G + v0 + vk - mk * A.G) * D + c + 8 * k;
+                        });
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            float x[16];
+                            columns(c + 16 * h, x);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                put(4 * h + k, make_uint4(__float_as_uint(x[4 * k]), __float_as_uint(x[4 * k + 1]), __float_as_uint(x[4 * k + 2]), __float_as_uint(x[4 * k + 3])));
+                        }
+                        rows_out([&](int vk, int k) { return A.part_o + (slot + vk) * D + c + 4 * k; });
+                    }
                 }
             }
             if (i0 + n == steps && threadIdx.x == 0 && !ends && starts)
