@@ -18,10 +18,12 @@
 //
 // Warp roles, handing on through mbarriers (all waits bounded):
 //   0-7   softmax: group w / 4, lane quarter w % 4 of tensor memory; also Q in, O out
-//   8-13  decode: stage -> K, V, scales; the last of them, which has less of it, also feeds the ring of raw blocks
-//   14-15 issue the MMAs of group 0, 1: S one of the group's steps ahead of P V
+//   8-13  decode: stage -> K, V, scales
+//   14    issues the MMAs, whichever can go: S up to one of a group's steps ahead of its P V
+//   15    feeds the ring of raw blocks
 // Runs, partial states and join as in the other kernels; one CTA per SM.
 #include <atomic>
+#include <type_traits>
 
 #include "nq_page_attn.cuh"
 #include "nq_tcgen.cuh"
@@ -30,8 +32,8 @@ namespace nq {
 namespace {
 
 constexpr int kGroups = 2, kGroupWarps = 4, kSoftWarps = kGroups * kGroupWarps, kDecodeWarps = 6;
-constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp - 1;
-constexpr int kThreads = (kMmaWarp + kGroups) * 32;            // four warps per scheduler: 128 registers
+constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp + 1;
+constexpr int kThreads = (kFeedWarp + 1) * 32;            // four warps per scheduler: 128 registers
 constexpr int kMinRun = 2;              // steps per CTA
 constexpr int kKeys = 64;               // cache rows per step
 constexpr int kTmem = 512;              // columns: S (P) of group g, buffer b at 64 (2 g + b), O of group g at 256 + 128 g
@@ -53,7 +55,7 @@ struct Tt {
 
 // Barriers by number.
 constexpr int kRawFull = 0, kRawEmpty = 4, kKvFull = 8, kKvEmpty = 12, kSFull = 16, kPFull = 20, kPvDone = 24, kQFull = 28, kState = 29, kDrain = 30,
-              kBars = 32;
+              kBars = 31;
 
 // Bits of the 32 rows from `row` on that node m of the tree sees, at position `own`; rows in front of a window that
 // ends at `from` are hidden among the committed ones (the nodes' own bits hold the window).
@@ -69,6 +71,99 @@ __device__ __forceinline__ uint32_t seen32(const TreeOf &t, int m, int from, int
     return x;
 }
 
+// Where a step's blocks lie in a stage: base block j at j step, its refinement at j
+// rstep + roff.  A page of 16 rows is one run of bytes, its base block and its
+// refinement, and comes by one copy; larger pages bring all base blocks, then all
+// refinements.
+template <int FMT, int D>
+struct Place {
+    int step, roff, rstep;
+    __device__ __forceinline__ explicit Place(const AttnArgs &A)
+    {
+        constexpr int BASE = block_base(FMT, D, 1), RESID = block_resid(FMT, D);
+        const bool one = FMT == kKv8 && A.p.P == 16;
+        step = one ? BASE + RESID : BASE;
+        roff = one ? BASE : kKeys / 16 * BASE;
+        rstep = one ? BASE + RESID : RESID;
+    }
+};
+// The feed of the other kernels costs its warp some 2000 cycles a step of eight copies:
+// each waits for the step's page ids, and takes some 190 where its operands are not
+// provably uniform.  Here lane l holds the page of block l of the 32 blocks from
+// `base` on, and of the 32 after them, and the copies go out from shuffled operands.
+template <int FMT, int D>
+struct Feeder {
+    static constexpr int BLKS = kKeys / 16, BASE = block_base(FMT, D, 1), RESID = block_resid(FMT, D), STAGE = BLKS * (BASE + RESID);
+    Walk<kKeys> w;
+    int row, left, base, id, id_next, lp;     // row of the next step; how many are left in this segment (0: none at all)
+    const int32_t *tab;
+    const uint8_t *rec;
+    uint32_t ring, bar;
+
+    __device__ __forceinline__ int page_of(int from) const
+    {
+        const int r = from + 16 * (threadIdx.x & 31);
+        return r >= from && r < w.s.hi ? tab[r >> lp] : 0;       // (r past 2^31 is below `from`)
+    }
+    __device__ __forceinline__ void aim(const AttnArgs &A, int segs, int f)   // at step f or the first one after it
+    {
+#pragma unroll 1
+        while (f >= w.end) {
+            if (w.end >= w.stop) {
+                left = 0;
+                return;
+            }
+            w.next(A, segs);
+        }
+        row = base = w.s.lo + (f - w.base) * kKeys;
+        left = w.end - f;
+        tab = A.m.table + static_cast<size_t>(w.s.slot) * A.m.W;
+        rec = A.p.data + static_cast<size_t>(w.seg / A.QT) * A.p.rec;
+        id = page_of(base);
+        id_next = base < 0x7ffffe00 - 512 ? page_of(base + 512) : 0;
+    }
+    __device__ __forceinline__ void start(const AttnArgs &A, const Walk<kKeys> &at, int segs, int f, uint32_t ring_, uint32_t bar_)
+    {
+        w = at;
+        ring = ring_;
+        bar = bar_;
+        lp = 31 - __clz(A.m.P);
+        aim(A, segs, f);
+    }
+    // The step into stage st, then on to the next; gone takes the blocks that are not there, of pages outside the pool.
+    __device__ __forceinline__ void issue(const AttnArgs &A, const Place<FMT, D> &at, int segs, int st, uint32_t &gone)
+    {
+        const int k = threadIdx.x & 31, n = min(BLKS, (w.s.hi - row + 15) >> 4), blk = ((row + 16 * k) & (A.m.P - 1)) >> 4;
+        const int mine = __shfl_sync(0xffffffffu, id, ((row - base) >> 4) + (k & (BLKS - 1)));
+        const uint32_t b = bar + 8 * st, dst = ring + st * STAGE;
+        const bool bad = k < n && (mine < 0 || mine >= A.p.N);
+        const uint32_t out = __ballot_sync(0xffffffffu, bad);
+        if (bad) set_status(A.status, NQ_DEV_BAD_PAGE);
+        gone = out;                           // before the barrier's arrival, which lets the decoders read it
+        __syncwarp();
+        if (k == 0) mbar_expect_tx(b, (n - __popc(out)) * (BASE + RESID));
+        __syncwarp();
+#pragma unroll 1
+        for (uint32_t todo = __ballot_sync(0xffffffffu, !bad && k < n && (k == 0 || blk == 0)); todo; todo &= todo - 1) {
+            const int j = __ffs(todo) - 1, jb = __shfl_sync(0xffffffffu, blk, j), x = min(n - j, (1 << (lp - 4)) - jb);   // blocks side by side in the page
+            const uint8_t *src = rec + static_cast<size_t>(__shfl_sync(0xffffffffu, mine, j)) * A.p.H * A.p.rec;
+            if (elect_one()) {
+                bulk_g2s(dst + j * at.step, src + jb * BASE, x * at.step, b);    // (x = 1 where the step holds the refinement too)
+                if (FMT == kKv8 && at.step == BASE) bulk_g2s(dst + at.roff + j * at.rstep, src + A.p.resid_off + jb * RESID, x * RESID, b);
+            }
+            __syncwarp();
+        }
+        row += kKeys;
+        if (--left == 0) {
+            aim(A, segs, w.base + (row - w.s.lo) / kKeys);
+        } else if (row - base == 512) {
+            base = row;
+            id = id_next;
+            id_next = base < 0x7ffffe00 - 512 ? page_of(base + 512) : 0;
+        }
+    }
+};
+
 // A value that is the same on all lanes, so that the compiler knows it: what tcgen05.mma takes lies in uniform registers, and
 // an operand that it cannot prove uniform costs some 190 cycles per MMA instead of 34 to 66.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -78,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
 {
     using Q = Tt<FMT, D, KS>;
-    constexpr int SR = kKeys, BLKS = Q::BLKS, RB = D / 2;
+    constexpr int SR = kKeys, RB = D / 2;
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) unsigned long long bars[kBars];
     __shared__ uint32_t gone_of[Q::STAGES], gone_decoded[Q::BUFS];               // blocks that are not there
@@ -98,14 +193,14 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             mbar_init(bar(kRawFull + i), 1);
             mbar_init(bar(kRawEmpty + i), kDecodeWarps);
             mbar_init(bar(kKvFull + i), kDecodeWarps);
-            mbar_init(bar(kKvEmpty + i), KS ? 1 : kGroups);
+            mbar_init(bar(kKvEmpty + i), 1);
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPFull + i), kGroupWarps);
             mbar_init(bar(kPvDone + i), 1);
         }
         mbar_init(bar(kQFull), KS ? kGroupWarps : kSoftWarps);
-        mbar_init(bar(kState), kGroupWarps + 1);
-        for (int g = 0; g < kGroups; ++g) mbar_init(bar(kDrain + g), 32);
+        mbar_init(bar(kState), kGroupWarps);
+        mbar_init(bar(kDrain), 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const Run run = find_run<SR, kThreads, D>(A, segs, kMinRun);
@@ -124,61 +219,94 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
     Walk<SR> use;
     use.open(A, run.b, run.base, run.f0, run.f1);
 
-    if (warp >= kMmaWarp) {
-        // ================================================= MMAs of group g
+    const Place<FMT, D> place(A);
+    if (warp == kFeedWarp) {
+        // ================================================= raw blocks into the ring
+        Feeder<FMT, D> feed;
+        feed.start(A, use, segs, run.f0, smem_u32(ring), bar(kRawFull));
+        int i = 0;
+        for (; i < steps && feed.left > 0; ++i) {
+            const int st = i % Q::STAGES;
+            if (!__all_sync(0xffffffffu, wait(kRawEmpty + st, (i / Q::STAGES & 1) ^ 1))) break;
+            feed.issue(A, place, segs, st, gone_of[st]);
+        }
+        // every copy issued has landed before the CTA may exit
+        volatile int never = 0;
+        for (int k = max(0, i - Q::STAGES); k < i; ++k) mbar_wait(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
+    } else if (warp == kMmaWarp) {
+        // ================================================= MMAs
         constexpr int STRIDE = KS ? kGroups : 1;
-        const int g = warp - kMmaWarp;
-        const uint32_t idesc_s = f16_idesc(128, kKeys), idesc_o = f16_idesc(128, D) | kMajorMN_B, ts = tmem + 128 * g, to = tmem + kColO + 128 * g;
-        const uint64_t q_desc = sw128_desc(smem_u32(sm) + (KS ? 0 : g * Q::Q_BYTES)), k_desc = sw128_desc(smem_u32(bufs)),
-                       v_desc = sw128_desc_mn(smem_u32(bufs) + Q::K_BYTES, Q::PANEL);
+        const uint32_t idesc_s = f16_idesc(128, kKeys), idesc_o = f16_idesc(128, D) | kMajorMN_B;
+        const uint64_t q_desc = sw128_desc(smem_u32(sm)), k_desc = sw128_desc(smem_u32(bufs)), v_desc = sw128_desc_mn(smem_u32(bufs) + Q::K_BYTES, Q::PANEL);
         uint32_t issued_by = 0, leader;
-        int ns = 0, np = 0;                                      // S and P V products issued
+        int ns[kGroups] = {}, np[kGroups] = {};                  // S and P V products issued
         int i0 = 0, seg_no = 0;                                  // first step of the segment (part), in steps of the run
         bool ok = true;
+        auto test = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_test(bar(i), static_cast<uint32_t>(phase) & 1u)); };
         while (ok && i0 < steps) {
-            const int n = uniform(use.end - max(use.base, run.f0));   // its steps; the group's: from g on, every second (KS), or all
+            const int n = uniform(use.end - max(use.base, run.f0));   // its steps; a group's: from g on, every second (KS), or all
             ok = __all_sync(0xffffffffu, wait(kQFull, seg_no));
-            if (KS && g == 1 && lane == 0) mbar_arrive(bar(kState));  // so that no barrier gets two phases ahead of a warp without steps
-            auto scores = [&](int k) {
-                const int i = uniform(i0 + k), b = uniform(ns & 1);
-                // decoded, and the buffer's P of two steps ago has been used
-                if (!__all_sync(0xffffffffu, wait(kKvFull + i % Q::BUFS, i / Q::BUFS) && (ns < 2 || wait(kPvDone + 2 * g + b, (ns - 2) >> 1)))) return false;
-                tc_fence_after();
-                // 16 dimensions on: 32 bytes, or the next panel of 64 (descriptors count in 16 bytes)
-                const uint64_t kt = k_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4));
-                if (elect_one(leader)) {
+            int ks[kGroups], kp[kGroups];                        // the step of the segment of a group's next S, P V
 #pragma unroll
-                    for (int d = 0; d < D / 16; ++d)
-                        tc_mma_ss(ts + 64 * b, q_desc + (d >> 2) * (128 * 128 >> 4) + (d & 3) * 2, kt + (d >> 2) * (Q::PANEL >> 4) + (d & 3) * 2, idesc_s, d != 0);
-                    tc_commit(bar(kSFull + 2 * g + b));
+            for (int g = 0; g < kGroups; ++g) ks[g] = kp[g] = KS ? g : 0;
+            auto products = [&](auto gc) {                       // whether any could go
+                constexpr int g = decltype(gc)::value;
+                const uint32_t ts = tmem + 128 * g, to = tmem + kColO + 128 * g;
+                bool went = false;
+                if (kp[g] < ks[g] && kp[g] < n && test(kPFull + 2 * g + (np[g] & 1), np[g] >> 1)) {
+                    const int k = uniform(kp[g]), i = i0 + k, b = uniform(np[g] & 1), buf = i % Q::BUFS;
+                    tc_fence_after();
+                    const uint64_t vt = v_desc + static_cast<uint32_t>(buf * (Q::BUF >> 4));
+                    const uint32_t more = uniform(k != (KS ? g : 0));
+                    const bool frees = KS || kp[g ^ 1] > k;      // the other group's P V of the step has gone
+                    if (elect_one(leader)) {
+#pragma unroll
+                        for (int d = 0; d < kKeys / 16; ++d) tc_mma(to, ts + 64 * b + 8 * d, vt + d * (2048 >> 4), idesc_o, d != 0 ? 1u : more);
+                        tc_commit(bar(kPvDone + 2 * g + b));
+                        if (frees) tc_commit(bar(kKvEmpty + buf));
+                    }
+                    __syncwarp();
+                    issued_by |= 1u << leader;
+                    kp[g] += STRIDE;
+                    ++np[g];
+                    went = true;
                 }
-                __syncwarp();
-                issued_by |= 1u << leader;
-                ++ns;
-                return true;
+                // decoded, and the buffer's P of two steps ago used
+                if (ks[g] < n && ks[g] <= kp[g] + STRIDE && test(kKvFull + (i0 + ks[g]) % Q::BUFS, (i0 + ks[g]) / Q::BUFS) &&
+                    (ns[g] < 2 || test(kPvDone + 2 * g + (ns[g] & 1), (ns[g] - 2) >> 1))) {
+                    const int i = uniform(i0 + ks[g]), b = uniform(ns[g] & 1);
+                    tc_fence_after();
+                    // 16 dimensions on: 32 bytes, or the next panel of 64 (descriptors count in 16 bytes)
+                    const uint64_t kt = k_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4)), qt = q_desc + (KS ? 0 : g * (Q::Q_BYTES >> 4));
+                    if (elect_one(leader)) {
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d)
+                            tc_mma_ss(ts + 64 * b, qt + (d >> 2) * (128 * 128 >> 4) + (d & 3) * 2, kt + (d >> 2) * (Q::PANEL >> 4) + (d & 3) * 2, idesc_s, d != 0);
+                        tc_commit(bar(kSFull + 2 * g + b));
+                    }
+                    __syncwarp();
+                    issued_by |= 1u << leader;
+                    ks[g] += STRIDE;
+                    ++ns[g];
+                    went = true;
+                }
+                return went;
             };
-            const int k0 = KS ? g : 0;
-            if (ok && k0 < n) ok = scores(k0);
-            for (int k = k0; ok && k < n; k += STRIDE) {
-                if (k + STRIDE < n && !scores(k + STRIDE)) {
-                    ok = false;
-                    break;
+            unsigned long long since = 0;                        // when waiting began
+            while (ok && (kp[0] < n || kp[1] < n)) {
+                bool went = products(std::integral_constant<int, 0>{});
+                went |= products(std::integral_constant<int, 1>{});
+                if (went) {
+                    since = 0;
+                    continue;
                 }
-                const int i = uniform(i0 + k), b = uniform(np & 1);
-                ok = __all_sync(0xffffffffu, wait(kPFull + 2 * g + b, np >> 1));
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t vt = v_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4));
-                const uint32_t more = uniform(k != k0);
-                if (elect_one(leader)) {
-#pragma unroll
-                    for (int d = 0; d < kKeys / 16; ++d) tc_mma(to, ts + 64 * b + 8 * d, vt + d * (2048 >> 4), idesc_o, d != 0 ? 1u : more);
-                    tc_commit(bar(kPvDone + 2 * g + b));
-                    tc_commit(bar(kKvEmpty + i % Q::BUFS));
+                const unsigned long long now = global_ns();
+                if (since == 0) since = now;
+                ok = __all_sync(0xffffffffu, *const_cast<volatile int *>(&abort_flag) == 0 && now - since <= A.wait_ns);
+                if (!ok && *const_cast<volatile int *>(&abort_flag) == 0) {
+                    abort_flag = 1;
+                    set_status(A.status, NQ_DEV_TIMEOUT);
                 }
-                __syncwarp();
-                issued_by |= 1u << leader;
-                ++np;
             }
             i0 += n;
             ++seg_no;
@@ -186,45 +314,38 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
         }
         // every MMA has completed before tensor memory is freed, whatever ended the loop
         if (issued_by) {
-            if ((issued_by >> lane) & 1u) tc_commit(bar(kDrain + g));
-            else mbar_arrive(bar(kDrain + g));
+            if ((issued_by >> lane) & 1u) tc_commit(bar(kDrain));
+            else mbar_arrive(bar(kDrain));
             __syncwarp();
             volatile int never = 0;
-            const bool drained = mbar_wait(bar(kDrain + g), 0, &never, A.status, A.wait_ns);
+            const bool drained = mbar_wait(bar(kDrain), 0, &never, A.status, A.wait_ns);
             if (!__all_sync(0xffffffffu, drained) && lane == 0) keep_tmem = 1;
         }
     } else if (warp >= kSoftWarps) {
-        // ================================================= raw blocks into the ring, and from there decoded
+        // ================================================= decode
         const int dt = threadIdx.x - 32 * kSoftWarps;
-        Feed<FMT, D, 1, BLKS, 1> feed;
-        feed.left = 0;
-        int fed = 0;
-        auto fill = [&]() {
-            const int st = fed % Q::STAGES;
-            feed.issue(A, segs, st, [&](uint32_t out) { gone_of[st] = out; });
-            ++fed;
-        };
-        if (warp == kFeedWarp) {
-            feed.start(A, use, segs, run.f0, smem_u32(ring), bar(kRawFull));
-            while (fed < Q::STAGES && feed.left > 0) fill();
-        }
         for (int i = 0; i < steps; ++i) {
             const int st = i % Q::STAGES, b = i % Q::BUFS;
-            if (warp == kFeedWarp && i > 0 && feed.left > 0) {   // the stage of the step before, which the other warps have just read as well
-                if (!__all_sync(0xffffffffu, wait(kRawEmpty + (i - 1) % Q::STAGES, (i - 1) / Q::STAGES & 1))) break;
-                fill();
-            }
             if (!__all_sync(0xffffffffu, wait(kRawFull + st, i / Q::STAGES & 1) && wait(kKvEmpty + b, (i / Q::BUFS & 1) ^ 1))) break;
             const unsigned char *sp = ring + st * Q::STAGE;
             unsigned char *buf = bufs + b * Q::BUF;
             // thread = (K or V, row, 16-byte chunk of nibbles): four words of eight values, in the order 0 4 1 5 2 6 3 7
             // that the masks give (Q's columns follow it, and O's are put back)
-            constexpr int CH = RB / 16;                          // 4 (D = 128) or 2
+            constexpr int CH = RB / 16, ALL = 2 * kKeys * CH, N = (ALL + 32 * kDecodeWarps - 1) / (32 * kDecodeWarps);   // CH: 4 (D = 128) or 2
+            uint4 xs[N], ys[N];
 #pragma unroll
-            for (int e = dt; e < 2 * kKeys * CH; e += 32 * kDecodeWarps) {
-                const int v = e / (kKeys * CH), r = e / CH % kKeys, c = e % CH, at = v * 16 * RB + nib_off(RB, r & 15, 16 * c);
-                uint4 x = *reinterpret_cast<const uint4 *>(sp + (r >> 4) * Q::BASE + at), y = make_uint4(0, 0, 0, 0);
-                if constexpr (FMT == kKv8) y = *reinterpret_cast<const uint4 *>(sp + BLKS * Q::BASE + (r >> 4) * Q::RESID + at);
+            for (int k = 0; k < N; ++k) {
+                const int e = dt + k * 32 * kDecodeWarps, v = e / (kKeys * CH), r = e / CH % kKeys, c = e % CH, at = v * 16 * RB + nib_off(RB, r & 15, 16 * c);
+                if (e < ALL) {
+                    xs[k] = *reinterpret_cast<const uint4 *>(sp + (r >> 4) * place.step + at);
+                    if constexpr (FMT == kKv8) ys[k] = *reinterpret_cast<const uint4 *>(sp + place.roff + (r >> 4) * place.rstep + at);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int e = dt + k * 32 * kDecodeWarps, v = e / (kKeys * CH), r = e / CH % kKeys, c = e % CH;
+                if (e >= ALL) break;
+                const uint4 x = xs[k], y = FMT == kKv8 ? ys[k] : make_uint4(0, 0, 0, 0);
                 // chunks of the upper 64 dimensions in another order: then eight lanes write to eight banks
                 const bool swap = c >= 2;
                 const uint32_t xw[4] = {swap ? x.z : x.x, swap ? x.w : x.y, swap ? x.x : x.z, swap ? x.y : x.w};
@@ -232,13 +353,13 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                 unsigned char *to = buf + v * Q::K_BYTES + (c >> 1) * Q::PANEL + r * 128;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const Codes<FMT> k(xw[w], yw[w]);
+                    const Codes<FMT> q(xw[w], yw[w]);
                     const int chunk = 4 * (c & 1) + (swap ? w ^ 2 : w);
-                    *reinterpret_cast<uint4 *>(to + ((chunk ^ (r & 7)) << 4)) = make_uint4(k.value(0), k.value(1), k.value(2), k.value(3));
+                    *reinterpret_cast<uint4 *>(to + ((chunk ^ (r & 7)) << 4)) = make_uint4(q.value(0), q.value(1), q.value(2), q.value(3));
                 }
             }
             if (dt < kKeys) {
-                const __half *sc = reinterpret_cast<const __half *>(sp + (dt >> 4) * Q::BASE + 32 * RB);
+                const __half *sc = reinterpret_cast<const __half *>(sp + (dt >> 4) * place.step + 32 * RB);
                 float *f = reinterpret_cast<float *>(scales + b * Q::SCALES);
                 // a scale that is not finite, or negative, counts as 0: rows that no query sees may hold anything
                 float sk = __half2float(sc[dt & 15]), sv = __half2float(sc[16 + (dt & 15)]);
@@ -256,9 +377,6 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                 mbar_arrive(bar(kRawEmpty + st));
             }
         }
-        // every copy issued has landed before the CTA may exit
-        volatile int never = 0;
-        for (int k = max(0, fed - Q::STAGES); k < fed; ++k) mbar_wait(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
     } else {
         // ================================================= softmax: thread = query vector
         const int g = warp >> 2, r = (warp & 3) * 32 + lane, row = KS ? r : 128 * g + r;      // row of the tensor cores; vector of the tile
