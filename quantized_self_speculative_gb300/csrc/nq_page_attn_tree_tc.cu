@@ -18,12 +18,12 @@
 //
 // Warp roles, handing on through mbarriers (all waits bounded):
 //   0-7   softmax: group w / 4, lane quarter w % 4 of tensor memory; also Q in, O out
-//   8-13  decode: stage -> K, V, scales
-//   14    issues the MMAs, whichever can go: S up to one of a group's steps ahead of its P V
+//   8-12  decode: stage -> K, V, scales
+//   13-14 issue the MMAs of group 0, 1, whichever can go: S up to one of the group's steps ahead of its P V.  (A warp's
+//         issue waits while the tensor pipe works: 460 cycles for S, 260 for P V, and 250 around each.)
 //   15    feeds the ring of raw blocks
 // Runs, partial states and join as in the other kernels; one CTA per SM.
 #include <atomic>
-#include <type_traits>
 
 #include "nq_page_attn.cuh"
 #include "nq_tcgen.cuh"
@@ -31,8 +31,8 @@
 namespace nq {
 namespace {
 
-constexpr int kGroups = 2, kGroupWarps = 4, kSoftWarps = kGroups * kGroupWarps, kDecodeWarps = 6;
-constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp + 1;
+constexpr int kGroups = 2, kGroupWarps = 4, kSoftWarps = kGroups * kGroupWarps, kDecodeWarps = 5;
+constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp + kGroups;
 constexpr int kThreads = (kFeedWarp + 1) * 32;            // four warps per scheduler: 128 registers
 constexpr int kMinRun = 2;              // steps per CTA
 constexpr int kKeys = 64;               // cache rows per step
@@ -55,7 +55,7 @@ struct Tt {
 
 // Barriers by number.
 constexpr int kRawFull = 0, kRawEmpty = 4, kKvFull = 8, kKvEmpty = 12, kSFull = 16, kPFull = 20, kPvDone = 24, kQFull = 28, kState = 29, kDrain = 30,
-              kBars = 31;
+              kBars = 32;
 
 // Bits of the 32 rows from `row` on that node m of the tree sees, at position `own`; rows in front of a window that
 // ends at `from` are hidden among the committed ones (the nodes' own bits hold the window).
@@ -193,14 +193,14 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             mbar_init(bar(kRawFull + i), 1);
             mbar_init(bar(kRawEmpty + i), kDecodeWarps);
             mbar_init(bar(kKvFull + i), kDecodeWarps);
-            mbar_init(bar(kKvEmpty + i), 1);
+            mbar_init(bar(kKvEmpty + i), KS ? 1 : kGroups);
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPFull + i), kGroupWarps);
             mbar_init(bar(kPvDone + i), 1);
         }
         mbar_init(bar(kQFull), KS ? kGroupWarps : kSoftWarps);
-        mbar_init(bar(kState), kGroupWarps);
-        mbar_init(bar(kDrain), 32);
+        mbar_init(bar(kState), kGroupWarps + 1);
+        for (int g = 0; g < kGroups; ++g) mbar_init(bar(kDrain + g), 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     const Run run = find_run<SR, kThreads, D>(A, segs, kMinRun);
@@ -233,69 +233,63 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
         // every copy issued has landed before the CTA may exit
         volatile int never = 0;
         for (int k = max(0, i - Q::STAGES); k < i; ++k) mbar_wait(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
-    } else if (warp == kMmaWarp) {
-        // ================================================= MMAs
+    } else if (warp >= kMmaWarp) {
+        // ================================================= MMAs of group g
         constexpr int STRIDE = KS ? kGroups : 1;
-        const uint32_t idesc_s = f16_idesc(128, kKeys), idesc_o = f16_idesc(128, D) | kMajorMN_B;
-        const uint64_t q_desc = sw128_desc(smem_u32(sm)), k_desc = sw128_desc(smem_u32(bufs)), v_desc = sw128_desc_mn(smem_u32(bufs) + Q::K_BYTES, Q::PANEL);
+        const int g = warp - kMmaWarp;
+        const uint32_t idesc_s = f16_idesc(128, kKeys), idesc_o = f16_idesc(128, D) | kMajorMN_B, ts = tmem + 128 * g, to = tmem + kColO + 128 * g;
+        const uint64_t q_desc = sw128_desc(smem_u32(sm) + (KS ? 0 : g * Q::Q_BYTES)), k_desc = sw128_desc(smem_u32(bufs)),
+                       v_desc = sw128_desc_mn(smem_u32(bufs) + Q::K_BYTES, Q::PANEL);
         uint32_t issued_by = 0, leader;
-        int ns[kGroups] = {}, np[kGroups] = {};                  // S and P V products issued
+        int ns = 0, np = 0;                                      // S and P V products issued
         int i0 = 0, seg_no = 0;                                  // first step of the segment (part), in steps of the run
         bool ok = true;
         auto test = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_test(bar(i), static_cast<uint32_t>(phase) & 1u)); };
         while (ok && i0 < steps) {
-            const int n = uniform(use.end - max(use.base, run.f0));   // its steps; a group's: from g on, every second (KS), or all
+            const int n = uniform(use.end - max(use.base, run.f0));   // its steps; the group's: from g on, every second (KS), or all
             ok = __all_sync(0xffffffffu, wait(kQFull, seg_no));
-            int ks[kGroups], kp[kGroups];                        // the step of the segment of a group's next S, P V
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) ks[g] = kp[g] = KS ? g : 0;
-            auto products = [&](auto gc) {                       // whether any could go
-                constexpr int g = decltype(gc)::value;
-                const uint32_t ts = tmem + 128 * g, to = tmem + kColO + 128 * g;
+            if (KS && g == 1 && lane == 0) mbar_arrive(bar(kState));  // so that no barrier gets two phases ahead of a warp without steps
+            const int k0 = KS ? g : 0;
+            int ks = k0, kp = k0;                                // the step of the segment of the next S, P V
+            unsigned long long since = 0;                        // when waiting began
+            while (ok && kp < n) {
                 bool went = false;
-                if (kp[g] < ks[g] && kp[g] < n && test(kPFull + 2 * g + (np[g] & 1), np[g] >> 1)) {
-                    const int k = uniform(kp[g]), i = i0 + k, b = uniform(np[g] & 1), buf = i % Q::BUFS;
+                if (kp < ks && test(kPFull + 2 * g + (np & 1), np >> 1)) {
+                    const int buf = uniform((i0 + kp) % Q::BUFS), b = uniform(np & 1);
                     tc_fence_after();
                     const uint64_t vt = v_desc + static_cast<uint32_t>(buf * (Q::BUF >> 4));
-                    const uint32_t more = uniform(k != (KS ? g : 0));
-                    const bool frees = KS || kp[g ^ 1] > k;      // the other group's P V of the step has gone
+                    const uint32_t more = uniform(kp != k0);
                     if (elect_one(leader)) {
 #pragma unroll
                         for (int d = 0; d < kKeys / 16; ++d) tc_mma(to, ts + 64 * b + 8 * d, vt + d * (2048 >> 4), idesc_o, d != 0 ? 1u : more);
                         tc_commit(bar(kPvDone + 2 * g + b));
-                        if (frees) tc_commit(bar(kKvEmpty + buf));
+                        tc_commit(bar(kKvEmpty + buf));
                     }
                     __syncwarp();
                     issued_by |= 1u << leader;
-                    kp[g] += STRIDE;
-                    ++np[g];
+                    kp += STRIDE;
+                    ++np;
                     went = true;
                 }
                 // decoded, and the buffer's P of two steps ago used
-                if (ks[g] < n && ks[g] <= kp[g] + STRIDE && test(kKvFull + (i0 + ks[g]) % Q::BUFS, (i0 + ks[g]) / Q::BUFS) &&
-                    (ns[g] < 2 || test(kPvDone + 2 * g + (ns[g] & 1), (ns[g] - 2) >> 1))) {
-                    const int i = uniform(i0 + ks[g]), b = uniform(ns[g] & 1);
+                if (ks < n && ks <= kp + STRIDE && test(kKvFull + (i0 + ks) % Q::BUFS, (i0 + ks) / Q::BUFS) &&
+                    (ns < 2 || test(kPvDone + 2 * g + (ns & 1), (ns - 2) >> 1))) {
+                    const int buf = uniform((i0 + ks) % Q::BUFS), b = uniform(ns & 1);
                     tc_fence_after();
                     // 16 dimensions on: 32 bytes, or the next panel of 64 (descriptors count in 16 bytes)
-                    const uint64_t kt = k_desc + static_cast<uint32_t>(i % Q::BUFS * (Q::BUF >> 4)), qt = q_desc + (KS ? 0 : g * (Q::Q_BYTES >> 4));
+                    const uint64_t kt = k_desc + static_cast<uint32_t>(buf * (Q::BUF >> 4));
                     if (elect_one(leader)) {
 #pragma unroll
                         for (int d = 0; d < D / 16; ++d)
-                            tc_mma_ss(ts + 64 * b, qt + (d >> 2) * (128 * 128 >> 4) + (d & 3) * 2, kt + (d >> 2) * (Q::PANEL >> 4) + (d & 3) * 2, idesc_s, d != 0);
+                            tc_mma_ss(ts + 64 * b, q_desc + (d >> 2) * (128 * 128 >> 4) + (d & 3) * 2, kt + (d >> 2) * (Q::PANEL >> 4) + (d & 3) * 2, idesc_s, d != 0);
                         tc_commit(bar(kSFull + 2 * g + b));
                     }
                     __syncwarp();
                     issued_by |= 1u << leader;
-                    ks[g] += STRIDE;
-                    ++ns[g];
+                    ks += STRIDE;
+                    ++ns;
                     went = true;
                 }
-                return went;
-            };
-            unsigned long long since = 0;                        // when waiting began
-            while (ok && (kp[0] < n || kp[1] < n)) {
-                bool went = products(std::integral_constant<int, 0>{});
-                went |= products(std::integral_constant<int, 1>{});
                 if (went) {
                     since = 0;
                     continue;
@@ -314,11 +308,11 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
         }
         // every MMA has completed before tensor memory is freed, whatever ended the loop
         if (issued_by) {
-            if ((issued_by >> lane) & 1u) tc_commit(bar(kDrain));
-            else mbar_arrive(bar(kDrain));
+            if ((issued_by >> lane) & 1u) tc_commit(bar(kDrain + g));
+            else mbar_arrive(bar(kDrain + g));
             __syncwarp();
             volatile int never = 0;
-            const bool drained = mbar_wait(bar(kDrain), 0, &never, A.status, A.wait_ns);
+            const bool drained = mbar_wait(bar(kDrain + g), 0, &never, A.status, A.wait_ns);
             if (!__all_sync(0xffffffffu, drained) && lane == 0) keep_tmem = 1;
         }
     } else if (warp >= kSoftWarps) {
