@@ -4,8 +4,13 @@
 // A tree of 32 nodes with four query heads per kv head is 128 query vectors, of 64
 // nodes with seven 448: products, softmax and decoding bound the time, not HBM.  As
 // in nq_page_attn_tc.cu a row of the tensor cores is a query vector and a step is 64
-// cache rows, decoded once into signed fp16 codes (exact; K's scales multiply S, V's
-// multiply P).  One warp per scheduler does not fill the softmax's dependent chain
+// cache rows, decoded once: K into signed fp16 codes (exact; its scales multiply S), V
+// into fp16 values relative to a power of two 2^E near the step's largest scale (one
+// rounding, 2^-11; P carries the 2^E).  Where a step's scales span more than 2^12
+// (values would leave fp16's normal numbers) V stays codes, and its scales multiply P.
+// That leaves the softmax one scale per key to read: with V's scale and its log2 as
+// well shared memory is 77% busy and bounds the kernel (150 us against XXX, 448 vectors
+// below).  One warp per scheduler does not fill the softmax's dependent chain
 // (load S, scale, maximum, exp2, store P: some 1700 cycles for 64 keys), so that here
 // two groups of four softmax warps work at once:
 //   KS = false (129 .. 256 vectors): group g has vectors 128 g .. of the tile, both take
@@ -19,8 +24,8 @@
 // Warp roles, handing on through mbarriers (all waits bounded):
 //   0-7   softmax: group w / 4, lane quarter w % 4 of tensor memory; also Q in, O out
 //   8-12  decode: stage -> K, V, scales
-//   13-14 issue the MMAs of group 0, 1, whichever can go: S up to one of the group's steps ahead of its P V.  (A warp's
-//         issue waits while the tensor pipe works: 460 cycles for S, 260 for P V, and 250 around each.)
+//   13-14 issue the MMAs of group 0, 1: S one of the group's steps ahead of its P V.  (A warp's issue waits while the
+//         tensor pipe works: 460 cycles for S, 260 for P V; one warp for both groups is late for every step.)
 //   15    feeds the ring of raw blocks
 // Runs, partial states and join as in the other kernels; one CTA per SM.
 #include <atomic>
@@ -38,6 +43,7 @@ constexpr int kMinRun = 2;              // steps per CTA
 constexpr int kKeys = 64;               // cache rows per step
 constexpr int kTmem = 512;              // columns: S (P) of group g, buffer b at 64 (2 g + b), O of group g at 256 + 128 g
 constexpr uint32_t kColO = 256;
+constexpr int kCodes = 1000, kSpan = 12;
 
 template <int FMT, int D, bool KS>
 struct Tt {
@@ -177,6 +183,7 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) unsigned long long bars[kBars];
     __shared__ uint32_t gone_of[Q::STAGES], gone_decoded[Q::BUFS];               // blocks that are not there
+    __shared__ int scaled_by[Q::BUFS];                                           // E of V's values; kCodes: they are codes
     __shared__ float2 state[KS ? 128 : 1];                                       // of group 1, for group 0
     __shared__ float cq_of[Q::Q_TILES * 128];                                    // factor of a query's scores
     __shared__ int abort_flag, keep_tmem;
@@ -244,63 +251,47 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
         int ns = 0, np = 0;                                      // S and P V products issued
         int i0 = 0, seg_no = 0;                                  // first step of the segment (part), in steps of the run
         bool ok = true;
-        auto test = [&](int i, int phase) { return __all_sync(0xffffffffu, mbar_test(bar(i), static_cast<uint32_t>(phase) & 1u)); };
         while (ok && i0 < steps) {
             const int n = uniform(use.end - max(use.base, run.f0));   // its steps; the group's: from g on, every second (KS), or all
             ok = __all_sync(0xffffffffu, wait(kQFull, seg_no));
             if (KS && g == 1 && lane == 0) mbar_arrive(bar(kState));  // so that no barrier gets two phases ahead of a warp without steps
             const int k0 = KS ? g : 0;
-            int ks = k0, kp = k0;                                // the step of the segment of the next S, P V
-            unsigned long long since = 0;                        // when waiting began
-            while (ok && kp < n) {
-                bool went = false;
-                if (kp < ks && test(kPFull + 2 * g + (np & 1), np >> 1)) {
-                    const int buf = uniform((i0 + kp) % Q::BUFS), b = uniform(np & 1);
-                    tc_fence_after();
-                    const uint64_t vt = v_desc + static_cast<uint32_t>(buf * (Q::BUF >> 4));
-                    const uint32_t more = uniform(kp != k0);
-                    if (elect_one(leader)) {
-#pragma unroll
-                        for (int d = 0; d < kKeys / 16; ++d) tc_mma(to, ts + 64 * b + 8 * d, vt + d * (2048 >> 4), idesc_o, d != 0 ? 1u : more);
-                        tc_commit(bar(kPvDone + 2 * g + b));
-                        tc_commit(bar(kKvEmpty + buf));
-                    }
-                    __syncwarp();
-                    issued_by |= 1u << leader;
-                    kp += STRIDE;
-                    ++np;
-                    went = true;
-                }
+            auto scores = [&](int k) {
+                const int buf = uniform((i0 + k) % Q::BUFS), b = uniform(ns & 1);
                 // decoded, and the buffer's P of two steps ago used
-                if (ks < n && ks <= kp + STRIDE && test(kKvFull + (i0 + ks) % Q::BUFS, (i0 + ks) / Q::BUFS) &&
-                    (ns < 2 || test(kPvDone + 2 * g + (ns & 1), (ns - 2) >> 1))) {
-                    const int buf = uniform((i0 + ks) % Q::BUFS), b = uniform(ns & 1);
-                    tc_fence_after();
-                    // 16 dimensions on: 32 bytes, or the next panel of 64 (descriptors count in 16 bytes)
-                    const uint64_t kt = k_desc + static_cast<uint32_t>(buf * (Q::BUF >> 4));
-                    if (elect_one(leader)) {
+                if (!__all_sync(0xffffffffu, wait(kKvFull + buf, (i0 + k) / Q::BUFS) && (ns < 2 || wait(kPvDone + 2 * g + b, (ns - 2) >> 1)))) return false;
+                tc_fence_after();
+                // 16 dimensions on: 32 bytes, or the next panel of 64 (descriptors count in 16 bytes)
+                const uint64_t kt = k_desc + static_cast<uint32_t>(buf * (Q::BUF >> 4));
+                if (elect_one(leader)) {
 #pragma unroll
-                        for (int d = 0; d < D / 16; ++d)
-                            tc_mma_ss(ts + 64 * b, q_desc + (d >> 2) * (128 * 128 >> 4) + (d & 3) * 2, kt + (d >> 2) * (Q::PANEL >> 4) + (d & 3) * 2, idesc_s, d != 0);
-                        tc_commit(bar(kSFull + 2 * g + b));
-                    }
-                    __syncwarp();
-                    issued_by |= 1u << leader;
-                    ks += STRIDE;
-                    ++ns;
-                    went = true;
+                    for (int d = 0; d < D / 16; ++d)
+                        tc_mma_ss(ts + 64 * b, q_desc + (d >> 2) * (128 * 128 >> 4) + (d & 3) * 2, kt + (d >> 2) * (Q::PANEL >> 4) + (d & 3) * 2, idesc_s, d != 0);
+                    tc_commit(bar(kSFull + 2 * g + b));
                 }
-                if (went) {
-                    since = 0;
-                    continue;
+                __syncwarp();
+                issued_by |= 1u << leader;
+                ++ns;
+                return true;
+            };
+            if (ok && k0 < n) ok = scores(k0);
+            for (int k = k0; ok && k < n; k += STRIDE) {
+                if (k + STRIDE < n) ok = scores(k + STRIDE);
+                const int buf = uniform((i0 + k) % Q::BUFS), b = uniform(np & 1);
+                ok = ok && __all_sync(0xffffffffu, wait(kPFull + 2 * g + b, np >> 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vt = v_desc + static_cast<uint32_t>(buf * (Q::BUF >> 4));
+                const uint32_t more = uniform(k != k0);
+                if (elect_one(leader)) {
+#pragma unroll
+                    for (int d = 0; d < kKeys / 16; ++d) tc_mma(to, ts + 64 * b + 8 * d, vt + d * (2048 >> 4), idesc_o, d != 0 ? 1u : more);
+                    tc_commit(bar(kPvDone + 2 * g + b));
+                    tc_commit(bar(kKvEmpty + buf));
                 }
-                const unsigned long long now = global_ns();
-                if (since == 0) since = now;
-                ok = __all_sync(0xffffffffu, *const_cast<volatile int *>(&abort_flag) == 0 && now - since <= A.wait_ns);
-                if (!ok && *const_cast<volatile int *>(&abort_flag) == 0) {
-                    abort_flag = 1;
-                    set_status(A.status, NQ_DEV_TIMEOUT);
-                }
+                __syncwarp();
+                issued_by |= 1u << leader;
+                ++np;
             }
             i0 += n;
             ++seg_no;
@@ -335,6 +326,17 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                     if constexpr (FMT == kKv8) ys[k] = *reinterpret_cast<const uint4 *>(sp + place.roff + (r >> 4) * place.rstep + at);
                 }
             }
+            // a scale that is not finite, or negative, counts as 0: rows that no query sees may hold anything
+            auto scale_of = [&](int r, int v) -> uint32_t {
+                const uint32_t x = reinterpret_cast<const uint16_t *>(sp + (r >> 4) * place.step + 32 * RB)[16 * v + (r & 15)];
+                return x < 0x7C00u ? x : 0u;
+            };
+            auto number = [](uint32_t x) { return __half2float(__ushort_as_half(static_cast<unsigned short>(x))); };
+            const uint32_t s0 = scale_of(lane, 1), s1 = scale_of(lane + 32, 1);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max(s0, s1)), low = __reduce_min_sync(0xffffffffu, min(s0 ? s0 : 0xFFFFu, s1 ? s1 : 0xFFFFu));
+            auto exponent = [&](uint32_t x) { return static_cast<int>(__float_as_uint(number(x)) >> 23) - 127; };
+            const int E = top == 0 ? 0 : exponent(top) - exponent(low) > kSpan ? kCodes : exponent(top);
+            const float by = __uint_as_float(static_cast<uint32_t>(127 - (E == kCodes ? 0 : E)) << 23);
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 const int e = dt + k * 32 * kDecodeWarps, v = e / (kKeys * CH), r = e / CH % kKeys, c = e % CH;
@@ -345,24 +347,30 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                 const uint32_t xw[4] = {swap ? x.z : x.x, swap ? x.w : x.y, swap ? x.x : x.z, swap ? x.y : x.w};
                 const uint32_t yw[4] = {swap ? y.z : y.x, swap ? y.w : y.y, swap ? y.x : y.z, swap ? y.y : y.w};
                 unsigned char *to = buf + v * Q::K_BYTES + (c >> 1) * Q::PANEL + r * 128;
+                const float one = v == 0 || E == kCodes ? 1.0f : number(scale_of(r, 1)) * by;    // exact in fp16
+                const uint32_t f2 = pack_h(one, one);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const Codes<FMT> q(xw[w], yw[w]);
                     const int chunk = 4 * (c & 1) + (swap ? w ^ 2 : w);
-                    *reinterpret_cast<uint4 *>(to + ((chunk ^ (r & 7)) << 4)) = make_uint4(q.value(0), q.value(1), q.value(2), q.value(3));
+                    uint32_t d[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d[u]) : "r"(q.value(u)), "r"(f2));
+                    *reinterpret_cast<uint4 *>(to + ((chunk ^ (r & 7)) << 4)) = make_uint4(d[0], d[1], d[2], d[3]);
                 }
             }
             if (dt < kKeys) {
-                const __half *sc = reinterpret_cast<const __half *>(sp + (dt >> 4) * place.step + 32 * RB);
                 float *f = reinterpret_cast<float *>(scales + b * Q::SCALES);
-                // a scale that is not finite, or negative, counts as 0: rows that no query sees may hold anything
-                float sk = __half2float(sc[dt & 15]), sv = __half2float(sc[16 + (dt & 15)]);
-                sk = sk >= 0.0f && sk <= 65504.0f ? sk : 0.0f;
-                sv = sv >= 0.0f && sv <= 65504.0f ? sv : 0.0f;
-                if (dt == 0) gone_decoded[b] = gone_of[st];
-                f[dt] = sk;
-                f[kKeys + dt] = sv;
-                f[2 * kKeys + dt] = lg2(fmaxf(sv, 3.7252902984619140625e-09f));  // a scale of 0 has codes of 0
+                if (dt == 0) {
+                    gone_decoded[b] = gone_of[st];
+                    scaled_by[b] = E;
+                }
+                f[dt] = number(scale_of(dt, 0));
+                if (E == kCodes) {
+                    const float sv = number(scale_of(dt, 1));
+                    f[kKeys + dt] = sv;
+                    f[2 * kKeys + dt] = lg2(fmaxf(sv, 3.7252902984619140625e-09f));              // a scale of 0 has codes of 0
+                }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read, and the next copy writes, through the async proxy
             __syncwarp();
@@ -448,6 +456,7 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                     tc_wait_ld();
                     const float *f = reinterpret_cast<const float *>(scales + i % Q::BUFS * Q::SCALES);
                     const uint32_t gone = gone_decoded[i % Q::BUFS];
+                    const int E = scaled_by[i % Q::BUFS];
                     // scores in base 2 (X), or what cq makes scores of; two keys at a time in packed fp32
                     const unsigned long long zero2 = f2_pack(0.0f, 0.0f), cq2 = f2_pack(cq, cq);
 #pragma unroll
@@ -492,20 +501,27 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
                         for (int j = 0; j < 64; ++j) s[j] = vis[j >> 5] >> (j & 31) & 1u ? s[j] : 0xFF800000u;
                     }
-                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};    // with the log2 of V's scales
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, top;
+                    if (E != kCodes) {        // the largest score, and V's power of two
 #pragma unroll
-                    for (int j = 0; j < 64; j += 4) {
-                        const float4 l4 = *reinterpret_cast<const float4 *>(f + 2 * kKeys + j);
-                        const unsigned long long x0 = f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])),
-                                                 x1 = f2_pack(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
-                        const float2 y0 = f2_unpack(X ? f2_add(x0, f2_pack(l4.x, l4.y)) : f2_fma(x0, cq2, f2_pack(l4.x, l4.y))),
-                                     y1 = f2_unpack(X ? f2_add(x1, f2_pack(l4.z, l4.w)) : f2_fma(x1, cq2, f2_pack(l4.z, l4.w)));
-                        tops[0] = fmaxf(tops[0], y0.x);
-                        tops[1] = fmaxf(tops[1], y0.y);
-                        tops[2] = fmaxf(tops[2], y1.x);
-                        tops[3] = fmaxf(tops[3], y1.y);
+                        for (int j = 0; j < 64; ++j) tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(s[j]));
+                        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                        top = X ? top + static_cast<float>(E) : fmaf(top, cq, static_cast<float>(E));
+                    } else {                  // scores with the log2 of V's scales
+#pragma unroll
+                        for (int j = 0; j < 64; j += 4) {
+                            const float4 l4 = *reinterpret_cast<const float4 *>(f + 2 * kKeys + j);
+                            const unsigned long long x0 = f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])),
+                                                     x1 = f2_pack(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+                            const float2 y0 = f2_unpack(X ? f2_add(x0, f2_pack(l4.x, l4.y)) : f2_fma(x0, cq2, f2_pack(l4.x, l4.y))),
+                                         y1 = f2_unpack(X ? f2_add(x1, f2_pack(l4.z, l4.w)) : f2_fma(x1, cq2, f2_pack(l4.z, l4.w)));
+                            tops[0] = fmaxf(tops[0], y0.x);
+                            tops[1] = fmaxf(tops[1], y0.y);
+                            tops[2] = fmaxf(tops[2], y1.x);
+                            tops[3] = fmaxf(tops[3], y1.y);
+                        }
+                        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     }
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     if (__any_sync(0xffffffffu, top > mref + slack<FMT>())) {
                         const float mn = top > mref + slack<FMT>() ? top - lead<FMT>() : mref, alpha = ex2(mref == -INFINITY ? -INFINITY : mref - mn);
                         mref = mn;
@@ -526,30 +542,47 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                             tc_wait_st();
                         }
                     }
-                    unsigned long long sum0 = f2_pack(lsum, 0.0f), sum1 = zero2;
-                    const unsigned long long less = f2_pack(-mz, -mz);
+                    unsigned long long sum0 = zero2, sum1 = zero2;
+                    const float less1 = E == kCodes ? -mz : static_cast<float>(E) - mz;
+                    const unsigned long long less = f2_pack(less1, less1);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t pr[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 v4 = *reinterpret_cast<const float4 *>(f + kKeys + 32 * c + j);
-                            const int q = 32 * c + j;
+                        auto exps = [&](int q, unsigned long long &e0, unsigned long long &e1) {
                             const unsigned long long x0 = f2_pack(__uint_as_float(s[q]), __uint_as_float(s[q + 1])),
                                                      x1 = f2_pack(__uint_as_float(s[q + 2]), __uint_as_float(s[q + 3]));
                             const float2 a0 = f2_unpack(X ? f2_add(x0, less) : f2_fma(x0, cq2, less)),
                                          a1 = f2_unpack(X ? f2_add(x1, less) : f2_fma(x1, cq2, less));
-                            const unsigned long long e0 = f2_pack(ex2(a0.x), ex2(a0.y)), e1 = f2_pack(ex2(a1.x), ex2(a1.y));
+                            e0 = f2_pack(ex2(a0.x), ex2(a0.y));
+                            e1 = f2_pack(ex2(a1.x), ex2(a1.y));
                             sum0 = f2_add(sum0, e0);
                             sum1 = f2_add(sum1, e1);
-                            const float2 p0 = f2_unpack(f2_fma(e0, f2_pack(v4.x, v4.y), zero2)), p1 = f2_unpack(f2_fma(e1, f2_pack(v4.z, v4.w), zero2));
-                            pr[j / 2] = pack_h(p0.x, p0.y);
-                            pr[j / 2 + 1] = pack_h(p1.x, p1.y);
+                        };
+                        if (E != kCodes) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                unsigned long long e0, e1;
+                                exps(32 * c + j, e0, e1);
+                                const float2 p0 = f2_unpack(e0), p1 = f2_unpack(e1);
+                                pr[j / 2] = pack_h(p0.x, p0.y);
+                                pr[j / 2 + 1] = pack_h(p1.x, p1.y);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 v4 = *reinterpret_cast<const float4 *>(f + kKeys + 32 * c + j);
+                                unsigned long long e0, e1;
+                                exps(32 * c + j, e0, e1);
+                                const float2 p0 = f2_unpack(f2_fma(e0, f2_pack(v4.x, v4.y), zero2)), p1 = f2_unpack(f2_fma(e1, f2_pack(v4.z, v4.w), zero2));
+                                pr[j / 2] = pack_h(p0.x, p0.y);
+                                pr[j / 2 + 1] = pack_h(p1.x, p1.y);
+                            }
                         }
                         tc_st16(tS + 16 * c, pr);
                     }
+                    // of the weights without V's power of two
                     const float2 sum = f2_unpack(f2_add(sum0, sum1));
-                    lsum = sum.x + sum.y;
+                    lsum = fmaf(sum.x + sum.y, __uint_as_float(static_cast<uint32_t>(127 - (E == kCodes ? 0 : E)) << 23), lsum);
                     tc_wait_st();
                 }
                 tc_fence_before();
