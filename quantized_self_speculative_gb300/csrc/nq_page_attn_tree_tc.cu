@@ -23,10 +23,10 @@
 //
 // Warp roles, handing on through mbarriers (all waits bounded):
 //   0-7   softmax: group w / 4, lane quarter w % 4 of tensor memory; also Q in, O out
-//   8-12  decode: stage -> K, V, scales
-//   13-14 issue the MMAs of group 0, 1: S one of the group's steps ahead of its P V.  (A warp's issue waits while the
+//   8-15  decode: stage -> K, V, scales
+//   16-17 issue the MMAs of group 0, 1: S one of the group's steps ahead of its P V.  (A warp's issue waits while the
 //         tensor pipe works: 460 cycles for S, 260 for P V; one warp for both groups is late for every step.)
-//   15    feeds the ring of raw blocks
+//   18-19 feed the ring of raw blocks, every second step each
 // Runs, partial states and join as in the other kernels; one CTA per SM.
 #include <atomic>
 
@@ -36,9 +36,13 @@
 namespace nq {
 namespace {
 
-constexpr int kGroups = 2, kGroupWarps = 4, kSoftWarps = kGroups * kGroupWarps, kDecodeWarps = 5;
-constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp + kGroups;
-constexpr int kThreads = (kFeedWarp + 1) * 32;            // four warps per scheduler: 128 registers
+constexpr int kGroups = 2, kGroupWarps = 4, kSoftWarps = kGroups * kGroupWarps, kDecodeWarps = 8;
+constexpr int kMmaWarp = kSoftWarps + kDecodeWarps, kFeedWarp = kMmaWarp + kGroups, kFeedWarps = 2;
+constexpr int kThreads = 20 * 32;       // five warps per scheduler, whole warpgroups
+static_assert(kThreads == 32 * (kFeedWarp + kFeedWarps), "roles");
+// Registers per thread: launched with 96 each, from which the warpgroups' shares are drawn.
+constexpr int kRegsLaunch = 96, kRegsSoft = 128, kRegsDecode = 72, kRegsRest = 80;
+static_assert(2 * kRegsSoft + 2 * kRegsDecode + kRegsRest == 5 * kRegsLaunch, "setmaxnreg draws on the launch's registers");
 constexpr int kMinRun = 2;              // steps per CTA
 constexpr int kKeys = 64;               // cache rows per step
 constexpr int kTmem = 512;              // columns: S (P) of group g, buffer b at 64 (2 g + b), O of group g at 256 + 128 g
@@ -122,7 +126,7 @@ struct Feeder {
             w.next(A, segs);
         }
         row = base = w.s.lo + (f - w.base) * kKeys;
-        left = w.end - f;
+        left = (w.end - f + kFeedWarps - 1) / kFeedWarps;
         tab = A.m.table + static_cast<size_t>(w.s.slot) * A.m.W;
         rec = A.p.data + static_cast<size_t>(w.seg / A.QT) * A.p.rec;
         id = page_of(base);
@@ -159,17 +163,39 @@ struct Feeder {
             }
             __syncwarp();
         }
-        row += kKeys;
+        row += kFeedWarps * kKeys;
         if (--left == 0) {
             aim(A, segs, w.base + (row - w.s.lo) / kKeys);
-        } else if (row - base == 512) {
-            base = row;
+        } else if (row - base >= 512) {
+            base += 512;
             id = id_next;
             id_next = base < 0x7ffffe00 - 512 ? page_of(base + 512) : 0;
         }
     }
 };
 
+// mbar_wait_fast without its call: with one in it ptxas does not allocate a warpgroup's own share of registers.
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned int *status, unsigned long long limit_ns)
+{
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i) {
+        uint32_t ok;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        if (ok) return true;
+    }
+    const unsigned long long t0 = global_ns();
+#pragma unroll 1
+    while (!mbar_try(bar, parity)) {
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > limit_ns) {
+            *abort_flag = 1;
+            set_status(status, NQ_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
 // A value that is the same on all lanes, so that the compiler knows it: what tcgen05.mma takes lies in uniform registers, and
 // an operand that it cannot prove uniform costs some 190 cycles per MMA instead of 34 to 66.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -179,11 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
 {
     using Q = Tt<FMT, D, KS>;
-    constexpr int SR = kKeys, RB = D / 2;
+    constexpr int SR = kKeys, RB = D / 2, STRIDE = KS ? kGroups : 1;            // of a group's steps
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) unsigned long long bars[kBars];
-    __shared__ uint32_t gone_of[Q::STAGES], gone_decoded[Q::BUFS];               // blocks that are not there
-    __shared__ int scaled_by[Q::BUFS];                                           // E of V's values; kCodes: they are codes
+    __shared__ uint32_t gone_of[Q::STAGES];                                      // blocks that are not there
+    __shared__ int2 about[Q::BUFS];                                              // the same; E of V's values, kCodes: they are codes
     __shared__ float2 state[KS ? 128 : 1];                                       // of group 1, for group 0
     __shared__ float cq_of[Q::Q_TILES * 128];                                    // factor of a query's scores
     __shared__ int abort_flag, keep_tmem;
@@ -221,28 +247,31 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
     tc_fence_after();
     const uint32_t tmem = uniform(tmem_slot);
     unsigned char *bufs = sm + Q::Q_TILES * Q::Q_BYTES, *scales = bufs + Q::BUFS * Q::BUF, *ring = scales + Q::BUFS * Q::SCALES;
-    auto wait = [&](int i, int phase) { return mbar_wait_fast(bar(i), static_cast<uint32_t>(phase) & 1u, &abort_flag, A.status, A.wait_ns); };
+    auto wait = [&](int i, int phase) { return wait_here(bar(i), static_cast<uint32_t>(phase) & 1u, &abort_flag, A.status, A.wait_ns); };
     const int steps = uniform(run.f1 - run.f0);
     Walk<SR> use;
     use.open(A, run.b, run.base, run.f0, run.f1);
 
     const Place<FMT, D> place(A);
-    if (warp == kFeedWarp) {
-        // ================================================= raw blocks into the ring
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp >= kFeedWarp) {
+        // ================================================= raw blocks into the ring: every second step
         Feeder<FMT, D> feed;
-        feed.start(A, use, segs, run.f0, smem_u32(ring), bar(kRawFull));
-        int i = 0;
-        for (; i < steps && feed.left > 0; ++i) {
+        int i = warp - kFeedWarp;
+        feed.start(A, use, segs, run.f0 + i, smem_u32(ring), bar(kRawFull));
+        for (; i < steps; i += kFeedWarps) {
             const int st = i % Q::STAGES;
             if (!__all_sync(0xffffffffu, wait(kRawEmpty + st, (i / Q::STAGES & 1) ^ 1))) break;
             feed.issue(A, place, segs, st, gone_of[st]);
         }
-        // every copy issued has landed before the CTA may exit
+        // every copy issued has landed before the CTA may exit: the last steps', as the others' stages have been read.  (Where
+        // a wait gave up: this warp's last two.)
         volatile int never = 0;
-        for (int k = max(0, i - Q::STAGES); k < i; ++k) mbar_wait(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
-    } else if (warp >= kMmaWarp) {
+        for (int k = i < steps ? i - 2 * kFeedWarps : i - kFeedWarps * Q::STAGES; k < i && k < steps; k += kFeedWarps)
+            if (k >= 0 && (i < steps || k >= steps - Q::STAGES)) wait_here(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
+    } else {
         // ================================================= MMAs of group g
-        constexpr int STRIDE = KS ? kGroups : 1;
         const int g = warp - kMmaWarp;
         const uint32_t idesc_s = f16_idesc(128, kKeys), idesc_o = f16_idesc(128, D) | kMajorMN_B, ts = tmem + 128 * g, to = tmem + kColO + 128 * g;
         const uint64_t q_desc = sw128_desc(smem_u32(sm) + (KS ? 0 : g * Q::Q_BYTES)), k_desc = sw128_desc(smem_u32(bufs)),
@@ -303,10 +332,12 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             else mbar_arrive(bar(kDrain + g));
             __syncwarp();
             volatile int never = 0;
-            const bool drained = mbar_wait(bar(kDrain + g), 0, &never, A.status, A.wait_ns);
+            const bool drained = wait_here(bar(kDrain + g), 0, &never, A.status, A.wait_ns);
             if (!__all_sync(0xffffffffu, drained) && lane == 0) keep_tmem = 1;
         }
+    }
     } else if (warp >= kSoftWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
         // ================================================= decode
         const int dt = threadIdx.x - 32 * kSoftWarps;
         for (int i = 0; i < steps; ++i) {
@@ -361,10 +392,7 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             }
             if (dt < kKeys) {
                 float *f = reinterpret_cast<float *>(scales + b * Q::SCALES);
-                if (dt == 0) {
-                    gone_decoded[b] = gone_of[st];
-                    scaled_by[b] = E;
-                }
+                if (dt == 0) about[b] = make_int2(gone_of[st], E);
                 f[dt] = number(scale_of(dt, 0));
                 if (E == kCodes) {
                     const float sv = number(scale_of(dt, 1));
@@ -380,6 +408,7 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         // ================================================= softmax: thread = query vector
         const int g = warp >> 2, r = (warp & 3) * 32 + lane, row = KS ? r : 128 * g + r;      // row of the tensor cores; vector of the tile
         const uint32_t tq = tmem + (static_cast<uint32_t>(warp & 3) << 21), to = tq + kColO + 128 * g;
@@ -443,9 +472,10 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             const int all_hi = tree.base, all_lo = first_seen(A, use.s.hi - 1);
             float mref = -INFINITY, mz = 0.0f, lsum = 0.0f;
 #pragma unroll 1
-            for (int k = KS ? g : 0; k < n; k += KS ? kGroups : 1, ++cnt) {
-                const int i = i0 + k, b = cnt & 1, row0 = use.s.lo + (run.f0 + i - use.base) * SR;
-                const bool begins = k < (KS ? kGroups : 1), masked = row0 < all_lo || row0 + SR > all_hi;
+            for (int k = KS ? g : 0, buf = (i0 + k) % Q::BUFS, row0 = use.s.lo + (run.f0 + i0 + k - use.base) * SR; k < n;
+                 k += STRIDE, ++cnt, row0 += STRIDE * SR, buf = buf + STRIDE >= Q::BUFS ? buf + STRIDE - Q::BUFS : buf + STRIDE) {
+                const int b = cnt & 1;
+                const bool begins = k < STRIDE, masked = row0 < all_lo || row0 + SR > all_hi;
                 const uint32_t tS = tq + 64 * (2 * g + b);
                 if (!__all_sync(0xffffffffu, wait(kSFull + 2 * g + b, cnt >> 1))) return false;
                 if (active) {
@@ -454,9 +484,10 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tc_ld16(tS + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(s + 16 * c));
                     tc_wait_ld();
-                    const float *f = reinterpret_cast<const float *>(scales + i % Q::BUFS * Q::SCALES);
-                    const uint32_t gone = gone_decoded[i % Q::BUFS];
-                    const int E = scaled_by[i % Q::BUFS];
+                    const float *f = reinterpret_cast<const float *>(scales + buf * Q::SCALES);
+                    const int2 info = about[buf];
+                    const uint32_t gone = info.x;
+                    const int E = info.y;
                     // scores in base 2 (X), or what cq makes scores of; two keys at a time in packed fp32
                     const unsigned long long zero2 = f2_pack(0.0f, 0.0f), cq2 = f2_pack(cq, cq);
 #pragma unroll
