@@ -311,6 +311,8 @@ static nq_status page_attn(const nq_page_pool *pool, int layer, const nq_page_ma
     A.QT = (M * G + cols - 1) / cols;
     // the kernel numbers the steps of all segments in 32 bits
     if (static_cast<double>(batch) * p.H * A.QT * (static_cast<double>(A.m.W) * A.m.P / 16 + 2) > 2.0e9) return NQ_ERR_SHAPE;
+    // (trees count the begin and end of a segment as steps as well)
+    if (tree && static_cast<double>(batch) * p.H * A.QT * (static_cast<double>(A.m.W) * A.m.P / 64 + 12) > 2.0e9) return NQ_ERR_SHAPE;
     A.seqs = seqs;
     A.len = len;
     A.scale = opts->scale;

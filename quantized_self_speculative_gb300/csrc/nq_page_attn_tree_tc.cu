@@ -44,6 +44,7 @@ static_assert(kThreads == 32 * (kFeedWarp + kFeedWarps), "roles");
 constexpr int kRegsLaunch = 96, kRegsSoft = 128, kRegsDecode = 72, kRegsRest = 80;
 static_assert(2 * kRegsSoft + 2 * kRegsDecode + kRegsRest == 5 * kRegsLaunch, "setmaxnreg draws on the launch's registers");
 constexpr int kMinRun = 2;              // steps per CTA
+constexpr int kSegCost = 8;             // what a segment costs beside its steps, in steps
 constexpr int kKeys = 64;               // cache rows per step
 constexpr int kTmem = 512;              // columns: S (P) of group g, buffer b at 64 (2 g + b), O of group g at 256 + 128 g
 constexpr uint32_t kColO = 256;
@@ -174,6 +175,98 @@ struct Feeder {
     }
 };
 
+// As find_run, but a segment's begin and end (queries in, rows out, pipelines that fill and
+// drain) count as kSegCost steps before its first: of ragged sequences some CTAs would
+// otherwise have five short segments where others have a part of one, and take twice as long.
+// f0, f1 are flat numbers of steps; `per` counts costs, of which segment number `seg`
+// (among all that have steps) begins at its flat number + seg * kSegCost.
+struct CostRun {
+    int f0, f1, per, b, base, seg;
+};
+template <int SR, int THREADS, int D>
+__device__ __forceinline__ CostRun find_cost_run(const AttnArgs &A, int segs)
+{
+    constexpr int WARPS = THREADS / 32;
+    __shared__ int2 sh_sum[WARPS];
+    __shared__ int sh_f[2], sh_b, sh_base, sh_seg;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_thread = (A.B + THREADS - 1) / THREADS, b_lo = min(static_cast<int>(threadIdx.x) * per_thread, A.B),
+              b_hi = min(b_lo + per_thread, A.B);
+    int2 mine = make_int2(0, 0);              // steps, segments
+#pragma unroll 1
+    for (int b = b_lo; b < b_hi; ++b) {
+        const int n = seq_of<SR>(A, b, blockIdx.x == 0).steps;
+        mine.x += n * segs;
+        mine.y += n ? segs : 0;
+    }
+    int2 incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+        if (lane >= o) {
+            incl.x += x;
+            incl.y += y;
+        }
+    }
+    if (lane == 31) sh_sum[warp] = incl;
+    __syncthreads();
+    int2 total = make_int2(0, 0), before = make_int2(incl.x - mine.x, incl.y - mine.y);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) {
+            before.x += sh_sum[w].x;
+            before.y += sh_sum[w].y;
+        }
+        total.x += sh_sum[w].x;
+        total.y += sh_sum[w].y;
+    }
+    if (threadIdx.x < 2) sh_f[threadIdx.x] = total.x;            // (an end past the last cost)
+    __syncthreads();
+    CostRun r;
+    const int all = total.x + kSegCost * total.y, grid = gridDim.x;
+    r.per = max(all / grid + (all % grid != 0), kMinRun + kSegCost);
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {                       // the run's first cost, and that of the next run
+        const long long c = static_cast<long long>(blockIdx.x + side) * r.per;
+        long long at = before.x + static_cast<long long>(kSegCost) * before.y;
+        if (c < at || c >= at + mine.x + static_cast<long long>(kSegCost) * mine.y) continue;
+        int flat = before.x, seg = before.y;
+#pragma unroll 1
+        for (int b = b_lo; b < b_hi; ++b) {
+            const int n = seq_of<SR>(A, b, false).steps;
+            if (n == 0) continue;
+            const long long cost = static_cast<long long>(n + kSegCost) * segs;
+            if (c < at + cost) {
+                const int k = static_cast<int>((c - at) / (n + kSegCost)), off = static_cast<int>(c - at) - k * (n + kSegCost);
+                sh_f[side] = flat + k * n + max(off - kSegCost, 0);
+                if (side == 0) {
+                    sh_b = b;
+                    sh_base = flat;
+                    sh_seg = seg + k;
+                }
+                break;
+            }
+            at += cost;
+            flat += n * segs;
+            seg += segs;
+        }
+    }
+#pragma unroll 1
+    for (int b = blockIdx.x; b < A.B; b += grid) {               // zeros of sequences of which no query sees a row
+        if (seq_of<SR>(A, b, false).steps != 0) continue;
+        const size_t n = static_cast<size_t>(A.M) * A.Hq * (D / 8);
+        uint4 *o = reinterpret_cast<uint4 *>(A.out) + b * n;
+#pragma unroll 1
+        for (size_t i = threadIdx.x; i < n; i += THREADS) o[i] = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    r.f0 = sh_f[0];
+    r.f1 = sh_f[1];
+    r.b = sh_b;
+    r.base = sh_base;
+    r.seg = sh_seg;
+    return r;
+}
 // mbar_wait_fast without its call: with one in it ptxas does not allocate a warpgroup's own share of registers.
 __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned int *status, unsigned long long limit_ns)
 {
@@ -236,7 +329,7 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
         for (int g = 0; g < kGroups; ++g) mbar_init(bar(kDrain + g), 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const Run run = find_run<SR, kThreads, D>(A, segs, kMinRun);
+    const CostRun run = find_cost_run<SR, kThreads, D>(A, segs);
     if (run.f0 >= run.f1) return;
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(kTmem) : "memory");
@@ -715,7 +808,7 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
                 }
             }
             if (i0 + n == steps && threadIdx.x == 0 && !ends && starts)
-                A.info[blockIdx.x] = make_int4(use.b, use.seg, (use.base + use.s.steps - 1) / run.per, 0);
+                A.info[blockIdx.x] = make_int4(use.b, use.seg, (use.base + use.s.steps - 1 + (run.seg + seg_no + 1) * kSegCost) / run.per, 0);
             return true;
         };
 #pragma unroll 1

@@ -11,7 +11,7 @@
 // goes on to the lowest child whose token is t of its parent.  Only the logits
 // rows of the walk are read (an argmax of all nodes would read nodes / length
 // times as much), one after another: a cluster of CTAs shares a row, so that one
-// sequence has 8 or 16 SMs' loads in flight, and every CTA learns the winner
+// sequence has eight SMs' loads in flight, and every CTA learns the winner
 // through distributed shared memory with one cluster barrier per row.
 //
 // Keep.  Row first + path[j] moves to row first + j.  path rises, so a row that is
@@ -56,8 +56,9 @@ plan_kernel(const int32_t *__restrict__ parents, int M, int words, int window, i
 }
 
 // ---------------------------------------------------------------- acceptance
-constexpr int kAccThreads = 512;
-constexpr int kAccUnroll = 5;             // 16-byte loads in flight per thread
+constexpr int kAccCluster = 8;            // the portable size
+constexpr int kAccThreads = 256;
+constexpr int kAccUnroll = 8;             // 16-byte loads in flight per thread
 
 // Larger is better: the value in order (the zeros alike), then the lower index.  NaN is below all.
 __device__ __forceinline__ unsigned long long order_of(float x, int i)
@@ -76,7 +77,7 @@ __device__ __forceinline__ unsigned long long shfl_max(unsigned long long v)
 }
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-__global__ void __launch_bounds__(kAccThreads)
+__global__ void __launch_bounds__(kAccThreads, 4)
 accept_tree_kernel(const int32_t *__restrict__ parents, const int32_t *__restrict__ depth, const int32_t *__restrict__ tokens,
                    const float *__restrict__ logits, int M, int V, int width, int32_t *__restrict__ out_tok,
                    int32_t *__restrict__ out_cnt, int32_t *__restrict__ path, unsigned int *status)
@@ -119,30 +120,31 @@ accept_tree_kernel(const int32_t *__restrict__ parents, const int32_t *__restric
             const unsigned long long k = order_of(x, static_cast<int>(f - f0));
             best = k > best ? k : best;
         };
-        for (size_t u = lo + threadIdx.x; u < hi; u += kAccUnroll * kAccThreads) {
+        // units wholly within the row: at most the first and the last are not
+        const size_t in0 = max(lo, (f0 + 3) >> 2), in1 = min(hi, f1 >> 2);
+        if (threadIdx.x == 0) {
+            for (size_t u = lo; u < min(in0, hi); ++u)
+                for (size_t f = max(4 * u, f0); f < min(4 * u + 4, f1); ++f) take(logits[f], f);
+            for (size_t u = max(in1, in0); u < hi; ++u)
+                for (size_t f = max(4 * u, f0); f < min(4 * u + 4, f1); ++f) take(logits[f], f);
+        }
+        for (size_t u = in0 + threadIdx.x; u < in1; u += kAccUnroll * kAccThreads) {
             float4 x[kAccUnroll];
-            bool whole[kAccUnroll];
 #pragma unroll
             for (int i = 0; i < kAccUnroll; ++i) {
-                const size_t v = u + i * kAccThreads;
-                whole[i] = v < hi && 4 * v >= f0 && 4 * v + 4 <= f1;
                 x[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                if (whole[i]) x[i] = __ldcs(reinterpret_cast<const float4 *>(logits) + v);
+                if (u + i * kAccThreads < in1) x[i] = __ldcs(reinterpret_cast<const float4 *>(logits) + u + i * kAccThreads);
             }
 #pragma unroll
             for (int i = 0; i < kAccUnroll; ++i) {
-                const size_t v = u + i * kAccThreads;
-                if (whole[i]) {
-                    // the first of the four that equals their largest; NaN leaves fmaxf, and is looked for apart
-                    const float top = fmaxf(fmaxf(x[i].x, x[i].y), fmaxf(x[i].z, x[i].w));
-                    const int e = x[i].x == top ? 0 : x[i].y == top ? 1 : x[i].z == top ? 2 : 3;
-                    odd |= !(fabsf(x[i].x) <= 3.4028235e38f) || !(fabsf(x[i].y) <= 3.4028235e38f) ||
-                           !(fabsf(x[i].z) <= 3.4028235e38f) || !(fabsf(x[i].w) <= 3.4028235e38f);
-                    const unsigned long long k = order_of(top, static_cast<int>(4 * v + e - f0));
-                    best = k > best ? k : best;
-                } else if (v < hi) {
-                    for (size_t f = max(4 * v, f0); f < min(4 * v + 4, f1); ++f) take(logits[f], f);
-                }
+                if (u + i * kAccThreads >= in1) break;
+                // the first of the four that equals their largest; NaN leaves fmaxf, and is looked for apart
+                const float top = fmaxf(fmaxf(x[i].x, x[i].y), fmaxf(x[i].z, x[i].w));
+                const int e = x[i].x == top ? 0 : x[i].y == top ? 1 : x[i].z == top ? 2 : 3;
+                odd |= !(fabsf(x[i].x) <= 3.4028235e38f) || !(fabsf(x[i].y) <= 3.4028235e38f) ||
+                       !(fabsf(x[i].z) <= 3.4028235e38f) || !(fabsf(x[i].w) <= 3.4028235e38f);
+                const unsigned long long k = order_of(top, static_cast<int>(4 * (u + i * kAccThreads) + e - f0));
+                best = k > best ? k : best;
             }
         }
         best = shfl_max(best);
@@ -314,7 +316,7 @@ extern "C" nq_status spec_accept_tree(const nq_tree *tree, const int32_t *tokens
     if (!status) return NQ_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 8;
+    attr[0].val.clusterDim.x = nq::kAccCluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tree->batch) * attr[0].val.clusterDim.x);
