@@ -614,9 +614,10 @@ def rope(x: torch.Tensor, pos: torch.Tensor, plan: Rope, out: Optional[torch.Ten
 # ---------------------------------------------------------------- between two linears
 def _matrix(t: torch.Tensor, M: int, K: int, what: str):
     """Address, type and row stride of fp32 or bf16 [M][K], each row contiguous."""
-    if not t.is_cuda or t.dtype not in _DT or t.shape != (M, K) or (t.stride(1) != 1 and K > 1):
+    kind = _DT.get(t.dtype)
+    if kind is None or not t.is_cuda or t.shape != (M, K) or not (t.is_contiguous() or t.stride(1) == 1 or K == 1):
         raise ValueError(f"{what} must be a CUDA tensor of fp32 or bf16, shape {(M, K)}, contiguous within a row")
-    return t.data_ptr(), _DT[t.dtype], t.stride(0) if M > 1 else K
+    return t.data_ptr(), kind, t.stride(0) if M > 1 else K
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6, add: Optional[torch.Tensor] = None,
@@ -627,31 +628,39 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float 
     quantize (s, xq, sx): int8 codes and fp32 row scales for LinearA8Batch."""
     if x.dim() != 2:
         raise ValueError("x must be fp32 or bf16 [M][K]")
-    M, K = x.shape
-    xp = _matrix(x, M, K, "x")
-    ap = (None, 0, 0) if add is None else _matrix(add, M, K, "add")
-    if weight is not None and (weight.shape != (K,) or weight.dtype not in _DT or not weight.is_cuda or not weight.is_contiguous()):
-        raise ValueError("weight must be a contiguous CUDA tensor of fp32 or bf16 [K]")
-    if sum_out is not None and (add is None or sum_out.dtype != x.dtype):
-        raise ValueError("sum_out comes with add and has x's type")
+    M, K = shape = x.shape
+    xp, xt, xs = _matrix(x, M, K, "x")
+    wp, wt = None, 0
+    if weight is not None:
+        wt = _DT.get(weight.dtype)
+        if wt is None or weight.shape != (K,) or not weight.is_cuda or not weight.is_contiguous():
+            raise ValueError("weight must be a contiguous CUDA tensor of fp32 or bf16 [K]")
+        wp = weight.data_ptr()
     if (y is not None) if quantize else (xq is not None or sx is not None):
         raise ValueError("y without quantize, xq and sx with it")
-    s = x if add is None else sum_out if sum_out is not None else _empty((M, K), x.dtype, x.device, stream)
-    sp = (None, 0, 0) if add is None else _matrix(s, M, K, "sum_out")
+    if add is None:
+        if sum_out is not None:
+            raise ValueError("sum_out comes with add and has x's type")
+        s, ap, at, as_, sp, ss = x, None, 0, 0, None, 0
+    else:
+        ap, at, as_ = _matrix(add, M, K, "add")
+        s = sum_out if sum_out is not None else _empty(shape, x.dtype, x.device, stream)
+        if s.dtype != x.dtype:
+            raise ValueError("sum_out comes with add and has x's type")
+        sp, _, ss = _matrix(s, M, K, "sum_out")
     if quantize:
-        xq = xq if xq is not None else _empty((M, K), torch.int8, x.device, stream)
+        xq = xq if xq is not None else _empty(shape, torch.int8, x.device, stream)
         sx = sx if sx is not None else _empty((M,), torch.float32, x.device, stream)
-        if xq.shape != (M, K) or sx.shape != (M,):
+        if xq.shape != shape or sx.shape != (M,):
             raise ValueError("xq must be int8 [M][K], sx fp32 [M]")
         out = None, _dev(xq, torch.int8, "xq"), _dev(sx, torch.float32, "sx")
     else:
-        y = y if y is not None else _empty((M, K), torch.bfloat16, x.device, stream)
-        if y.shape != (M, K):
+        y = y if y is not None else _empty(shape, torch.bfloat16, x.device, stream)
+        if y.shape != shape:
             raise ValueError("y must be bf16 [M][K]")
         out = _dev(y, torch.bfloat16, "y"), None, None
     if M:
-        _check(lib().nq_rms_norm(*xp, *ap, None if weight is None else weight.data_ptr(), 0 if weight is None else _DT[weight.dtype],
-                                 float(eps), M, K, sp[0], sp[2], *out, _stream(stream)), "nq_rms_norm")
+        _check(lib().nq_rms_norm(xp, xt, xs, ap, at, as_, wp, wt, eps, M, K, sp, ss, *out, _stream(stream)), "nq_rms_norm")
     return (s, xq, sx) if quantize else (s, y)
 
 
