@@ -205,3 +205,31 @@ def test_refusals(nq):
     assert e.value.status == nq.NQ_ERR_WORKSPACE
     empty = nq.Tree(torch.empty(0, 6, dtype=torch.int32, device="cuda"))
     assert pool.attention(0, m, q[:0], n[:0], 2, 0.1, tree=empty).shape == (0, 6, 2, 64)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("planes", [1, 2])
+@pytest.mark.parametrize("M,Hq", [(9, 1), (20, 1), (40, 1), (50, 3)])
+@pytest.mark.parametrize("sizes", ["tiny", "large", "mixed", "mixed late", "zeros"])
+def test_values_of_very_unequal_size(nq, D, planes, M, Hq, sizes):
+    """V rows whose scales are near fp16's ends, span more than fp16's normal numbers within a step or from step to
+    step, or are zero: the tensor-core kernel takes them as values relative to the step's largest, or as codes."""
+    lens, parents = [M + 400, M + 70], T.trees(M, 2, M)
+    pool, m, q = setup(nq, lens, parents, 16, 1, Hq, D, D, 0, M + D)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    at = [(b, t) for b, n in enumerate(lens) for t in range(n) if t < n - M or T.sets_of(parents[b])[t - (n - M)][0] >= 0]
+    kv = torch.randn(len(at), 2, D, generator=g, device="cuda")
+    f = torch.ones(len(at), device="cuda")
+    if sizes == "tiny":
+        f *= 2e-5
+    elif sizes == "large":
+        f *= 1e5
+    elif sizes == "mixed":
+        f[::5], f[1::5], f[2::7] = 2e-4, 3e3, 1e-6
+    elif sizes == "mixed late":
+        f[:200], f[200:330], f[400:] = 1e-4, 1e2, 1e4
+    else:
+        f[::2] = 0
+    pool.append(0, m, kv[:, :1], kv[:, 1:] * f[:, None, None], i32([b for b, _ in at]), i32([t for _, t in at]))
+    assert nq.device_status() == 0
+    check(nq, pool, m, q, lens, parents, planes)
