@@ -239,7 +239,13 @@ int cols_of(int vectors, bool tc)
     return vectors <= 8 ? 8 : vectors <= 16 ? 16 : vectors <= 32 ? 32 : 64;
 }
 
-// Trees: the same rule, but a tile of the tensor cores holds up to 256 vectors, even shares of what there is.
+// Trees have a tensor-core kernel of their own, which takes more than 16 vectors of a cache
+// with one scale per row.  us on the tensor cores / per CTA, 8 kv heads, 4-bit | 8-bit view:
+//                        heads of 128: 20               24       heads of 64: 20                24
+//   16 of 500..4000 rows       47 / 62 | 49 / 66  47 / 63 | 49 / 68   39 / 37 | 41 / 41   39 / 39 | 41 / 41
+//   one of 32768 rows          41 / 64 | 43 / 67  41 / 65 | 43 / 68   35 / 44 | 36 / 46   35 / 45 | 37 / 47
+bool tree_tensor_cores(int vectors, int fmt, int ng) { return vectors > 16 && fmt != kBf16 && ng == 1; }
+// Its tiles hold up to 256 vectors, even shares of what there is.
 int tree_cols(int vectors, bool tc)
 {
     const int tiles = (vectors + 255) / 256;
@@ -306,7 +312,7 @@ static nq_status page_attn(const nq_page_pool *pool, int layer, const nq_page_ma
     A.G = G;
     A.g_mul = static_cast<unsigned>((0x100000000ull + G - 1) / G);
     const int fmt = p.NG == 0 ? nq::kBf16 : planes == 1 ? nq::kKv4 : nq::kKv8;
-    const bool tc = nq::tensor_cores(M * G, fmt, p.NG, p.D);
+    const bool tc = tree ? nq::tree_tensor_cores(M * G, fmt, p.NG) : nq::tensor_cores(M * G, fmt, p.NG, p.D);
     const int cols = A.cols = tree ? nq::tree_cols(M * G, tc) : nq::cols_of(M * G, tc);
     A.QT = (M * G + cols - 1) / cols;
     // the kernel numbers the steps of all segments in 32 bits

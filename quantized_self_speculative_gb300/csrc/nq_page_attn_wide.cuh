@@ -492,20 +492,24 @@ cudaError_t launch(const AttnArgs &A, cudaStream_t s, int *grid)
     attn_wide_kernel<FMT, D, NG, WARPS, X, T><<<*grid, 32 * WARPS, Q::SMEM, s>>>(A);
     return cudaGetLastError();
 }
-// (Trees take the form for capped or biased scores whatever theirs are.)
+// (Trees take the form for capped or biased scores whatever theirs are, and come with bf16 pages or two scales per row.)
 template <int FMT, int D, int NG, bool T>
 cudaError_t launch_x(const AttnArgs &A, int warps, cudaStream_t s, int *grid)
 {
     const bool x = T || A.softcap > 0.0f || A.slopes;
-    // nested pages with one scale per row come with at most 32 vectors: more go to the tensor cores
-    if constexpr (FMT == kBf16 || NG == 2)
-        if (warps == 8) {
-            if (x) return launch<FMT, D, NG, 8, true, T>(A, s, grid);
-            if constexpr (!T) return launch<FMT, D, NG, 8, false, T>(A, s, grid);
-        }
-    if (warps != 4) return cudaErrorInvalidValue;
-    if (x) return launch<FMT, D, NG, 4, true, T>(A, s, grid);
-    if constexpr (!T) return launch<FMT, D, NG, 4, false, T>(A, s, grid);
+    if constexpr (T && FMT != kBf16 && NG == 1) {
+        return cudaErrorInvalidValue;
+    } else {
+        // nested pages with one scale per row come with at most 32 vectors: more go to the tensor cores
+        if constexpr (FMT == kBf16 || NG == 2)
+            if (warps == 8) {
+                if (x) return launch<FMT, D, NG, 8, true, T>(A, s, grid);
+                if constexpr (!T) return launch<FMT, D, NG, 8, false, T>(A, s, grid);
+            }
+        if (warps != 4) return cudaErrorInvalidValue;
+        if (x) return launch<FMT, D, NG, 4, true, T>(A, s, grid);
+        if constexpr (!T) return launch<FMT, D, NG, 4, false, T>(A, s, grid);
+    }
 }
 template <int FMT, bool T>
 cudaError_t launch_d(const AttnArgs &A, int warps, cudaStream_t s, int *grid)

@@ -223,13 +223,14 @@ def test_values_of_very_unequal_size(nq, D, planes, M, Hq, sizes):
     if sizes == "tiny":
         f *= 2e-5
     elif sizes == "large":
-        f *= 1e5
+        f *= 5e4
     elif sizes == "mixed":
         f[::5], f[1::5], f[2::7] = 2e-4, 3e3, 1e-6
     elif sizes == "mixed late":
         f[:200], f[200:330], f[400:] = 1e-4, 1e2, 1e4
     else:
         f[::2] = 0
-    pool.append(0, m, kv[:, :1], kv[:, 1:] * f[:, None, None], i32([b for b, _ in at]), i32([t for _, t in at]))
+    kv[:, 1] *= f[:, None]
+    pool.append(0, m, kv[:, :1], kv[:, 1:], i32([b for b, _ in at]), i32([t for _, t in at]))
     assert nq.device_status() == 0
     check(nq, pool, m, q, lens, parents, planes)
