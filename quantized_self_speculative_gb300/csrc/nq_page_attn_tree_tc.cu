@@ -7,7 +7,8 @@
 // cache rows, decoded once: K into signed fp16 codes (exact; its scales multiply S), V
 // into fp16 values relative to a power of two 2^E near the step's largest scale (one
 // rounding, 2^-11; P carries the 2^E).  Where a step's scales span more than 2^12
-// (values would leave fp16's normal numbers) V stays codes, and its scales multiply P.
+// (values would leave fp16's normal numbers), and where it has rows that some query does
+// not see, V stays codes, and its scales multiply P.
 // That leaves the softmax one scale per key to read: with V's scale and its log2 as
 // well shared memory is 77% busy (13 instead of 19 million wavefronts, the long case
 // below).  One warp per scheduler does not fill the softmax's dependent chain
@@ -31,8 +32,8 @@
 // cost, of which a segment's begin and end are eight steps' worth.
 //
 // Measured (GB300, 8-bit view): 16 sequences of 333..4131 rows, 8 kv heads of 128, trees
-// of up to 32 nodes, 128 vectors: 53 us for 86 MB and 20 GFLOP (13 us at the copy rate; the
-// warp-MMA kernels 233); 4 of 20065..32832 rows, 4 kv heads, 64 nodes x 7 heads: 135 us
+// of up to 32 nodes, 128 vectors: 55 us for 86 MB and 20 GFLOP (13 us at the copy rate; the
+// warp-MMA kernels 233); 4 of 20065..32832 rows, 4 kv heads, 64 nodes x 7 heads: 137 us
 // for 104 GFLOP (55 us at the measured bf16 rate, 40%; the warp-MMA kernels 988).  A step
 // of 256 vectors takes some 2400 cycles: the tensor pipe 1020, the softmax of a group 1600
 // beside some 800 of waits, fences and loop.
@@ -57,6 +58,7 @@ constexpr int kKeys = 64;               // cache rows per step
 constexpr int kTmem = 512;              // columns: S (P) of group g, buffer b at 64 (2 g + b), O of group g at 256 + 128 g
 constexpr uint32_t kColO = 256;
 constexpr int kCodes = 1000, kSpan = 12;
+constexpr uint32_t kHidden = 0x100;      // with the bits of the blocks that are not there: the step has rows that some query does not see
 
 template <int FMT, int D, bool KS>
 struct Tt {
@@ -158,7 +160,10 @@ struct Feeder {
         const bool bad = k < n && (mine < 0 || mine >= A.p.N);
         const uint32_t out = __ballot_sync(0xffffffffu, bad);
         if (bad) set_status(A.status, NQ_DEV_BAD_PAGE);
-        gone = out;                           // before the barrier's arrival, which lets the decoders read it
+        // before the barrier's arrival, which lets the decoders read it.  Where some row is hidden from some query nothing
+        // may depend on what such rows hold (or what a stage held before): V stays codes there
+        const bool masked = row < first_seen(A, w.s.hi - 1) || row + kKeys > w.s.hi - A.M;
+        gone = out | (masked ? kHidden : 0u);
         __syncwarp();
         if (k == 0) mbar_expect_tx(b, (n - __popc(out)) * (BASE + RESID));
         __syncwarp();
@@ -467,7 +472,8 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             const uint32_t s0 = scale_of(lane, 1), s1 = scale_of(lane + 32, 1);
             const uint32_t top = __reduce_max_sync(0xffffffffu, max(s0, s1)), low = __reduce_min_sync(0xffffffffu, min(s0 ? s0 : 0xFFFFu, s1 ? s1 : 0xFFFFu));
             auto exponent = [&](uint32_t x) { return static_cast<int>(__float_as_uint(number(x)) >> 23) - 127; };
-            const int E = top == 0 ? 0 : exponent(top) - exponent(low) > kSpan ? kCodes : exponent(top);
+            const uint32_t flags = gone_of[st];
+            const int E = flags ? kCodes : top == 0 ? 0 : exponent(top) - exponent(low) > kSpan ? kCodes : exponent(top);
             const float by = __uint_as_float(static_cast<uint32_t>(127 - (E == kCodes ? 0 : E)) << 23);
 #pragma unroll
             for (int k = 0; k < N; ++k) {
@@ -493,7 +499,7 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             }
             if (dt < kKeys) {
                 float *f = reinterpret_cast<float *>(scales + b * Q::SCALES);
-                if (dt == 0) about[b] = make_int2(gone_of[st], E);
+                if (dt == 0) about[b] = make_int2(flags & (kHidden - 1), E);
                 f[dt] = number(scale_of(dt, 0));
                 if (E == kCodes) {
                     const float sv = number(scale_of(dt, 1));

@@ -234,3 +234,74 @@ def test_values_of_very_unequal_size(nq, D, planes, M, Hq, sizes):
     pool.append(0, m, kv[:, :1], kv[:, 1:], i32([b for b, _ in at]), i32([t for _, t in at]))
     assert nq.device_status() == 0
     check(nq, pool, m, q, lens, parents, planes)
+
+
+SIZES = [(5, 1), (14, 1), (20, 2), (20, 4), (40, 4)]            # nodes, query heads of one kv head: every kernel
+
+
+@pytest.mark.parametrize("fmt,planes", [(0, 1), (0, 2), (1, 2)])
+@pytest.mark.parametrize("M,Hq", SIZES)
+def test_lengths_up_to_the_largest(nq, fmt, planes, M, Hq):
+    """2^27 - 1 pages that are all one and the same: row t is row t mod 16, wherever the tree lies.  Lengths past
+    2^31 - 4096 are clamped and reported."""
+    W, P, D = (1 << 27) - 1, 16, 64
+    parents = T.trees(4 * M, 1, M)
+    assert all(p >= -1 for p in parents[0])
+    pool, small, q = setup(nq, [P], [[-1] * M], P, 1, Hq, D, D, fmt, 12)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    kv = torch.randn(P, 2, D, generator=g, device="cuda")
+    pool.append(0, small, kv[:, :1], kv[:, 1:], i32([0] * P), torch.arange(P, device="cuda").int())
+    one = int(small.table[0, 0])
+    m = nq.PageMap(1, W, pool.n_pages, P, table=torch.full((1, W), one, dtype=torch.int32, device="cuda"))
+    few, most = np.full((1, 24), one), 2 ** 31 - 4096
+    tree = nq.Tree(i32(parents), window=70)
+    for n in (most - 7, most - 64, most, most + 1, W * P - 9, 2 ** 31 - 1):
+        n0 = 256 + min(n, most) % 16
+        ref, tol = T.tree_attention64(HostPool(pool), 0, few, q.float().cpu().numpy(), [n0], planes, 0.125, parents, window=70)
+        out = pool.attention(0, m, q, i32([n]), planes, 0.125, window=70, tree=tree).double().cpu().numpy()
+        assert nq.device_status() == (nq.NQ_DEV_SEQ_FULL if n > most else 0)
+        assert (np.abs(out - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("D,G,P,fmt", GEO)
+@pytest.mark.parametrize("M,Hq", SIZES)
+@pytest.mark.parametrize("window", [0, 50])
+def test_pages_outside_the_pool_are_hidden(nq, D, G, P, fmt, M, Hq, window):
+    """Their rows count as not there for every query, and nothing of another page takes their place."""
+    lens = [5 * P + M, 3 * P + 1 + M, M, 7 * P + 3 + M]
+    broken = [[0, 3], [1, 2], [0], [2, 4, 7]]
+    parents = T.trees(5 * M, 4, M)
+    pool, m, q = setup(nq, lens, parents, P, 1, Hq, D, G, fmt, M + P)
+    table = m.table.cpu().numpy().copy()
+    gone = [np.isin(np.arange(n) // P, broken[b]) for b, n in enumerate(lens)]
+    ref, tol = T.tree_attention64(HostPool(pool), 0, table, q.float().nan_to_num(0).cpu().numpy(), lens, 2, 0.125, parents, window=window, gone=gone)
+    tree = nq.Tree(i32(parents), window=window)
+    for bad in (-1, pool.n_pages, 2 ** 31 - 1, -2 ** 31):
+        for b, js in enumerate(broken):
+            for j in js:
+                m.table[b, j] = bad
+        out = pool.attention(0, m, q, i32(lens), 2, 0.125, window=window, tree=tree).double().cpu().numpy()
+        assert nq.device_status() == nq.NQ_DEV_BAD_PAGE
+        assert (np.abs(out - ref) <= tol + 1e-30).all()
+
+
+@pytest.mark.parametrize("M,Hq", SIZES)
+def test_two_graphs_at_once(nq, M, Hq):
+    """Captured on two streams and replayed together: each has a workspace of its own."""
+    lens, parents = [M + 900, M + 40], T.trees(M, 2, M)
+    pool, m, q = setup(nq, lens, parents, 16, 2, 2 * Hq, 128, 128, 0, 3)
+    n, tree = i32(lens), nq.Tree(i32(parents))
+    qs = [q, (q.float() * 0.5).bfloat16()]
+    want = [pool.attention(0, m, x, n, 2, 0.09, tree=tree) for x in qs]
+    outs, graphs = [torch.empty_like(q) for _ in qs], [torch.cuda.CUDAGraph() for _ in qs]
+    for x, o, gr in zip(qs, outs, graphs):
+        with torch.cuda.graph(gr):
+            pool.attention(0, m, x, n, 2, 0.09, tree=tree, out=o)
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(5):
+        torch.cuda.synchronize()
+        for s, gr in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))

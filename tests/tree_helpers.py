@@ -62,8 +62,9 @@ def accept(parents, tokens, logits, width):
     return out, path
 
 
-def tree_attention64(hp, layer, table, q, lens, planes, scale, parents, softcap=0.0, window=0, slopes=None):
-    """(out, tol) as paged_helpers.attention64 derives them, over the rows that each node sees."""
+def tree_attention64(hp, layer, table, q, lens, planes, scale, parents, softcap=0.0, window=0, slopes=None, gone=None):
+    """(out, tol) as paged_helpers.attention64 derives them, over the rows that each node sees
+    (less those that are gone[b])."""
     B, M, Hq, D = q.shape
     g = Hq // hp.H
     out, tol = np.zeros((B, M, Hq, D)), np.zeros((B, M, Hq, D))
@@ -81,6 +82,8 @@ def tree_attention64(hp, layer, table, q, lens, planes, scale, parents, softcap=
             rows = np.array(list(range(max(base, 0))) + [base + j for j in up if base + j >= 0], np.int64)
             pos = np.array(list(range(max(base, 0))) + [base + k for k, j in enumerate(up) if base + j >= 0], np.int64)
             seen = pos > at - (window or 1 << 40)         # (positions below 0 where a sequence is shorter than its tree)
+            if gone is not None:
+                seen &= ~gone[b][rows]
             rows, pos = rows[seen], pos[seen]
             if len(rows) == 0:
                 continue
