@@ -7,8 +7,8 @@
 // cache rows, decoded once: K into signed fp16 codes (exact; its scales multiply S), V
 // into fp16 values relative to a power of two 2^E near the step's largest scale (one
 // rounding, 2^-11; P carries the 2^E).  Where a step's scales span more than 2^12
-// (values would leave fp16's normal numbers), and where it has rows that some query does
-// not see, V stays codes, and its scales multiply P.
+// (values would leave fp16's normal numbers) or one of them is 0, and where it has rows that
+// some query does not see, V stays codes, and its scales multiply P.
 // That leaves the softmax one scale per key to read: with V's scale and its log2 as
 // well shared memory is 77% busy (13 instead of 19 million wavefronts, the long case
 // below).  One warp per scheduler does not fill the softmax's dependent chain
@@ -470,10 +470,11 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
             };
             auto number = [](uint32_t x) { return __half2float(__ushort_as_half(static_cast<unsigned short>(x))); };
             const uint32_t s0 = scale_of(lane, 1), s1 = scale_of(lane + 32, 1);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, max(s0, s1)), low = __reduce_min_sync(0xffffffffu, min(s0 ? s0 : 0xFFFFu, s1 ? s1 : 0xFFFFu));
+            const uint32_t top = __reduce_max_sync(0xffffffffu, max(s0, s1)), low = __reduce_min_sync(0xffffffffu, min(s0, s1));
             auto exponent = [&](uint32_t x) { return static_cast<int>(__float_as_uint(number(x)) >> 23) - 127; };
             const uint32_t flags = gone_of[st];
-            const int E = flags ? kCodes : top == 0 ? 0 : exponent(top) - exponent(low) > kSpan ? kCodes : exponent(top);
+            // (a row of scale 0 adds nothing to the numerator: among codes its log2 keeps its score from raising the reference)
+            const int E = flags || low == 0 || exponent(top) - exponent(low) > kSpan ? kCodes : exponent(top);
             const float by = __uint_as_float(static_cast<uint32_t>(127 - (E == kCodes ? 0 : E)) << 23);
 #pragma unroll
             for (int k = 0; k < N; ++k) {
