@@ -15,8 +15,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // between (at 2^6 some row of 32 outgrew it at nearly every step of 64 keys).  fp16
 // holds P <= 2^15, and below its normal part rounds by 2^-25: 2^-28 of the maximum at
 // most, so that the numerator keeps the tails that the sum of the unrounded P counts
-// (n rows: n 2^-28 of it at most).  bf16 has the range of fp32 and rounds P to 2^-8:
-// there the largest P stays 1, which is exact.
+// (n rows: n 2^-28 of it at most; n 2^-23 where trees' V holds its scales, see kSpan
+// there).  bf16 has the range of fp32 and rounds P to 2^-8: there the largest P stays 1,
+// which is exact.
 template <int FMT> __host__ __device__ constexpr float lead() { return FMT == kBf16 ? 0.0f : 3.0f; }
 template <int FMT> __host__ __device__ constexpr float slack() { return FMT == kBf16 ? 0.0f : 15.0f; }
 

@@ -6,9 +6,9 @@
 // in nq_page_attn_tc.cu a row of the tensor cores is a query vector and a step is 64
 // cache rows, decoded once: K into signed fp16 codes (exact; its scales multiply S), V
 // into fp16 values relative to a power of two 2^E near the step's largest scale (one
-// rounding, 2^-11; P carries the 2^E).  Where a step's scales span more than 2^12
-// (values would leave fp16's normal numbers) or one of them is 0, and where it has rows that
-// some query does not see, V stays codes, and its scales multiply P.
+// rounding, 2^-11; P carries the 2^E).  Where a step's scales span more than 2^4 (kSpan) or
+// one of them is 0, and where it has rows that some query does not see, V stays codes, and
+// its scales multiply P.
 // That leaves the softmax one scale per key to read: with V's scale and its log2 as
 // well shared memory is 77% busy (13 instead of 19 million wavefronts, the long case
 // below).  One warp per scheduler does not fill the softmax's dependent chain
@@ -57,7 +57,13 @@ constexpr int kSegCost = 8;             // what a segment costs beside its steps
 constexpr int kKeys = 64;               // cache rows per step
 constexpr int kTmem = 512;              // columns: S (P) of group g, buffer b at 64 (2 g + b), O of group g at 256 + 128 g
 constexpr uint32_t kColO = 256;
-constexpr int kCodes = 1000, kSpan = 12;
+constexpr int kCodes = 1000;
+// V's scales of a step may span 2^kSpan where they go into its values.  P is then relative to the step's largest scale, not
+// to each row's: of a largest contribution from a row with the smallest scale the reference lies up to 2^(kSpan + 1) above
+// it, and P's rounding of 2^-25 below fp16's normal numbers is 2^(kSpan - 27) of it, n rows' n times that (2^-28 among codes).
+// At 12, where V itself would leave the normal numbers, 12000 rows below one key with nearly all the weight and a value
+// 2^11 below theirs were lost, some hundredths of the output.
+constexpr int kSpan = 4;
 constexpr uint32_t kHidden = 0x100;      // with the bits of the blocks that are not there: the step has rows that some query does not see
 
 template <int FMT, int D, bool KS>

@@ -68,13 +68,8 @@ def small_tail(hp, table, q, lens, planes, scale, parents):
     return out, tol
 
 
-@pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("planes", [1, 2])
-@pytest.mark.parametrize("M,Hq", SIZES)
-@pytest.mark.parametrize("value,bits", [(0.0, 27.0), (0.0, 29.6)])
-def test_a_long_tail_below_one_key(nq, D, planes, M, Hq, value, bits):
-    """One key has nearly all the weight and a value of nothing, or of little beside its neighbours': the many others
-    carry the output."""
+def long_tail(nq, D, planes, M, Hq, value, bits, batch):
+    """One key of 12000 has nearly all the weight, and `value` times the size of the others' values."""
     lens, parents = [12000 + M], T.trees(M, 1, M)
     pool, m, _ = setup(nq, lens, parents, 64, 1, Hq, D, D, 0, M + D)
     g = torch.Generator(device="cuda").manual_seed(9)
@@ -83,10 +78,29 @@ def test_a_long_tail_below_one_key(nq, D, planes, M, Hq, value, bits):
     k[:, 5] = bits * np.log(2.0) * D ** -0.5             # against queries of ones
     v[:, 5] *= value
     store(pool, m, lens, parents, k, v)
-    q = torch.ones(1, M, Hq, D, device="cuda").bfloat16()
+    q = torch.ones(batch, M, Hq, D, device="cuda").bfloat16()
     scale = D ** -0.5
-    out = pool.attention(0, m, q, i32(lens), planes, scale, tree=nq.Tree(i32(parents))).double().cpu().numpy()
+    out = pool.attention(0, m, q, i32(lens * batch), planes, scale, seqs=i32([0] * batch), tree=nq.Tree(i32(parents * batch)))
     assert nq.device_status() == 0
-    ref, tol = small_tail(HostPool(pool), m.table.cpu().numpy(), q.float().cpu().numpy(), lens, planes, scale, parents)
-    off = np.abs(out - ref)
+    ref, tol = small_tail(HostPool(pool), m.table.cpu().numpy(), q[:1].float().cpu().numpy(), lens, planes, scale, parents)
+    off = np.abs(out.double().cpu().numpy() - ref)
     assert (off <= tol + 1e-30).all(), (off / (np.abs(ref) + 1e-30)).max()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("planes", [1, 2])
+@pytest.mark.parametrize("M,Hq", SIZES)
+@pytest.mark.parametrize("value,bits", [(0.0, 27.0), (0.0, 29.6)])
+def test_a_long_tail_below_one_key(nq, D, planes, M, Hq, value, bits):
+    """One key has nearly all the weight and a value of nothing: the many others carry the output."""
+    long_tail(nq, D, planes, M, Hq, value, bits, 1)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("planes", [1, 2])
+@pytest.mark.parametrize("M,Hq", SIZES)
+@pytest.mark.parametrize("value,bits", [(0.0, 29.6), (2.0 ** -11, 27.0), (2.0 ** -11, 28.3), (2.0 ** -8, 28.3), (2.0 ** -4, 28.3)])
+def test_a_long_tail_within_one_state(nq, D, planes, M, Hq, value, bits):
+    """The same, or a value of little beside its neighbours', for more sequences than there are SMs: one running maximum
+    goes over all of the rows, none of which may fall out of fp16's range beside it."""
+    long_tail(nq, D, planes, M, Hq, value, bits, 160)
