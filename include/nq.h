@@ -731,6 +731,11 @@ NQ_API nq_status nq_selftest_page_attn(const nq_page_pool *pool, int layer, cons
                                        int64_t q_stride, int batch, int M, int heads_q, const int32_t *seqs,
                                        const int32_t *len, int planes, const nq_attn_opts *opts, uint16_t *out, void *ws,
                                        size_t ws_bytes, int steps, uint32_t limit_us, cudaStream_t stream);
+/* Likewise for nq_page_attn_tree. */
+NQ_API nq_status nq_selftest_page_attn_tree(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,
+                                            int64_t q_stride, int heads_q, const int32_t *seqs, const int32_t *len, int planes,
+                                            const nq_attn_opts *opts, const nq_tree *tree, uint16_t *out, void *ws,
+                                            size_t ws_bytes, int steps, uint32_t limit_us, cudaStream_t stream);
 
 /* Human-readable name of a status code (static string). */
 NQ_API const char *nq_status_string(int status);

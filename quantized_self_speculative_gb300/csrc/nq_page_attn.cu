@@ -385,3 +385,15 @@ extern "C" nq_status nq_selftest_page_attn(const nq_page_pool *pool, int layer, 
     return page_attn(pool, layer, map, q, q_stride, batch, M, heads_q, seqs, len, planes, opts, nullptr, out, ws, ws_bytes, stream, steps,
                      limit_us * 1000ull);
 }
+
+extern "C" nq_status nq_selftest_page_attn_tree(const nq_page_pool *pool, int layer, const nq_page_map *map, const uint16_t *q,
+                                                int64_t q_stride, int heads_q, const int32_t *seqs, const int32_t *len, int planes,
+                                                const nq_attn_opts *opts, const nq_tree *tree, uint16_t *out, void *ws,
+                                                size_t ws_bytes, int steps, uint32_t limit_us, cudaStream_t stream)
+{
+    if (steps < 0 || limit_us < 1 || limit_us > 1000000u) return NQ_ERR_ARG;
+    const nq_status st = nq::tree_of(tree);
+    if (st != NQ_OK) return st;
+    return page_attn(pool, layer, map, q, q_stride, tree->batch, tree->nodes, heads_q, seqs, len, planes, opts, tree, out, ws, ws_bytes, stream,
+                     steps, limit_us * 1000ull);
+}

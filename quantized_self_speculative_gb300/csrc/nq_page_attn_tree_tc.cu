@@ -371,14 +371,15 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
         // ================================================= raw blocks into the ring: every second step
         Feeder<FMT, D> feed;
         int i = warp - kFeedWarp;
+        const int fed = A.starve < 0 ? steps : static_cast<int>(min(static_cast<long long>(steps), i + static_cast<long long>(A.starve) * kFeedWarps));
         feed.start(A, use, segs, run.f0 + i, smem_u32(ring), bar(kRawFull));
-        for (; i < steps; i += kFeedWarps) {
+        for (; i < fed; i += kFeedWarps) {
             const int st = i % Q::STAGES;
             if (!__all_sync(0xffffffffu, wait(kRawEmpty + st, (i / Q::STAGES & 1) ^ 1))) break;
             feed.issue(A, place, segs, st, gone_of[st]);
         }
         // every copy issued has landed before the CTA may exit: the last steps', as the others' stages have been read.  (Where
-        // a wait gave up: this warp's last two.)
+        // a wait gave up, or the feed stops early: this warp's last two.)
         volatile int never = 0;
         for (int k = i < steps ? i - 2 * kFeedWarps : i - kFeedWarps * Q::STAGES; k < i && k < steps; k += kFeedWarps)
             if (k >= 0 && (i < steps || k >= steps - Q::STAGES)) wait_here(bar(kRawFull + k % Q::STAGES), k / Q::STAGES & 1, &never, A.status, A.wait_ns);
@@ -844,6 +845,7 @@ attn_tree_tc_kernel(const __grid_constant__ AttnArgs A)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (threadIdx.x == 0 && abort_flag) A.info[blockIdx.x] = make_int4(-1, 0, 0, 0);   // some of what would be joined may be missing
     if (warp == kMmaWarp && keep_tmem == 0) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");

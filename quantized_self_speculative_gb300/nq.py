@@ -150,7 +150,8 @@ def lib():
             L.nq_page_attn_tree_workspace_bytes.argtypes = [i32, i32, i32, i32]
             L.nq_page_attn_tree_workspace_bytes.restype = sz
             L.nq_page_attn_tree.argtypes = [PP, i32, PM, vp, i64, i32, vp, vp, i32, AO, TR, vp, vp, sz, vp]
-            for name in ("nq_page_attn_tree", "nq_tree_plan", "spec_accept_tree", "nq_page_keep", "nq_page_append_at", "nq_rms_norm"):
+            L.nq_selftest_page_attn_tree.argtypes = [PP, i32, PM, vp, i64, i32, vp, vp, i32, AO, TR, vp, vp, sz, i32, C.c_uint32, vp]
+            for name in ("nq_page_attn_tree", "nq_selftest_page_attn_tree", "nq_tree_plan", "spec_accept_tree", "nq_page_keep", "nq_page_append_at", "nq_rms_norm"):
                 getattr(L, name).restype = i32
             for name in ("nq_rope_rates", "nq_rope_mscale", "nq_rope", "nq_page_pool_bytes", "nq_page_map_init", "nq_page_reserve",
                          "nq_page_fork", "nq_page_truncate", "nq_page_compact", "nq_page_copy", "nq_page_append",
