@@ -442,16 +442,18 @@ attn_kernel(const __grid_constant__ AttnArgs A)
                             // P is 0 where a query does not see a row, but 0 times NaN or infinity is not:
                             // rows that no query sees (they may hold anything) leave V's fragments.  A
                             // non-finite row that only some queries see is rare; then query row by query row.
-                            // of query row m, of any of them (m < 0)
-                            auto kept = [&](int m, int k) {
+                            // rows of [lo, hi); trees: rows that node m sees, or any of them (m < 0)
+                            auto kept = [&](int m, int lo, int hi, int k) {
                                 const int a = blk0 + 2 * t + 8 * k;
-                                auto keep = [&](int row) {
-                                    if (m < 0) return row >= any_lo && row < any_hi && (!T || tree.live(row));
-                                    if constexpr (T) return tree.used(m) && tree.sees(m, tree.base + tree.depth[m], row, window);
-                                    const int hi = use.s.hi - A.M + m + 1, lo = first_seen(A, hi - 1);
-                                    return row >= lo && row < hi;
-                                };
-                                return (keep(a) ? 0x0000FFFFu : 0u) | (keep(a + 1) ? 0xFFFF0000u : 0u);
+                                if constexpr (T) {
+                                    auto keep = [&](int row) {
+                                        if (m < 0) return row >= any_lo && row < any_hi && tree.live(row);
+                                        return tree.used(m) && tree.sees(m, tree.base + tree.depth[m], row, window);
+                                    };
+                                    return (keep(a) ? 0x0000FFFFu : 0u) | (keep(a + 1) ? 0xFFFF0000u : 0u);
+                                } else {
+                                    return (a >= lo && a < hi ? 0x0000FFFFu : 0u) | (a + 1 >= lo && a + 1 < hi ? 0xFFFF0000u : 0u);
+                                }
                             };
                             bool bad = false;
                             if (m_hi > m_lo) {
@@ -469,9 +471,12 @@ attn_kernel(const __grid_constant__ AttnArgs A)
                                 }
                             }
                             if (__any_sync(0xffffffffu, bad)) {
-                                for (int m = m_lo; m <= m_hi; ++m) product(std::true_type{}, kept(m, 0), kept(m, 1), m);
+                                for (int m = m_lo; m <= m_hi; ++m) {
+                                    const int hi = use.s.hi - A.M + m + 1, lo = first_seen(A, hi - 1);   // without trees: of query m
+                                    product(std::true_type{}, kept(m, lo, hi, 0), kept(m, lo, hi, 1), m);
+                                }
                             } else {
-                                product(std::true_type{}, kept(-1, 0), kept(-1, 1), -1);
+                                product(std::true_type{}, kept(-1, any_lo, any_hi, 0), kept(-1, any_lo, any_hi, 1), -1);
                             }
                         } else {
                             product(std::false_type{}, 0u, 0u, -1);
