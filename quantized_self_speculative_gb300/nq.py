@@ -687,9 +687,13 @@ class Tree:
         if self.batch:
             _check(lib().nq_tree_plan(self.ref, _stream(stream)), "nq_tree_plan")
 
-    def positions(self, base: torch.Tensor) -> torch.Tensor:
-        """Positions int32 [batch][nodes] of the nodes above base int32 [batch] committed rows (a node not used: base's)."""
-        return base[:, None] + self.depth.clamp(min=0)
+    def positions(self, base: torch.Tensor, stream=None) -> torch.Tensor:
+        """Positions int32 [batch][nodes] of the nodes above base int32 [batch] committed rows (a node not used: base's).
+        stream: the plan's, where that was made on one."""
+        if stream is None:
+            return base[:, None] + self.depth.clamp(min=0)
+        with torch.cuda.stream(stream):
+            return base[:, None] + self.depth.clamp(min=0)
 
 
 def accept_tree(tokens: torch.Tensor, logits: torch.Tensor, tree: Tree, width: Optional[int] = None, out_tok=None, out_cnt=None,
