@@ -64,12 +64,14 @@ def run(prompts=(40, 7, 129), rounds=6, branch=3, depth=3, page_size=16, seed=0,
     pool = nq.PagePool(model.L, B * W, page_size, model.H, model.D, nq.KV_NESTED44, group=64)
     pmap = nq.PageMap(B, W, B * W, page_size)
     slots, base, last, tokens = torch.arange(B, dtype=torch.int32, device="cuda"), [], [], []
-    for b, n in enumerate(prompts):              # a prompt is a chain
+    for b, n in enumerate(prompts):              # a prompt is a chain, in pieces of what a tree holds
         ids = torch.randint(0, model.vocab, (1, n), generator=g, device="cuda", dtype=torch.int32)
         if n > 1:
             assert int(pmap.reserve(pool, i32([b]), i32([0]), i32([n - 1])))
-            chain = nq.Tree(i32([list(range(-1, n - 2))]))
-            step(model, ids[:, :n - 1].contiguous(), i32([b]), i32([0]), chain, pool, pmap, False)
+            for at in range(0, n - 1, 1024):
+                part = ids[:, at:min(at + 1024, n - 1)].contiguous()
+                chain = nq.Tree(torch.arange(-1, part.shape[1] - 1, dtype=torch.int32, device="cuda")[None])
+                step(model, part, i32([b]), i32([at]), chain, pool, pmap, False)
         base.append(n - 1)
         last.append(int(ids[0, -1]))
         tokens.append(ids[0].tolist())
