@@ -244,6 +244,12 @@ int cols_of(int vectors, bool tc)
 //                        heads of 128: 20               24       heads of 64: 20                24
 //   16 of 500..4000 rows       47 / 62 | 49 / 66  47 / 63 | 49 / 68   39 / 37 | 41 / 41   39 / 39 | 41 / 41
 //   one of 32768 rows          41 / 64 | 43 / 67  41 / 65 | 43 / 68   35 / 44 | 36 / 46   35 / 45 | 37 / 47
+// on the tensor cores / per warp:
+//                        heads of 128: 9                16       heads of 64: 9                 16
+//   16 of 500..4000 rows       46 / 35 | 48 / 39  46 / 37 | 49 / 41   38 / 29 | 39 / 31   39 / 30 | 39 / 32
+//   one of 32768 rows          41 / 39 | 43 / 43  41 / 39 | 43 / 43   35 / 32 | 35 / 35   35 / 33 | 35 / 35
+//   one of 533, 32 kv heads                              - | 23 / 20
+// (Plain scores.  Capped ones cost the tensor-core kernel more, see there.)
 bool tree_tensor_cores(int vectors, int fmt, int ng) { return vectors > 16 && fmt != kBf16 && ng == 1; }
 // Its tiles hold up to 256 vectors, even shares of what there is.
 int tree_cols(int vectors, bool tc)

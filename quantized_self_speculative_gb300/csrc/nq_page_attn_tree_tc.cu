@@ -36,7 +36,10 @@
 // warp-MMA kernels 233); 4 of 20065..32832 rows, 4 kv heads, 64 nodes x 7 heads: 137 us
 // for 104 GFLOP (55 us at the measured bf16 rate, 40%; the warp-MMA kernels 988).  A step
 // of 256 vectors takes some 2400 cycles: the tensor pipe 1020, the softmax of a group 1600
-// beside some 800 of waits, fences and loop.
+// beside some 800 of waits, fences and loop.  All forms spill (40 to 80 bytes of
+// stores per thread, 92 to 312 of loads; under a cap or bias 216 to 224 and 300 to 348).  A cap
+// doubles the time: 16 sequences of 500..4000 rows, 8 kv heads of 128, 36 / 128 / 256 vectors,
+// plain 51 / 55 / 72 us, capped 101 / 114 / 176, with a bias too 121 / 131 / 222.
 #include <atomic>
 
 #include "nq_page_attn.cuh"
@@ -53,7 +56,10 @@ static_assert(kThreads == 32 * (kFeedWarp + kFeedWarps), "roles");
 constexpr int kRegsLaunch = 96, kRegsSoft = 128, kRegsDecode = 72, kRegsRest = 80;
 static_assert(2 * kRegsSoft + 2 * kRegsDecode + kRegsRest == 5 * kRegsLaunch, "setmaxnreg draws on the launch's registers");
 constexpr int kMinRun = 2;              // steps per CTA
-constexpr int kSegCost = 8;             // what a segment costs beside its steps, in steps
+// What a segment costs beside its steps, in steps.  us with 4 / 6 / 8 / 12, 16 sequences of 500..4000 rows, 8 kv heads:
+// heads of 128, 20 vectors 54 / 50 / 49 / 50, 128 vectors 60 / 55 / 55 / 54, 256 vectors 76 / 72 / 72 / 74; heads of 64,
+// 128 vectors 46 / 43 / 43 / 43, 256 vectors 64 / 66 / 68 / 71 (the one form that 4 suits better).
+constexpr int kSegCost = 8;
 constexpr int kKeys = 64;               // cache rows per step
 constexpr int kTmem = 512;              // columns: S (P) of group g, buffer b at 64 (2 g + b), O of group g at 256 + 128 g
 constexpr uint32_t kColO = 256;
